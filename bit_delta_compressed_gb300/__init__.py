@@ -29,7 +29,7 @@ _PKG = Path(__file__).resolve().parent
 LIB_PATH = _PKG / "libbitdelta.so"
 
 BD_OK, BD_ERR_NULL, BD_ERR_ALIGN, BD_ERR_SHAPE, BD_ERR_DTYPE, BD_ERR_VARIANT, \
-    BD_ERR_WORKSPACE, BD_ERR_CUDA, BD_ERR_TIMEOUT, BD_ERR_UNSUPPORTED = range(10)
+    BD_ERR_WORKSPACE, BD_ERR_CUDA, BD_ERR_TIMEOUT, BD_ERR_UNSUPPORTED, BD_ERR_SLOT = range(11)
 BD_F32, BD_BF16 = 0, 1
 BD_PATH_AUTO, BD_PATH_SIMT, BD_PATH_DECODE_TC, BD_PATH_PREFILL_TC, BD_PATH_DECODE_FOLD, BD_PATH_DECODE_WEFF = range(6)
 MAX_VARIANTS = 64
@@ -40,6 +40,15 @@ PATHS = {"auto": BD_PATH_AUTO, "simt": BD_PATH_SIMT, "decode_tc": BD_PATH_DECODE
 # name -> (restype, argtypes), in the order of include/bitdelta.h
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
 _ST = ctypes.c_int
+_F32 = ctypes.c_float
+
+
+class KVCacheDesc(ctypes.Structure):
+    """``bd_kv_cache``: one layer's key/value cache as the C ABI takes it."""
+    _fields_ = [("k", _P), ("v", _P), ("slots", _I64), ("capacity", _I64), ("kv_heads", _I32), ("head_dim", _I32),
+                ("stride_slot", _I64), ("stride_token", _I64), ("stride_head", _I64)]
+
+
 SIGNATURES = {
     "bitdelta_compress_workspace": (_SZ, [_I64, _I64]),
     "bitdelta_compress": (_ST, [_P, _P, _ST, _I64, _I64, _P, _P, _P, _SZ, _P]),
@@ -55,6 +64,14 @@ SIGNATURES = {
                                       _P, _ST]),
     "bitdelta_linear_rows": (_ST, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _I32, _P, _ST, _P, _SZ,
                                    _P, _ST]),
+    "bitdelta_attn_workspace": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I64]),
+    "bitdelta_attn_decode": (_ST, [_P, _I64, _I64, _I32, _P, _P, _P, _I32, _I32, _F32, _P, _P, _P, _SZ, _P]),
+    "bitdelta_attn_decode_prefix": (_ST, [_P, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _F32,
+                                          _P, _P, _P, _SZ, _P]),
+    "bitdelta_attn_prefill": (_ST, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32,
+                                    _F32, _P, _P, _SZ, _P]),
+    "bitdelta_evict_workspace": (_SZ, [_I64, _I32, _I64]),
+    "bitdelta_cache_evict": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     "bitdelta_device_status": (_ST, [_P, _P]),
     "bitdelta_check_bounded_wait": (_ST, [_P, ctypes.c_uint32, ctypes.c_int, _P]),
     "bitdelta_launch_count": (ctypes.c_uint64, []),
@@ -271,6 +288,160 @@ def linear_grouped(x, w_base, alphas, bits_ptrs, V: int, y, workspace, path: str
                                             workspace.data_ptr(), workspace.numel(),
                                             _stream(stream), PATHS[path]),
           "bitdelta_linear_grouped")
+
+
+# -- attention over a key/value cache -----------------------------------------------
+
+def _cache_desc(k_cache, v_cache):
+    """``bd_kv_cache`` of two [slots, capacity, kv_heads, head_dim] bf16 CUDA
+    tensors; any strides the C ABI takes (a transposed view is one layout)."""
+    torch = _torch()
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k and v must be 4-D [slots, capacity, kv_heads, head_dim] of one shape and strides")
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+        raise TypeError("the cache must be bfloat16")
+    if not k_cache.is_cuda or not v_cache.is_cuda or k_cache.stride(3) != 1:
+        raise ValueError("the cache must be CUDA tensors with contiguous head_dim")
+    S, C, H, D = k_cache.shape
+    # the stride of a dimension of one entry is never used, and torch leaves it open
+    strides = [st if n > 1 else D for st, n in zip(k_cache.stride()[:3], (S, C, H))]
+    return KVCacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), S, C, H, D, *strides)
+
+
+def _int32(name, t, shape):
+    torch = _torch()
+    if t is None:
+        return None
+    _need_cuda(t)
+    if t.dtype != torch.int32 or tuple(t.shape) != shape:
+        raise ValueError("%s must be an int32 tensor of shape %s" % (name, shape))
+    return t.data_ptr()
+
+
+def _attn_args(q, k_cache, out):
+    torch = _torch()
+    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or q.dtype != torch.bfloat16 or not q.is_cuda:
+        raise ValueError("q must be a bf16 CUDA tensor [rows, q_heads, head_dim]")
+    if q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+        raise ValueError("the heads of a row of q must be contiguous")
+    stride = q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _need_cuda(out)
+    if out.shape != q.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bf16 and of q's shape")
+    return stride, out
+
+
+def _weights_ptr(weights, k_cache):
+    torch = _torch()
+    if weights is None:
+        return None
+    _need_cuda(weights)
+    S, C, H, _ = k_cache.shape
+    if weights.dtype != torch.float32 or tuple(weights.shape) != (S, H, C):
+        raise ValueError("weights must be float32 [slots, kv_heads, capacity]")
+    return weights.data_ptr()
+
+
+def _prefix_args(prefix_ids, prefix_slots, prefix_lens, B):
+    if prefix_ids is None and prefix_slots is None and prefix_lens is None:
+        return None, None, None, 0
+    if prefix_ids is None or prefix_slots is None or prefix_lens is None:
+        raise ValueError("prefix_ids, prefix_slots and prefix_lens go together")
+    P = prefix_slots.numel()
+    return (_int32("prefix_ids", prefix_ids, (B,)), _int32("prefix_slots", prefix_slots, (P,)),
+            _int32("prefix_lens", prefix_lens, (P,)), P)
+
+
+def attn_workspace(tokens: int, batch: int, q_heads: int, kv_heads: int, head_dim: int, weigh_len: int = 0,
+                   device=None):
+    """Zeroed workspace for attention calls of at most ``tokens`` query rows and
+    ``batch`` requests; ``weigh_len``: the cache's capacity if decode
+    accumulates weights."""
+    torch = _torch()
+    n = int(get_lib().bitdelta_attn_workspace(tokens, batch, q_heads, kv_heads, head_dim, weigh_len))
+    if n == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "bitdelta_attn_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def attn_decode(q, k_cache, v_cache, lens, workspace, slots=None, window: int = 0, sinks: int = 0, scale=None,
+                weights=None, out=None, stream=None):
+    """Attention of one new token a request: q [B, q_heads, head_dim] bf16 on the
+    cache [slots, capacity, kv_heads, head_dim] (see ``bitdelta_attn_decode``).
+    ``weights`` (f32 [slots, kv_heads, capacity]) is added to in place;
+    ``scale`` defaults to head_dim ** -0.5.  Returns out [B, q_heads, head_dim]."""
+    return attn_decode_prefix(q, k_cache, v_cache, lens, None, None, None, workspace, slots=slots, window=window,
+                              sinks=sinks, scale=scale, weights=weights, out=out, stream=stream)
+
+
+def attn_decode_prefix(q, k_cache, v_cache, lens, prefix_ids, prefix_slots, prefix_lens, workspace, slots=None,
+                       window: int = 0, sinks: int = 0, scale=None, weights=None, out=None, stream=None):
+    """``attn_decode`` for requests that share prefixes: request b's keys follow
+    the ``prefix_lens[p]`` keys in slot ``prefix_slots[p]``, p = ``prefix_ids[b]``
+    (-1: none), which are read once for all requests that name them (see
+    ``bitdelta_attn_decode_prefix``)."""
+    desc = _cache_desc(k_cache, v_cache)
+    stride, out = _attn_args(q, k_cache, out)
+    B, H, D = q.shape
+    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
+    args = [q.data_ptr(), stride, B, H, ctypes.byref(desc), _int32("slots", slots, (B,)), _int32("lens", lens, (B,))]
+    rest = [window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, k_cache), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(stream)]
+    if P == 0:
+        check(get_lib().bitdelta_attn_decode(*args, *rest), "bitdelta_attn_decode")
+    else:
+        check(get_lib().bitdelta_attn_decode_prefix(*args, ids, pslots, plens, P, *rest),
+              "bitdelta_attn_decode_prefix")
+    return out
+
+
+def attn_prefill(q, k_cache, v_cache, cu_q, lens, workspace, slots=None, window: int = 0, sinks: int = 0, scale=None,
+                 prefix_ids=None, prefix_slots=None, prefix_lens=None, out=None, stream=None):
+    """Causal attention of several new tokens a request: rows ``cu_q[b]`` to
+    ``cu_q[b+1]`` of q [T, q_heads, head_dim] are request b's newest tokens,
+    whose keys are the last of its ``lens[b]`` keys in the cache (see
+    ``bitdelta_attn_prefill``).  Returns out [T, q_heads, head_dim]."""
+    desc = _cache_desc(k_cache, v_cache)
+    stride, out = _attn_args(q, k_cache, out)
+    T, H, D = q.shape
+    B = lens.numel()
+    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
+    check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, ctypes.byref(desc),
+                                          _int32("slots", slots, (B,)), _int32("cu_q", cu_q, (B + 1,)),
+                                          _int32("lens", lens, (B,)), ids, pslots, plens, P, window, sinks,
+                                          D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                          workspace.data_ptr(), workspace.numel(), _stream(stream)),
+          "bitdelta_attn_prefill")
+    return out
+
+
+def evict_workspace(n: int, kv_heads: int, capacity: int, device=None):
+    torch = _torch()
+    b = int(get_lib().bitdelta_evict_workspace(n, kv_heads, capacity))
+    if b == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "bitdelta_evict_workspace")
+    return torch.zeros(b, dtype=torch.uint8, device=device)
+
+
+def cache_evict(k_cache, v_cache, weights, lens, src, dst, budget: int, workspace, sinks: int = 0, recent: int = 0,
+                kept=None, stream=None) -> None:
+    """Move requests from slots ``src`` to slots ``dst``, keeping the first
+    ``sinks``, the last ``recent`` and the heaviest other keys, ``budget`` in
+    all, of every head (see ``bitdelta_cache_evict``).  ``lens`` holds a length
+    for every slot.  ``kept`` (int32 [n, kv_heads, budget]) receives the kept
+    keys' old places."""
+    desc = _cache_desc(k_cache, v_cache)
+    S, _, H, _ = k_cache.shape
+    n = src.numel()
+    if weights is None:
+        raise ValueError("weights are needed")
+    check(get_lib().bitdelta_cache_evict(ctypes.byref(desc), _weights_ptr(weights, k_cache),
+                                         _int32("lens", lens, (S,)), _int32("src", src, (n,)),
+                                         _int32("dst", dst, (n,)), n, budget, sinks, recent,
+                                         _int32("kept", kept, (n, H, budget)), workspace.data_ptr(),
+                                         workspace.numel(), _stream(stream)), "bitdelta_cache_evict")
 
 
 def device_status(workspace, stream=None) -> int:

@@ -50,6 +50,7 @@ extern "C" const char* bitdelta_status_string(bd_status s) {
         case BD_ERR_CUDA: return "CUDA runtime error";
         case BD_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
         case BD_ERR_UNSUPPORTED: return "kernel path does not support this shape";
+        case BD_ERR_SLOT: return "cache slot, length, prefix id or token offset out of range";
     }
     return "unknown status";
 }

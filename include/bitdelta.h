@@ -64,7 +64,8 @@ typedef enum {
     BD_ERR_WORKSPACE = 6,   /* workspace NULL or smaller than the *_workspace() size */
     BD_ERR_CUDA = 7,        /* a CUDA runtime call or launch failed */
     BD_ERR_TIMEOUT = 8,     /* device: a bounded wait inside a kernel ran out */
-    BD_ERR_UNSUPPORTED = 9  /* the requested kernel path cannot run this shape */
+    BD_ERR_UNSUPPORTED = 9, /* the requested kernel path cannot run this shape */
+    BD_ERR_SLOT = 10        /* device: a cache slot, length, prefix id or token offset out of range */
 } bd_status;
 
 typedef enum { BD_F32 = 0, BD_BF16 = 1 } bd_dtype;
@@ -255,11 +256,121 @@ bd_status bitdelta_linear_rows(const void *x, const int32_t *variant_ids,
                                bd_path path);
 
 /* ------------------------------------------------------------------ */
+/* Attention over a key/value cache: the part of a decoder layer between */
+/* its v and o projections.  The page leaves the attention arithmetic to */
+/* the standard forward pass ("Serving architecture": the model's forward */
+/* runs with the rebuilt weights); these entry points are that part.      */
+/* ------------------------------------------------------------------ */
+
+/* One layer's cache, described on the HOST and read during the call only.
+ *   k, v  : device, bf16 [slots, capacity, kv_heads, head_dim] with the given
+ *           strides (in elements, shared by k and v); the head_dim values of a
+ *           key are contiguous.  Pointers 16-byte aligned, strides multiples of
+ *           8 and positive; distinct (slot, token, head) rows do not overlap.
+ *   slots, capacity, kv_heads >= 1; head_dim 64 or 128; capacity <= 2^24,
+ *   slots <= 2^24.
+ * A request owns one slot: its key j lies at token j of the slot.  What lies
+ * behind a slot's length is never used, whatever it holds. */
+typedef struct {
+    void *k, *v;
+    int64_t slots, capacity;
+    int32_t kv_heads, head_dim;
+    int64_t stride_slot, stride_token, stride_head;
+} bd_kv_cache;
+
+/* Shared by the attention entry points.
+ *   Heads.  q_heads is a multiple of kv_heads (at most 128 times it); query
+ *     heads h * q_heads / kv_heads ... read key/value head h.
+ *   Positions.  With P keys of a shared prefix (0 without one) prefix key j
+ *     stands at position j and own key j at position P + j.
+ *   Mask.  A query at position t sees position p when p <= t and (window == 0
+ *     or p > t - window or p < sinks): window >= 0 (0: everything), sinks >= 0.
+ *   Result.  out = sum_j p_j v_j, p = softmax of scale * q.k over the visible
+ *     keys, statistics and sums in f32, the result rounded once to bf16.  A row
+ *     that sees nothing, or whose visible scores are all -inf, gives zeros.
+ *     Values at positions that no query of the request sees never reach a result,
+ *     NaN and infinities included.
+ *   Requests.  slots: device int32 [B], the slot of each request (NULL: request
+ *     b owns slot b).  lens: device int32 [B], its own keys in the cache,
+ *     0 <= lens[b] <= capacity.  A request with a slot, length or prefix id
+ *     out of range gets zero rows and sets BD_ERR_SLOT in the status word.
+ *   Prefixes.  prefix_slots, prefix_lens: device int32 [P], the slot that holds
+ *     each prefix and its length (<= capacity); prefix_ids: device int32 [B],
+ *     each in [-1, P), -1 for none.  All three NULL (P == 0): no prefixes.
+ *   q         : device bf16, row t starts at q + t * q_stride elements and holds
+ *               q_heads * head_dim contiguous values; q_stride a multiple of 8.
+ *   out       : device bf16 [rows, q_heads, head_dim], contiguous.
+ *   workspace : device, zero-filled once before its first use, ws_bytes >=
+ *               bitdelta_attn_workspace(...).
+ * Every call is deterministic: equal inputs give equal bits. */
+
+/* Bytes of device workspace for calls of at most `tokens` query rows and
+ * `batch` requests; `weigh_len`: the cache's capacity if decode is to
+ * accumulate weights, else 0.  Returns 0 for invalid sizes. */
+size_t bitdelta_attn_workspace(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads,
+                               int32_t head_dim, int64_t weigh_len);
+
+/* One new token for each of B requests: query b stands at the request's last
+ * position (its key is already in the cache, lens[b] counts it).
+ *   weights : NULL, or device f32 [slots, kv_heads, capacity]: to the entry of
+ *             every visible own key the softmax weights that the heads of its
+ *             group gave it are added.  Two requests of one call may then not
+ *             share a slot (their additions would come in either order). */
+bd_status bitdelta_attn_decode(const void *q, int64_t q_stride, int64_t B, int32_t q_heads,
+                               const bd_kv_cache *cache, const int32_t *slots, const int32_t *lens,
+                               int32_t window, int32_t sinks, float scale, float *weights, void *out,
+                               void *workspace, size_t ws_bytes, void *stream);
+
+/* The same for requests that share prefixes: a prefix's keys are read once
+ * for all requests that name it.  (Requests of one variant share its prompt;
+ * the keys of different variants differ.)  The weights count own keys only. */
+bd_status bitdelta_attn_decode_prefix(const void *q, int64_t q_stride, int64_t B, int32_t q_heads,
+                                      const bd_kv_cache *cache, const int32_t *slots, const int32_t *lens,
+                                      const int32_t *prefix_ids, const int32_t *prefix_slots,
+                                      const int32_t *prefix_lens, int32_t P, int32_t window,
+                                      int32_t sinks, float scale, float *weights, void *out,
+                                      void *workspace, size_t ws_bytes, void *stream);
+
+/* Several new tokens a request.  Rows cu_q[b] .. cu_q[b+1] - 1 of q (device
+ * int32 [B + 1], ascending from 0 to T) are request b's newest tokens, the last
+ * of them at its last position; their keys are already in the cache.  With a
+ * prefix, the queries see it as decode does.  Rows outside every request's
+ * range are left as they are. */
+bd_status bitdelta_attn_prefill(const void *q, int64_t q_stride, int64_t T, int64_t B, int32_t q_heads,
+                                const bd_kv_cache *cache, const int32_t *slots, const int32_t *cu_q,
+                                const int32_t *lens, const int32_t *prefix_ids,
+                                const int32_t *prefix_slots, const int32_t *prefix_lens, int32_t P,
+                                int32_t window, int32_t sinks, float scale, void *out, void *workspace,
+                                size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace of bitdelta_cache_evict.  0 for invalid sizes. */
+size_t bitdelta_evict_workspace(int64_t n, int32_t kv_heads, int64_t capacity);
+
+/* Evict by accumulated weight: n requests move from slot src[i] to slot dst[i],
+ * keeping at most `budget` keys each, every key/value head its own: the first
+ * `sinks`, the last `recent`, and of the others the heaviest by `weights`
+ * (equal weights: the earlier key; a NaN counts as the heaviest).  The kept
+ * keys stay in order.
+ *   weights  : device f32 [slots, kv_heads, capacity].
+ *   lens     : device int32 [slots] (here a length for every SLOT): lens[dst]
+ *              becomes min(lens[src], budget).
+ *   src, dst : device int32 [n].  No slot may be in both, nor twice in dst: such a
+ *              pair, or one out of range, is left undone and sets BD_ERR_SLOT.
+ *   budget   : 1 <= budget <= capacity, sinks + recent <= budget.
+ *   kept     : NULL, or device int32 [n, kv_heads, budget]: the kept keys' old
+ *              places, -1 behind the last.
+ * K, V and weights of the kept keys are copied; src is left as it is. */
+bd_status bitdelta_cache_evict(const bd_kv_cache *cache, float *weights, int32_t *lens,
+                               const int32_t *src, const int32_t *dst, int64_t n, int64_t budget,
+                               int64_t sinks, int64_t recent, int32_t *kept, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Status                                                               */
 /* ------------------------------------------------------------------ */
 
 /* Synchronise `stream`, read the status word at the start of `workspace`
- * (any workspace given to bitdelta_compress or bitdelta_linear), clear it,
+ * (any workspace given to an entry point of this library), clear it,
  * and return the lowest-numbered error it holds (BD_OK if none). */
 bd_status bitdelta_device_status(void *workspace, void *stream);
 
