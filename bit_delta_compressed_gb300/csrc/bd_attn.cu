@@ -2,7 +2,7 @@
 // of the arguments, workspace) and the kernels' launches.
 #include <math.h>
 
-#include "bd_attn.cuh"
+#include "bd_attn_math.cuh"
 
 namespace bd {
 namespace attn {
@@ -10,7 +10,8 @@ namespace attn {
 bool bad_cache(const bd_kv_cache* c, bd_status* st) {
     if (!c || !c->k || !c->v) { *st = BD_ERR_NULL; return true; }
     if (c->slots < 1 || c->slots > kMaxTokens || c->capacity < 1 || c->capacity > kMaxTokens || c->kv_heads < 1 ||
-        (c->head_dim != 64 && c->head_dim != 128) || c->stride_slot < 1 || c->stride_token < 1 || c->stride_head < 1) {
+        (c->head_dim != 64 && c->head_dim != 128) || c->stride_slot < 1 || c->stride_token < 1 || c->stride_head < 1 ||
+        c->stride_slot > kMaxStride || c->stride_token > kMaxStride || c->stride_head > kMaxStride) {
         *st = BD_ERR_SHAPE;
         return true;
     }
@@ -23,63 +24,54 @@ bool bad_cache(const bd_kv_cache* c, bd_status* st) {
 
 namespace {
 
-// One warp a (row, query head), the softmax in one pass over the keys with a
-// running maximum and sum: lane i holds head_dim / 32 neighbouring values.
-template <int D>
-__global__ void __launch_bounds__(256) rows_kernel(const Args a) {
-    constexpr int E = D / 32;
-    const int64_t id = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-    const int lane = threadIdx.x % 32;
-    const int b = blockIdx.y;
-    const Request rq = read_request(a, b);
-    const int64_t i = id / a.Hq;
-    const int h = id % a.Hq;
-    if (i >= rq.rows) return;
-    const int64_t row = rq.row0 + i;
-    float q[E], o[E] = {};
-    for (int e = 0; e < E; ++e)
-        q[e] = __bfloat162float(a.q[row * a.q_stride + (int64_t)h * D + lane * E + e]) * a.scale_log2;
-    const int end = rq.plen + rq.len;
-    const int t = end - rq.rows + (int)i;
-    const int lo = window_lo(a, t);
-    float m = -INFINITY, l = 0.f;
-    for (int p = 0; p <= t && p < end; ++p) {
-        if (p >= a.sinks && p < lo) continue;
-        const bool own = p >= rq.plen;
-        const int64_t at = (int64_t)(own ? rq.slot : rq.pslot) * a.ss + (int64_t)(own ? p - rq.plen : p) * a.st +
-                           (int64_t)(h / a.G) * a.sh + lane * E;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(a.k[at + e]), s);
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float mn = fmaxf(m, s);
-        if (mn == -INFINITY) continue;
-        const float f = exp2f(m - mn), w = exp2f(s - mn);
-        l = l * f + w;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * __bfloat162float(a.v[at + e]);
-        m = mn;
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    for (int e = 0; e < E; ++e)
-        a.out[(row * a.Hq + h) * D + lane * E + e] = __float2bfloat16(o[e] * inv);
-    if (a.weights) {
-        const int kv = h / a.G;
-        const int first = 0;
-        for (int p = max(first, rq.plen); p <= t && p < end; ++p) {
-            if (p >= a.sinks && p < lo) continue;
-            const int64_t at = (int64_t)rq.slot * a.ss + (int64_t)(p - rq.plen) * a.st + (int64_t)kv * a.sh + lane * E;
-            float s = 0.f;
-            for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(a.k[at + e]), s);
-            for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            if (lane == 0)
-                atomicAdd(a.weights + ((int64_t)rq.slot * a.Hk + kv) * a.capacity + p - rq.plen, exp2f(s - m) * inv);
-        }
-    }
-}
-
 bool sizes_ok(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     return tokens >= 0 && tokens <= (int64_t)1 << 30 && batch >= 0 && batch <= 65535 && kv_heads >= 1 &&
            q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= kMaxGroup && q_heads <= 65535 &&
            (head_dim == 64 || head_dim == 128);
+}
+
+// The workspace of one call: the header and the tickets lie where every call
+// expects them, the rest is scratch.
+struct Workspace {
+    DecodeBuffers decode;
+    TilePlan plan;
+    size_t total;
+};
+
+Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                 int64_t weigh_len) {
+    Workspace w{};
+    char* p = static_cast<char*>(base);
+    size_t at = kHeaderBytes;
+    auto take = [&](size_t bytes) {
+        char* r = p ? p + at : nullptr;
+        at += round_up(bytes, kAlign);
+        return r;
+    };
+    w.decode.tickets = reinterpret_cast<int*>(take(kMaxBlocks * sizeof(int)));
+    w.decode.parts = reinterpret_cast<float*>(take(decode_parts_bytes(head_dim)));
+    if (weigh_len > 0) {
+        w.decode.score_stride = (int64_t)round_up((size_t)weigh_len, 4);
+        w.decode.lse = reinterpret_cast<float*>(take((size_t)batch * q_heads * sizeof(float)));
+        w.decode.scores = reinterpret_cast<float*>(take((size_t)batch * q_heads * w.decode.score_stride * sizeof(float)));
+    }
+    const int64_t tiles = most_tiles(tokens, batch, q_heads / kv_heads), units = tiles * kv_heads;
+    w.plan.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
+    w.plan.tiles = reinterpret_cast<RowTile*>(take((size_t)tiles * sizeof(RowTile)));
+    w.plan.order = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
+    w.plan.req_unit = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
+    w.plan.req_row = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
+    w.plan.unit_row = reinterpret_cast<int64_t*>(take((size_t)units * sizeof(int64_t)));
+    w.plan.unit_segs = reinterpret_cast<int2*>(take((size_t)units * sizeof(int2)));
+    // parts: every row once, and one unit's rows more for each thread block; a prefill
+    // of so many rows that it is not split leaves none
+    int64_t rows = split_below() * kPartRows;
+    rows = rows < batch * q_heads ? batch * q_heads : rows;
+    rows = (rows < tokens * q_heads ? rows : tokens * q_heads) + (int64_t)tile_blocks() * kPartRows;
+    w.plan.o = reinterpret_cast<float*>(take((size_t)rows * head_dim * sizeof(float)));
+    w.plan.ml = reinterpret_cast<float2*>(take((size_t)rows * sizeof(float2)));
+    w.total = at;
+    return w;
 }
 
 bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32_t q_heads, const bd_kv_cache* c,
@@ -88,7 +80,7 @@ bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32
                     float scale, float* weights, void* out, void* workspace, size_t ws_bytes, cudaStream_t stream) {
     bd_status st;
     if (bad_cache(c, &st)) return st;
-    if (!sizes_ok(T, B, q_heads, c->kv_heads, c->head_dim) || window < 0 || sinks < 0 || P < 0 || !isfinite(scale) ||
+    if (!sizes_ok(T, B, q_heads, c->kv_heads, c->head_dim) || window < 0 || sinks < 0 || P < 0 || P > kMaxPrefixes || !isfinite(scale) ||
         q_stride < (int64_t)q_heads * c->head_dim)
         return BD_ERR_SHAPE;
     if (T == 0 || B == 0) return BD_OK;
@@ -130,13 +122,17 @@ bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32
     a.scale_log2 = scale * 1.4426950408889634f;
     a.weights = weights;
     a.status = static_cast<unsigned*>(workspace);
-    const int64_t most = cu_q ? T : 1;
-    const dim3 grid((unsigned)((most * q_heads + 7) / 8), (unsigned)B);
-    if (c->head_dim == 128)
-        rows_kernel<128><<<grid, 256, 0, stream>>>(a);
-    else
-        rows_kernel<64><<<grid, 256, 0, stream>>>(a);
-    return launch_status();
+    const Workspace w = layout(workspace, T, B, q_heads, c->kv_heads, c->head_dim, weights ? c->capacity : 0);
+    if (cu_q) return launch_tiles(a, c->head_dim, w.plan, stream);
+    PrefixParts parts{};
+    if (P > 0) {
+        const bd_status done = launch_tiles(a, c->head_dim, w.plan, stream);
+        if (done != BD_OK) return done;
+        parts = {w.plan.o, w.plan.ml, w.plan.req_unit, w.plan.req_row, w.plan.unit_row, w.plan.unit_segs};
+    }
+    DecodeBuffers buf = w.decode;
+    buf.least_tiles = 32;
+    return launch_decode(a, c->head_dim, buf, parts, stream);
 }
 
 }  // namespace
@@ -148,7 +144,7 @@ extern "C" size_t bitdelta_attn_workspace(int64_t tokens, int64_t batch, int32_t
     if (!bd::attn::sizes_ok(tokens, batch, q_heads, kv_heads, head_dim) || weigh_len < 0 ||
         weigh_len > bd::attn::kMaxTokens)
         return 0;
-    return bd::kHeaderBytes;
+    return bd::attn::layout(nullptr, tokens, batch, q_heads, kv_heads, head_dim, weigh_len).total;
 }
 
 extern "C" bd_status bitdelta_attn_decode(const void* q, int64_t q_stride, int64_t B, int32_t q_heads,

@@ -10,6 +10,8 @@ namespace attn {
 
 constexpr int kMaxGroup = 128;          // query heads of one key/value head
 constexpr int64_t kMaxTokens = 1 << 24; // a slot's capacity: positions stay below 2^25
+constexpr int64_t kMaxStride = (int64_t)1 << 38;   // elements: a tensor map's strides end at 2^40 bytes
+constexpr int kMaxPrefixes = BITDELTA_MAX_PREFIXES;
 
 struct Args {
     const __nv_bfloat16* q;

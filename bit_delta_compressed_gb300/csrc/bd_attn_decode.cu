@@ -1,0 +1,560 @@
+// bd_attn_decode.cu -- attention of one query row a request on its own keys.
+//
+// o = sum_j p_j v_j with p the softmax of q.k_j: 4 flops a byte of cache for
+// each head of a group, so the cache's bytes bound it.  One launch of one block
+// a SM; the visible keys of all (request, key/value head) units, in tiles of 16,
+// form one line that is cut into equal parts for the blocks and again for their
+// warps: ragged lengths, one long request and thousands of short ones all keep
+// every SM reading.  A warp works alone: it streams its tiles through a ring of
+// its own in shared memory (cp.async, 16 bytes a lane; keys that are not visible
+// are never read, their rows are filled with zeros), multiplies with mma.sync
+// (m16n8k16: a group's heads are the rows) and keeps a running maximum, sum and
+// output in registers.  tcgen05 has nothing to give here: its tiles are 128 rows
+// high where a group has 1 to 16, and the tensor work is a tenth of the time.
+// Units that several warps or blocks share are joined in their order from shared
+// memory and, across blocks, from the workspace by the block that finishes last,
+// so the result does not depend on timing.
+#include <math.h>
+
+#include "bd_attn.cuh"
+#include "bd_attn_math.cuh"
+#include "bd_tc_common.cuh"
+
+namespace bd {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;                 // keys of a tile
+constexpr int kRuns = 128;                // runs of requests that a block looks its place up in
+
+// R: rows of a unit (8 or 16 query heads).  A probability is multiplied as two
+// bf16 terms, so that it keeps 16 significant bits and the result is rounded once,
+// at its end.  With up to 8 heads the second term costs nothing (it takes rows 8 to
+// 15 of the product), with more a second product, and the bytes still bound it.
+template <int D, int R>
+struct Shape {
+    static constexpr int kStage = 2 * kTile * D * 2;                        // K and V of a tile
+    static constexpr int kStages = (R == 8 ? 3 : 2) * (128 / D);
+    static constexpr int kRing = kStage * kStages;                          // of one warp
+    static constexpr int kPart = R * D * 4 + R * 8;                         // an open unit: O, then (m, l)
+    static constexpr int kSmem = kWarps * (kRing + kPart);
+    static_assert(kRing >= kPart, "a warp's last open unit reuses its ring");
+};
+
+// Where the visible own keys of a request lie: the first `head` and, behind a
+// gap, the window.  Key x of the n visible ones is key x + (x >= head ? gap : 0).
+struct Keys {
+    int n, head, gap;
+};
+
+__device__ __forceinline__ Keys visible_keys(const Args& a, const Request& r) {
+    Keys k;
+    const int lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);
+    const int sinks = min(max(a.sinks - r.plen, 0), r.len);
+    k.gap = max(lo - sinks, 0);
+    k.head = k.gap ? sinks : r.len;
+    k.n = r.len - k.gap;
+    return k;
+}
+
+__device__ __forceinline__ int tiles_of(const Args& a, const Request& r) {
+    return max(1, (visible_keys(a, r).n + kTile - 1) / kTile);
+}
+
+// One position on the line of tiles and the geometry of its unit.
+struct Cursor {
+    int b, u, tile, tiles;
+    Request r;
+    Keys k;
+};
+
+__device__ __forceinline__ void load_request(const Args& a, Cursor& c) {
+    c.r = read_request(a, c.b);
+    c.k = visible_keys(a, c.r);
+    c.tiles = max(1, (c.k.n + kTile - 1) / kTile);
+}
+
+__device__ __forceinline__ void advance(const Args& a, Cursor& c, int units) {
+    if (++c.tile < c.tiles) return;
+    c.tile = 0;
+    if (++c.u < units) return;
+    c.u = 0;
+    if (++c.b < a.B) load_request(a, c);
+}
+
+struct Record {                            // an open unit of a warp
+    int valid, b, u, tile, tiles, open_end;
+    int64_t at;                            // its first tile's place on the line
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int chunks, uint32_t stage, int lane) {
+    constexpr int L = D / 8;               // lanes of a row
+    const int h = c.u / chunks;
+    const int64_t base = (int64_t)c.r.slot * a.ss + (int64_t)h * a.sh + (lane % L) * 8;
+#pragma unroll
+    for (int i = 0; i < kTile * L / 32; ++i) {
+        const int row = i * (32 / L) + lane / L;
+        const int x = c.tile * kTile + row;
+        const bool in = x < c.k.n;
+        const int64_t off = in ? base + (int64_t)(x + (x >= c.k.head ? c.k.gap : 0)) * a.st : 0;
+        const uint32_t to = stage + row * (D * 2) + (((lane % L) ^ (row & 7)) << 4);
+        cp_async16(to, a.k + off, in);
+        cp_async16(to + kTile * D * 2, a.v + off, in);
+    }
+}
+
+// log2 of a row's denominator; a row without keys weighs nothing.
+__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? m + log2f(l) : (l == 0.f ? INFINITY : l); }
+
+// Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
+// gives a part's base, O [R][D] then (m, l) [R].
+template <int D, int R, typename F>
+__device__ __forceinline__ void join(int row, int col, int count, F part, float& m, float& l, float4& o) {
+    float top = m;
+    for (int s = 0; s < count; ++s) top = fmaxf(top, part(s)[R * D + 2 * row]);
+    const float use = top == -INFINITY ? 0.f : top;
+    float f = exp2_approx(m - use);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 4
+    for (int s = 0; s < count; ++s) {
+        const float* p = part(s);
+        f = exp2_approx(p[R * D + 2 * row] - use);
+        l += f * p[R * D + 2 * row + 1];
+        const float4 v = *reinterpret_cast<const float4*>(p + row * D + col);
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+    }
+    m = top;
+}
+
+// Adds what the shared prefix gave row `row` of a group: n pairs of neighbouring
+// values, the pairs `step` apart.
+template <int N>
+__device__ __forceinline__ void join_prefix(const PrefixParts& pp, int D, int b, int hk, int row, int col, float& m,
+                                            float& l, float* o, int o_step, int step) {
+    const int unit0 = pp.req_unit[b];
+    if (unit0 < 0) return;
+    const int2 seg = pp.unit_segs[unit0 + hk];
+    const int64_t r0 = pp.unit_row[unit0 + hk] + pp.req_row[b] + row;
+#pragma unroll 2
+    for (int s = 0; s < seg.y; ++s) {
+        const int64_t r = r0 + (int64_t)(seg.x + s) * kPartRows;
+        const float2 ml = pp.ml[r];
+        const float top = fmaxf(m, ml.x);
+        const float use = top == -INFINITY ? 0.f : top;
+        const float f = exp2_approx(m - use), g = exp2_approx(ml.x - use);
+        l = l * f + ml.y * g;
+        const float* from = pp.o + r * D + col;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float2 v = *reinterpret_cast<const float2*>(from + i * step);
+            o[i * o_step] = o[i * o_step] * f + g * v.x;
+            o[i * o_step + 1] = o[i * o_step + 1] * f + g * v.y;
+        }
+        m = top;
+    }
+}
+
+// A row's joined sums become its result: row r of the group, four values.
+template <int D>
+__device__ __forceinline__ void finish(const Args& a, const DecodeBuffers& buf, const PrefixParts& pp, int b, int hk,
+                                       int r, int col, float m, float l, float4 v) {
+    float o[4] = {v.x, v.y, v.z, v.w};
+    if (pp.o) join_prefix<2>(pp, D, b, hk, r, col, m, l, o, 2, 2);
+    const float inv = inverse(l);
+    const int64_t at = (int64_t)b * a.Hq + hk * a.G + r;
+    *reinterpret_cast<uint2*>(a.out + at * D + col) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    if (a.weights && col == 0) buf.lse[at] = log_sum(m, l);
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf, const PrefixParts pp) {
+    using S = Shape<D, R>;
+    constexpr int NT = D / 8;              // 8-wide column tiles of the output
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sums[kRuns + 1];
+    __shared__ Record records[2 * kWarps];
+    __shared__ int last_block;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
+    const int units = a.Hk * chunks;
+
+    // the line: tiles of the requests before each of kRuns runs of requests
+    const int run = (a.B + kRuns - 1) / kRuns;
+    {
+        int64_t mine = 0;
+        for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) mine += tiles_of(a, read_request(a, b));
+        int64_t incl = mine;
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += o;
+        }
+        if (lane == 31 && tid < kRuns) sums[warp] = incl;
+        __syncthreads();
+        int64_t before = 0;
+        for (int w = 0; w < warp && tid < kRuns; ++w) before += sums[w];
+        __syncthreads();
+        if (tid < kRuns) sums[tid + 1] = before + incl;
+        if (tid == 0) sums[0] = 0;
+        if (tid < 2 * kWarps) records[tid].valid = 0;
+        __syncthreads();
+    }
+    const int64_t total = sums[kRuns] * units;
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    per = per < buf.least_tiles ? buf.least_tiles : per;
+    const int64_t block_lo = min(total, per * blockIdx.x), block_hi = min(total, block_lo + per);
+    const int64_t lo = block_lo + (block_hi - block_lo) * warp / kWarps;
+    const int64_t hi = block_lo + (block_hi - block_lo) * (warp + 1) / kWarps;
+
+    const uint32_t ring = smem_addr(smem) + warp * S::kRing;
+    float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
+    float* const head_part = reinterpret_cast<float*>(smem + kWarps * S::kRing + warp * S::kPart);
+
+    if (lo < hi) {
+        Cursor c;
+        {
+            int s = 0;                     // the run that holds place lo
+            for (int step = kRuns / 2; step; step /= 2)
+                if (sums[s + step] * units <= lo) s += step;
+            int64_t rest = lo - sums[s] * units;
+            c.b = s * run;
+            load_request(a, c);
+            while (rest >= (int64_t)c.tiles * units && c.b + 1 < a.B) {
+                rest -= (int64_t)c.tiles * units;
+                ++c.b;
+                load_request(a, c);
+            }
+            c.u = (int)(rest / c.tiles);
+            c.tile = (int)(rest % c.tiles);
+        }
+        Cursor ahead = c;
+        int64_t ahead_at = lo;
+        int put = 0;
+        auto prefetch = [&]() {
+            if (ahead_at < hi) {
+                load_tile<D>(a, ahead, chunks, ring + put * S::kStage, lane);
+                if (++ahead_at < hi) advance(a, ahead, units);
+            }
+            cp_async_commit();
+            if (++put == S::kStages) put = 0;
+        };
+#pragma unroll 1
+        for (int i = 0; i < S::kStages - 1; ++i) prefetch();
+
+        int got = 0;
+        int64_t at = lo, seg_at = lo;
+        int seg_tile = c.tile;             // the unit's first tile in this warp
+        uint32_t qf[D / 16][R == 8 ? 2 : 4];
+        float o[NT][4], m[R / 8], l[R / 8];
+        const int row = lane / 4, col = 2 * (lane % 4);
+        bool fresh = true;
+        while (at < hi) {
+            if (fresh) {
+                fresh = false;
+                const int hk = c.u / chunks, head0 = hk * a.G + (c.u % chunks) * R;
+                const int rows = min(R, a.G - (c.u % chunks) * R);
+                const __nv_bfloat16* qp = a.q + (int64_t)c.b * a.q_stride + (int64_t)head0 * D;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int j = 0; j < (R == 8 ? 2 : 4); ++j) {
+                        const int r = R == 8 ? row : row + 8 * (j % 2), half = R == 8 ? j : j / 2;
+                        qf[kk][j] = r < rows ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + half * 8 + col) : 0u;
+                    }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < R / 8; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
+            }
+            prefetch();
+            cp_async_wait<S::kStages - 1>();
+            __syncwarp();
+            const uint32_t ks = ring + got * S::kStage, vs = ks + kTile * D * 2;
+            if (++got == S::kStages) got = 0;
+            float s[2][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int key = (lane / 16) * 8 + lane % 8, chunk = 2 * kk + (lane / 8) % 2;
+                uint32_t kf[4];
+                ldmatrix4(kf, ks + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+                if constexpr (R == 8) {
+                    mma16816(s[0], qf[kk][0], 0u, qf[kk][1], 0u, kf[0], kf[1]);
+                    mma16816(s[1], qf[kk][0], 0u, qf[kk][1], 0u, kf[2], kf[3]);
+                } else {
+                    mma16816(s[0], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[0], kf[1]);
+                    mma16816(s[1], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[2], kf[3]);
+                }
+            }
+            const int x0 = c.tile * kTile + col;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool in = x0 + 8 * t + i < c.k.n;
+                    s[t][i] = in ? s[t][i] * a.scale_log2 : -INFINITY;
+                    if (R == 16) s[t][2 + i] = in ? s[t][2 + i] * a.scale_log2 : -INFINITY;
+                }
+            if (a.weights) {
+                // the raw scores, for the weights' pass over them
+                const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
+#pragma unroll
+                for (int i = 0; i < R / 8; ++i) {
+                    const int r = g0 + row + 8 * i;
+                    if (r >= a.G) continue;
+                    float* to = buf.scores + ((int64_t)c.b * a.Hq + hk * a.G + r) * buf.score_stride;
+                    if (x0 < c.k.n) to[x0] = s[0][2 * i];
+                    if (x0 + 1 < c.k.n) to[x0 + 1] = s[0][2 * i + 1];
+                    if (x0 + 8 < c.k.n) to[x0 + 8] = s[1][2 * i];
+                    if (x0 + 9 < c.k.n) to[x0 + 9] = s[1][2 * i + 1];
+                }
+            }
+            uint32_t pf[4], pl[4];
+            float top[R / 8];
+            bool grows = false;
+#pragma unroll
+            for (int i = 0; i < R / 8; ++i) {
+                float t = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                top[i] = fmaxf(m[i], t);
+                grows = grows || top[i] > m[i];
+            }
+            if (__any_sync(0xffffffffu, grows)) {
+                float f[R / 8];
+#pragma unroll
+                for (int i = 0; i < R / 8; ++i) {
+                    f[i] = top[i] > m[i] ? exp2_approx(m[i] - top[i]) : 1.f;
+                    l[i] *= f[i];
+                    m[i] = top[i];
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    o[i][0] *= f[0];
+                    o[i][1] *= f[0];
+                    o[i][2] *= f[R / 8 - 1];
+                    o[i][3] *= f[R / 8 - 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R / 8; ++i) {
+                const float use = m[i] == -INFINITY ? 0.f : m[i];
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[e / 2][2 * i + e % 2] - use);
+                l[i] += (p[0] + p[1]) + (p[2] + p[3]);
+                const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
+                if constexpr (R == 8) {
+                    pf[0] = h0;
+                    pf[1] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
+                    pf[2] = h1;
+                    pf[3] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
+                } else {
+                    pf[i] = h0;
+                    pf[2 + i] = h1;
+                    pl[i] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
+                    pl[2 + i] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
+                }
+            }
+#pragma unroll
+            for (int cc = 0; cc < D / 16; ++cc) {
+                const int key = ((lane / 8) % 2) * 8 + lane % 8, chunk = 2 * cc + lane / 16;
+                uint32_t vf[4];
+                ldmatrix4_trans(vf, vs + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+                mma16816(o[2 * cc], pf[0], pf[1], pf[2], pf[3], vf[0], vf[1]);
+                mma16816(o[2 * cc + 1], pf[0], pf[1], pf[2], pf[3], vf[2], vf[3]);
+                if constexpr (R == 16) {
+                    mma16816(o[2 * cc], pl[0], pl[1], pl[2], pl[3], vf[0], vf[1]);
+                    mma16816(o[2 * cc + 1], pl[0], pl[1], pl[2], pl[3], vf[2], vf[3]);
+                }
+            }
+            __syncwarp();
+            ++at;
+            if (c.tile + 1 < c.tiles && at < hi) {
+                ++c.tile;
+                continue;
+            }
+            // the unit, or this warp's part of it, is done
+#pragma unroll
+            for (int i = 0; i < R / 8; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            }
+            if constexpr (R == 8) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    o[i][0] += o[i][2];
+                    o[i][1] += o[i][3];
+                }
+            }
+            const bool open_start = seg_tile > 0, open_end = c.tile + 1 < c.tiles;
+            if (open_start || open_end) {
+                // one that began before is kept beside the ring, the last one (no
+                // tile follows it) in the ring
+                if (!open_start) cp_async_wait<0>();
+                __syncwarp();
+                float* part = open_start ? head_part : tail_part;
+#pragma unroll
+                for (int i = 0; i < R / 8; ++i) {
+                    const int r = row + 8 * i;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        *reinterpret_cast<float2*>(part + r * D + t * 8 + col) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+                    if (lane % 4 == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m[i], l[i]);
+                }
+                if (lane == 0) {
+                    Record& rec = records[2 * warp + (open_start ? 0 : 1)];
+                    rec.valid = 1;
+                    rec.b = c.b;
+                    rec.u = c.u;
+                    rec.tile = seg_tile;
+                    rec.tiles = c.tiles;
+                    rec.open_end = open_end;
+                    rec.at = seg_at;
+                }
+            } else {
+                const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
+#pragma unroll
+                for (int i = 0; i < R / 8; ++i) {
+                    const int r = g0 + row + 8 * i;
+                    if (r >= a.G) continue;
+                    if (pp.o) join_prefix<NT>(pp, D, c.b, hk, r, col, m[i], l[i], &o[0][2 * i], 4, 8);
+                    const float inv = inverse(l[i]);
+                    __nv_bfloat16* to = a.out + ((int64_t)c.b * a.Hq + hk * a.G + r) * D + col;
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        *reinterpret_cast<uint32_t*>(to + t * 8) = pack_bf16(o[t][2 * i] * inv, o[t][2 * i + 1] * inv);
+                    if (a.weights && lane % 4 == 0)
+                        buf.lse[(int64_t)c.b * a.Hq + hk * a.G + r] = log_sum(m[i], l[i]);
+                }
+            }
+            seg_at = at;
+            seg_tile = 0;
+            fresh = true;
+            if (at < hi) advance(a, c, units);
+        }
+        cp_async_wait<0>();
+    }
+    __syncthreads();
+
+    // join the open units of this block's warps, run by run
+    for (int first = 0; first < 2 * kWarps;) {
+        if (!records[first].valid) {
+            ++first;
+            continue;
+        }
+        int last = first, next = first, count = 0;
+        int8_t chain[2 * kWarps];           // the unit's records
+        for (;;) {
+            chain[count++] = (int8_t)last;
+            if (!records[last].open_end) break;
+            do ++next; while (next < 2 * kWarps && !records[next].valid);
+            if (next >= 2 * kWarps) break;
+            last = next;
+        }
+        const Record rec = records[first];
+        const bool before = rec.at - rec.tile < block_lo, after = records[last].open_end;
+        const int hk = rec.u / chunks, g0 = (rec.u % chunks) * R;
+        for (int i = tid; i < R * D / 4; i += kThreads) {
+            const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            join<D, R>(r, col, count,
+                       [&](int j) {
+                           const int k = chain[j];
+                           return reinterpret_cast<const float*>(
+                               k % 2 ? smem + (k / 2) * S::kRing : smem + kWarps * S::kRing + (k / 2) * S::kPart);
+                       },
+                       m, l, o);
+            if (before || after) {
+                float* part = buf.parts + (int64_t)(2 * blockIdx.x + (before ? 0 : 1)) * (R * D + 2 * R);
+                *reinterpret_cast<float4*>(part + r * D + col) = o;
+                if (col == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, l);
+            } else if (g0 + r < a.G) {
+                finish<D>(a, buf, pp, rec.b, hk, g0 + r, col, m, l, o);
+            }
+        }
+        if (before || after) {
+            // the block that brings a unit's last part joins them all
+            const int64_t start = rec.at - rec.tile;
+            const int c0 = (int)(start / per), c1 = (int)((start + rec.tiles - 1) / per);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int n = atomicAdd(buf.tickets + c0, 1);
+                last_block = n == c1 - c0;
+                if (last_block) buf.tickets[c0] = 0;
+            }
+            __syncthreads();
+            if (last_block) {
+                __threadfence();
+                for (int i = tid; i < R * D / 4; i += kThreads) {
+                    const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+                    float m = -INFINITY, l = 0.f;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    join<D, R>(r, col, c1 - c0 + 1,
+                               [&](int s) { return buf.parts + (int64_t)(2 * (c0 + s) + (s ? 0 : 1)) * (R * D + 2 * R); }, m, l, o);
+                    if (g0 + r < a.G) finish<D>(a, buf, pp, rec.b, hk, g0 + r, col, m, l, o);
+                }
+            }
+            __syncthreads();
+        }
+        first = last + 1;
+    }
+}
+
+// weights[slot, h, key] += sum over the group's heads of exp(score - log of the
+// row's denominator).  Reads the scores that the decode kernel left (in L2, up
+// to its size) instead of the keys: 4 bytes a head and key for 2 head_dim.
+__global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBuffers buf) {
+    const int b = blockIdx.z, hk = blockIdx.y;
+    const Request r = read_request(a, b);
+    const Keys k = visible_keys(a, r);
+    const int64_t row = (int64_t)b * a.Hq + (int64_t)hk * a.G;
+    float* w = a.weights + ((int64_t)r.slot * a.Hk + hk) * a.capacity;
+    for (int x = blockIdx.x * 256 + threadIdx.x; x < k.n; x += gridDim.x * 256) {
+        float sum = 0.f;
+#pragma unroll 8
+        for (int g = 0; g < a.G; ++g) sum += exp2_approx(buf.scores[(row + g) * buf.score_stride + x] - buf.lse[row + g]);
+        w[x + (x >= k.head ? k.gap : 0)] += sum;
+    }
+}
+
+template <int D, int R>
+bd_status launch_shape(const Args& a, DecodeBuffers buf, const PrefixParts& pp, cudaStream_t stream) {
+    const void* kernel = reinterpret_cast<const void*>(decode_kernel<D, R>);
+    if (!set_smem_attr(kernel, Shape<D, R>::kSmem, D == 128 ? (R == 8 ? 4 : 5) : (R == 8 ? 6 : 7))) return BD_ERR_CUDA;
+    const int blocks = decode_blocks();
+    decode_kernel<D, R><<<blocks, kThreads, Shape<D, R>::kSmem, stream>>>(a, buf, pp);
+    return launch_status();
+}
+
+}  // namespace
+
+int decode_blocks() { return sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks; }
+
+size_t decode_parts_bytes(int head_dim) { return (size_t)2 * decode_blocks() * (16 * head_dim + 32) * sizeof(float); }
+
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const PrefixParts& pp,
+                        cudaStream_t stream) {
+    bd_status st;
+    if (a.G <= 8)
+        st = head_dim == 128 ? launch_shape<128, 8>(a, buf, pp, stream) : launch_shape<64, 8>(a, buf, pp, stream);
+    else
+        st = head_dim == 128 ? launch_shape<128, 16>(a, buf, pp, stream) : launch_shape<64, 16>(a, buf, pp, stream);
+    if (st != BD_OK || !a.weights) return st;
+    const int64_t heads = (int64_t)a.B * a.Hk, most = (a.capacity + 255) / 256;
+    int64_t x = (8 * (int64_t)sm_count() + heads - 1) / heads;
+    x = x < most ? x : most;
+    weigh_kernel<<<dim3((unsigned)x, (unsigned)a.Hk, (unsigned)a.B), 256, 0, stream>>>(a, buf);
+    return launch_status();
+}
+
+}  // namespace attn
+}  // namespace bd

@@ -1,0 +1,132 @@
+// bd_attn_math.cuh -- device pieces of the attention kernels: warp-level copies
+// and matrix products, the softmax's exponential, and the interface between the
+// kernels of one call (what lies where in the workspace).
+#pragma once
+
+#include <math.h>
+
+#include "bd_attn.cuh"
+
+namespace bd {
+namespace attn {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes from global to shared memory; where `in` is false nothing is read
+// and zeros are written.
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from, bool in) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// c (16 x 8, f32) += a (16 x 16, bf16) b (16 x 8, bf16)
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 2^x (2 units in the last place; -inf gives 0).
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// What a row's sum divides by: a row that saw nothing gives zeros, a NaN stays.
+__device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
+
+// ---- the workspace -----------------------------------------------------------
+// header, then tickets of units that several blocks join (zero between calls),
+// then what one call needs.
+constexpr int kMaxBlocks = 2048;
+
+struct DecodeBuffers {
+    float* parts;        // [2 * blocks] open units: O [R][D], (m, l) [R]
+    int* tickets;        // [kMaxBlocks]
+    float* scores;       // [B, Hq, score_stride] scaled scores of the visible own keys, by place among them
+    float* lse;          // [B, Hq] log2 of the softmax's denominator
+    int64_t score_stride;
+    int32_t least_tiles; // of a block
+};
+
+// Unnormalised parts of rows that the tile kernel computed: part s of a unit's
+// row lies kPartRows rows behind part s - 1.
+constexpr int kPartRows = 256;
+struct PrefixParts {
+    const float* o;          // [rows][D]; NULL: none
+    const float2* ml;        // [rows] maximum (log2) and sum
+    const int32_t* req_unit; // [B] unit of the request's row tile and head 0, -1: no prefix
+    const int32_t* req_row;  // [B] its first row in the unit
+    const int64_t* unit_row; // [units] first row of the unit's part from block 0
+    const int2* unit_segs;   // [units] first block and number of parts
+};
+
+// ---- the tile kernel's plan (in the workspace) ---------------------------------
+// A row tile: `tokens` tokens (their rows of q begin at row0; for prefixes row0 is
+// a place in `order`) and the keys that any of them sees, as blocks of 128 of two
+// sources, the prefix (0) and the request's own keys (1): of each the blocks
+// [0, head) and [from, from + tail).
+struct RowTile {
+    int32_t slot[2], head[2], from[2], tail[2];
+    int32_t off;             // keys of the prefix: the own keys' positions begin there
+    int32_t own_hi;          // own keys that the last token sees
+    int32_t lo_min;          // first position of the earliest window
+    int32_t row0, tokens, t0;// t0: the first token's position (prefill)
+    int32_t blocks, pad;
+    int64_t line, rows_before;
+};
+struct PlanHead {
+    int64_t tiles, line, per;// row tiles, blocks of all units, blocks of a thread block
+};
+struct TilePlan {
+    PlanHead* head;
+    RowTile* tiles;
+    int32_t* order;          // requests sorted by prefix
+    int32_t *req_unit, *req_row;
+    int64_t* unit_row;
+    int2* unit_segs;
+    float* o;                // unnormalised parts
+    float2* ml;
+};
+
+int tile_blocks();
+int64_t split_below();       // units from which on a prefill is not split
+int64_t most_tiles(int64_t tokens, int64_t batch, int G);
+bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
+
+int decode_blocks();
+size_t decode_parts_bytes(int head_dim);
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const PrefixParts& pp,
+                        cudaStream_t stream);
+
+}  // namespace attn
+}  // namespace bd

@@ -1,0 +1,781 @@
+// bd_attn_tile.cu -- attention of many query rows on the same keys: prefill, and
+// the shared prefixes of a decode step.
+//
+// A unit is up to 256 query rows on one key/value head: the rows are (token,
+// query head of the group) pairs, so that a group's heads read their keys once.
+// 4 head_dim flops a row and key against 4 head_dim bytes a key: with 256 rows
+// the tensor cores bound it.  One block a SM: one warp loads keys and values
+// by TMA through a ring, one thread issues the tcgen05 products, two groups of four
+// warps own 128 rows each, one thread a row.  Tensor memory holds the scores of
+// both groups (2 x 128 columns) and both outputs (2 x head_dim).  Per block of
+// 128 keys: S = Q K^T (both operands in shared memory), the row's thread takes its
+// 128 scores to registers, keeps the running maximum and sum, writes P as bf16
+// over the scores, and O += P V runs with P from tensor memory.  While one group
+// works on its softmax the products of the other run.
+// The output is only rescaled when a row's maximum has grown by more than 2^8
+// since the last time; P is then at most 2^8 and rounds no worse.
+//
+// With enough units each block takes whole ones and writes the result.  Else the
+// blocks of keys of all units form one line that is cut into equal parts for the
+// thread blocks, which leave unnormalised parts in the workspace; the decode
+// kernel joins them with the requests' own keys, the join kernel those of a prefill.
+#include <math.h>
+
+#include <algorithm>
+
+#include "bd_attn_math.cuh"
+#include "bd_sm100.cuh"
+#include "bd_tc_common.cuh"
+
+namespace bd {
+namespace attn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kKeys = 128;                 // of a block
+constexpr int kThreads = 384;
+constexpr uint32_t kLimit = 1u << 20;      // polls of a wait
+constexpr float kGrow = 8.f;               // powers of two that a maximum may grow before a rescale
+
+// Which of a tensor map's outer dimensions is which.
+struct MapOrder {
+    int32_t head, token, slot;
+};
+
+template <int D>
+struct Tile {
+    static constexpr int kHalves = D / 64;                 // 128-byte wide parts of a row
+    static constexpr int kQ = 128 * D * 2;                 // bytes of 128 rows
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kQ;
+};
+
+// Blocks [0, head) and [from, from + tail) of a source.
+struct Span {
+    int32_t head, from, tail;
+};
+
+__device__ __forceinline__ Span span_of(int lo, int hi, int sinks) {
+    // keys [0, min(sinks, hi)) and [lo, hi) of a source
+    Span s;
+    hi = max(hi, 0);
+    lo = min(max(lo, 0), hi);
+    const int last = (hi + kKeys - 1) / kKeys;
+    s.head = min((min(max(sinks, 0), hi) + kKeys - 1) / kKeys, last);
+    s.from = max(lo / kKeys, s.head);
+    s.tail = max(last - s.from, 0);
+    return s;
+}
+
+__device__ __forceinline__ int tokens_of_tile(int G) { return kPartRows / G; }
+
+// The row tile's keys: a prefix (source 0) and the request's own (source 1).
+__device__ __forceinline__ void set_keys(const Args& a, RowTile& t, int plen, int lo_min, int own_hi) {
+    const Span p = span_of(lo_min, plen, a.sinks), o = span_of(lo_min - plen, own_hi, a.sinks - plen);
+    t.off = plen;
+    t.own_hi = own_hi;
+    t.lo_min = lo_min;
+    t.head[0] = p.head;
+    t.from[0] = p.from;
+    t.tail[0] = p.tail;
+    t.head[1] = o.head;
+    t.from[1] = o.from;
+    t.tail[1] = o.tail;
+    // a unit without keys still has its rows to write
+    t.blocks = max(1, p.head + p.tail + o.head + o.tail);
+}
+
+// The largest v with table[v] <= x (table ascending, table[0] <= x).
+template <typename T, typename X>
+__device__ __forceinline__ int last_at_most(const T* table, int n, X x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (table[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t* total) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int64_t incl = v;
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += o;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        before += w < warp ? part[w] : 0;
+        all += part[w];
+    }
+    __syncthreads();
+    *total = all;
+    return before + incl - v;
+}
+
+// Lays out the row tiles of a call (one block).  Prefill: every request's rows in
+// tiles of whole tokens.  Prefixes: the requests sorted by prefix (stably), every
+// prefix's requests in tiles.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const TilePlan plan, int blocks, int split) {
+    extern __shared__ int32_t counts[];     // [P + 1] of each prefix, then its first place
+    __shared__ int64_t part[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int per_tile = tokens_of_tile(a.G);
+    int tiles = 0;
+    if (a.cu_q) {
+        for (int base = 0; base < a.B; base += kPlanThreads) {
+            const int b = base + tid;
+            int n = 0;
+            if (b < a.B) n = (read_request(a, b).rows + per_tile - 1) / per_tile;
+            int64_t all;
+            const int first = tiles + (int)block_scan(n, part, &all);
+            if (b < a.B) plan.req_unit[b] = first;
+            tiles += (int)all;
+        }
+        __syncthreads();
+        for (int i = tid; i < tiles; i += kPlanThreads) {
+            const int b = last_at_most(plan.req_unit, a.B, i);
+            const Request r = read_request(a, b);
+            RowTile t{};
+            const int i0 = (i - plan.req_unit[b]) * per_tile;
+            t.slot[0] = r.pslot;
+            t.slot[1] = r.slot;
+            t.row0 = r.row0 + i0;
+            t.tokens = min(per_tile, r.rows - i0);
+            t.t0 = r.plen + r.len - r.rows + i0;
+            const int end = min(r.plen + r.len, t.t0 + t.tokens);
+            set_keys(a, t, r.plen, window_lo(a, t.t0), max(0, end - r.plen));
+            plan.tiles[i] = t;
+        }
+    } else {
+        for (int p = tid; p <= a.P; p += kPlanThreads) counts[p] = 0;
+        __syncthreads();
+        for (int b = tid; b < a.B; b += kPlanThreads) {
+            const Request r = read_request(a, b);
+            plan.req_unit[b] = -1;
+            if (r.plen > 0) atomicAdd(counts + a.prefix_ids[b], 1);
+        }
+        __syncthreads();
+        int first = 0;
+        for (int base = 0; base < a.P; base += kPlanThreads) {
+            const int p = base + tid;
+            const int n = p < a.P ? counts[p] : 0;
+            int64_t all;
+            const int at = first + (int)block_scan(n, part, &all);
+            const int tile = tiles;
+            int64_t all_tiles;
+            const int t0 = tile + (int)block_scan((n + per_tile - 1) / per_tile, part, &all_tiles);
+            if (p < a.P) counts[p] = at;
+            // what every tile of the group shares
+            for (int i = 0; i * per_tile < n; ++i) {
+                RowTile t{};
+                t.slot[0] = a.prefix_slots[p];
+                t.row0 = at + i * per_tile;
+                t.tokens = min(per_tile, n - i * per_tile);
+                t.off = a.prefix_lens[p];
+                plan.tiles[t0 + i] = t;
+            }
+            first += (int)all;
+            tiles += (int)all_tiles;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // stable placement, 32 requests at a time
+            for (int base = 0; base < a.B; base += 32) {
+                const int b = base + lane;
+                int id = -1;
+                if (b < a.B) {
+                    const Request r = read_request(a, b);
+                    id = r.plen > 0 ? a.prefix_ids[b] : -1;
+                }
+                const unsigned same = __match_any_sync(0xffffffffu, id);
+                const int rank = __popc(same & ((1u << lane) - 1));
+                const int at = id >= 0 ? counts[id] : 0;
+                __syncwarp();
+                if (id >= 0) {
+                    plan.order[at + rank] = b;
+                    if (rank == 0) counts[id] = at + __popc(same);
+                }
+                __syncwarp();
+            }
+        }
+        __syncthreads();
+        // a warp a tile: the earliest key that its requests see
+        for (int i = warp; i < tiles; i += kPlanThreads / 32) {
+            RowTile t = plan.tiles[i];
+            int lo = a.window > 0 ? 0x7fffffff : 0;
+            for (int j = lane; j < t.tokens; j += 32) {
+                const int b = plan.order[t.row0 + j];
+                if (a.window > 0) {
+                    const Request r = read_request(a, b);
+                    lo = min(lo, window_lo(a, r.plen + r.len - 1));
+                }
+                plan.req_unit[b] = i * a.Hk;
+                plan.req_row[b] = j * a.G;
+            }
+            for (int x = 16; x; x >>= 1) lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+            if (lane == 0) {
+                set_keys(a, t, t.off, lo, 0);
+                plan.tiles[i] = t;
+            }
+        }
+        __syncthreads();
+    }
+    if (!split) {
+        if (tid == 0) *plan.head = PlanHead{tiles, 0, 0};
+        return;
+    }
+    __syncthreads();
+    // the line of blocks
+    int64_t line = 0, rows = 0;
+    for (int base = 0; base < tiles; base += kPlanThreads) {
+        const int i = base + tid;
+        int64_t all, n = i < tiles ? plan.tiles[i].blocks : 0;
+        const int64_t at = line + block_scan(n, part, &all);
+        line += all;
+        int64_t all_rows;
+        const int64_t r = rows + block_scan(i < tiles ? plan.tiles[i].tokens * a.G : 0, part, &all_rows);
+        rows += all_rows;
+        if (i < tiles) {
+            plan.tiles[i].line = at;
+            plan.tiles[i].rows_before = r;
+        }
+    }
+    __syncthreads();
+    line *= a.Hk;
+    const int64_t per = max((int64_t)1, (line + blocks - 1) / blocks);
+    for (int64_t u = tid; u < (int64_t)tiles * a.Hk; u += kPlanThreads) {
+        const int i = (int)(u / a.Hk), hk = (int)(u % a.Hk);
+        const RowTile& t = plan.tiles[i];
+        const int64_t start = t.line * a.Hk + (int64_t)hk * t.blocks;
+        const int c0 = (int)(start / per), c1 = (int)((start + t.blocks - 1) / per);
+        plan.unit_segs[u] = make_int2(c0, c1 - c0 + 1);
+        plan.unit_row[u] = t.rows_before * a.Hk + (int64_t)hk * t.tokens * a.G;
+    }
+    if (tid == 0) *plan.head = PlanHead{tiles, line, per};
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
+                                            int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
+          "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
+          "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr));
+}
+
+// Shared-memory descriptor of a 16-key slice of V: rows of 64 head_dim values
+// (128 bytes, 128-byte swizzle), the reduction running over rows: groups of 8 rows
+// are 1024 bytes apart, the second 64 values of a row 128 rows further.
+__device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((kKeys * 128) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+constexpr uint32_t kTransposeB = 1u << 16;   // instruction descriptor: B's rows run along the reduction
+
+// One part of a unit that a block works on.
+struct Segment {
+    int tile, hk, first, last;               // blocks [first, last) of the unit
+};
+
+// The segments of this block, in order.
+struct Walk {
+    int64_t at, end;                          // places on the line
+    int tile, hk, first;
+    bool whole;
+    __device__ __forceinline__ bool next(const Args& a, const TilePlan& plan, Segment& s) {
+        if (at >= end) return false;
+        const int n = plan.tiles[tile].blocks;
+        s.tile = tile;
+        s.hk = hk;
+        s.first = first;
+        s.last = whole ? n : (int)min((int64_t)n, first + (end - at));
+        at += whole ? 1 : s.last - first;
+        first = 0;
+        if (++hk == a.Hk) {
+            hk = 0;
+            ++tile;
+        }
+        return true;
+    }
+};
+
+// Block i of a row tile: its source, first key and the source's end.
+struct Block {
+    int src, slot, key, end, off;
+};
+__device__ __forceinline__ Block block_of(const RowTile& t, int i) {
+    Block b;
+    b.src = i >= t.head[0] + t.tail[0];
+    if (b.src) i -= t.head[0] + t.tail[0];
+    const int head = b.src ? t.head[1] : t.head[0], from = b.src ? t.from[1] : t.from[0];
+    b.key = (i < head ? i : from + i - head) * kKeys;
+    b.slot = b.src ? t.slot[1] : t.slot[0];
+    b.off = b.src ? t.off : 0;
+    b.end = b.src ? t.own_hi : t.off;
+    return b;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    tile_kernel(const Args a, const TilePlan plan, const __grid_constant__ CUtensorMap kmap,
+                const __grid_constant__ CUtensorMap vmap, const MapOrder order, int split) {
+    using T = Tile<D>;
+    constexpr int NS = T::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], s_full[2], p_full[2], pv_done[2], drained;
+    __shared__ uint32_t tmem_at;
+    __shared__ int start[2];
+    __shared__ int64_t line_at[2];
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    unsigned* status = a.status;
+    auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        return mbar_wait(bar, parity & 1, kLimit, status, where, status + 2);
+    };
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t q_at = base, ring = base + 2 * T::kQ;
+
+    const PlanHead head = *plan.head;
+    Walk walk{};
+    if (split) {
+        walk.at = min(head.line, head.per * blockIdx.x);
+        walk.end = min(head.line, walk.at + head.per);
+        if (walk.at >= walk.end) return;
+        for (int i = tid; i < head.tiles; i += kThreads) {
+            const int64_t lo = plan.tiles[i].line * a.Hk, n = plan.tiles[i].blocks;
+            if (walk.at >= lo && walk.at < lo + n * a.Hk) {
+                start[0] = i;
+                line_at[0] = walk.at - lo;
+            }
+        }
+        __syncthreads();
+        walk.tile = start[0];
+        const int n = plan.tiles[walk.tile].blocks;
+        walk.hk = (int)(line_at[0] / n);
+        walk.first = (int)(line_at[0] % n);
+    } else {
+        // the last tile of a prompt has the most keys: begin there
+        const int64_t units = (int64_t)head.tiles * a.Hk;
+        if ((int64_t)blockIdx.x >= units) return;
+        const int64_t u = units - 1 - blockIdx.x;
+        walk.at = 0;
+        walk.end = 1;
+        walk.tile = (int)(u / a.Hk);
+        walk.hk = (int)(u % a.Hk);
+        walk.whole = true;
+    }
+
+    if (warp == 8) tmem_alloc(&tmem_at, 512);
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(kv_full + i, 1);
+            mbar_init(kv_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 128);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 128);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+
+    // registers: 3 x 168 for each lane of the three warp groups at launch; the loading
+    // and issuing group gives 48 of its own to each of the others, whose threads keep
+    // a row's 128 scores
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8 && lane == 0) {
+            // keys and values: stage 2 i holds the keys of the i-th block, stage 2 i + 1 its values
+            prefetch_tensormap(&kmap);
+            prefetch_tensormap(&vmap);
+            int put = 0;
+            bool ok = true;
+            Segment s;
+            while (ok && walk.next(a, plan, s)) {
+                const RowTile t = plan.tiles[s.tile];
+                for (int i = s.first; ok && i < s.last; ++i) {
+                    const Block b = block_of(t, i);
+                    auto at = [&](int dim) { return dim == order.token ? b.key : dim == order.head ? s.hk : b.slot; };
+                    for (int kv = 0; ok && kv < 2; ++kv, ++put) {
+                        const int st = put % NS;
+                        if (put >= NS) ok = wait(kv_empty + st, put / NS - 1, 1);
+                        if (!ok) break;
+                        mbar_expect_tx(kv_full + st, T::kQ);
+                        for (int h = 0; h < T::kHalves; ++h)
+                            tma_load_4d(ring + st * T::kQ + h * kKeys * 128, kv ? &vmap : &kmap, kv_full + st, h * 64, at(0), at(1), at(2));
+                    }
+                }
+            }
+            // nothing may still be on its way into shared memory when the block ends
+            for (int i = max(0, put - NS); i < put; ++i) wait(kv_full + i % NS, i / NS, 2);
+        }
+        if (warp == 9 && lane == 0) {
+            const uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
+            int steps[2] = {0, 0}, segs[2] = {0, 0};
+            bool ok = true;
+            auto scores = [&](int g, int st, bool fresh) {      // S of group g from the keys in stage st
+                if (fresh) ok = ok && wait(q_full + g, segs[g]++, 3);
+                // P of the block before lies where S goes
+                if (steps[g] > 0) ok = ok && wait(pv_done + g, steps[g] - 1, 4);
+                if (!ok) return;
+                tc_fence_after();
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = (k / 4) * (kKeys * 128) + (k % 4) * 32;
+                    mma_ss(tmem + g * 128, desc_sw128(q_at + g * T::kQ + off), desc_sw128(ring + st * T::kQ + off), idesc_s, k > 0);
+                }
+                mma_commit(s_full + g);
+            };
+            auto values = [&](int g, int st, bool first) {      // O of group g += P V, the values in stage st
+                ok = ok && wait(p_full + g, steps[g]++, 5);
+                if (!ok) return;
+                tc_fence_after();
+                for (int k = 0; k < kKeys / 16; ++k)
+                    mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, desc_v(ring + st * T::kQ + k * 2048), idesc_o, !first || k > 0);
+                mma_commit(pv_done + g);
+            };
+            Segment s, next;
+            int got = 0;
+            bool more = walk.next(a, plan, s);
+            int groups = more && plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+            int i = s.first;
+            if (more) {
+                ok = wait(kv_full, 0, 6);
+                for (int g = 0; ok && g < groups; ++g) scores(g, 0, true);
+                if (ok) mma_commit(kv_empty);
+            }
+            while (ok && more) {
+                const bool same = i + 1 < s.last;
+                bool has_next = same;
+                next = s;
+                int next_groups = groups;
+                if (!same) {
+                    has_next = walk.next(a, plan, next);
+                    if (has_next) next_groups = plan.tiles[next.tile].tokens * a.G > 128 ? 2 : 1;
+                }
+                const int kst = (got + 2) % NS, vst = (got + 1) % NS;
+                const bool first = i == s.first;
+                ok = wait(kv_full + vst, (got + 1) / NS, 7);
+                if (ok && has_next) ok = wait(kv_full + kst, (got + 2) / NS, 8);
+                if (!ok) break;
+                if (same) {
+                    values(0, vst, first);
+                    scores(0, kst, false);
+                    if (groups == 2) values(1, vst, first);
+                    mma_commit(kv_empty + vst);
+                    if (groups == 2) scores(1, kst, false);
+                    mma_commit(kv_empty + kst);
+                } else {
+                    for (int g = 0; g < groups; ++g) values(g, vst, first);
+                    mma_commit(kv_empty + vst);
+                    if (has_next) {
+                        for (int g = 0; g < next_groups; ++g) scores(g, kst, true);
+                        mma_commit(kv_empty + kst);
+                    }
+                }
+                more = has_next;
+                i = same ? i + 1 : next.first;
+                s = next;
+                groups = next_groups;
+                got += 2;
+            }
+            // the products in flight end before the tensor memory is given back
+            mma_commit(&drained);
+            wait(&drained, 0, 9);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // a group of 128 rows, one thread a row
+        const int g = warp / 4, r = g * 128 + tid % 128;
+        const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * D;
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+        const float scale = fmaxf(fabsf(a.scale_log2), 1.2e-38f);   // never 0: a hidden score's -inf stays -inf
+        int step = 0, put = 0;
+        bool ok = true;
+        Segment s;
+        while (ok && walk.next(a, plan, s)) {
+            const RowTile t = plan.tiles[s.tile];
+            const int blocks = s.last - s.first;
+            if (g == 1 && t.tokens * a.G <= 128) {
+                put += 2 * blocks;
+                continue;
+            }
+            // this row's token, head and visible range
+            const int token = r / a.G;
+            const bool real = token < t.tokens;
+            int row = 0, hi = 0, lo = 0;
+            if (real) {
+                row = t.row0 + token;
+                int pos = t.t0 + token;
+                if (!a.cu_q) {
+                    row = plan.order[row];
+                    const Request rq = read_request(a, row);
+                    pos = rq.plen + rq.len - 1;
+                }
+                hi = pos + 1;
+                lo = window_lo(a, pos);
+            }
+            const int head_at = s.hk * a.G + r - token * a.G;
+            {
+                const uint4* from = reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.q_stride + (int64_t)head_at * D);
+                const uint32_t to = q_at + g * T::kQ + (tid % 128) * 128;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = real ? from[c] : make_uint4(0, 0, 0, 0);
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + (c / 8) * (kKeys * 128) + (((c % 8) ^ (tid % 8)) << 4)),
+                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(q_full + g);
+
+            float m = -INFINITY, l = 0.f;
+            for (int i = s.first; i < s.last; ++i, ++step, put += 2) {
+                const Block b = block_of(t, i);
+                if (g == 0) {
+                    // values that no row of the unit sees may be anything: they are
+                    // multiplied by zero, so they have to be finite
+                    const int key = b.key + tid;
+                    const int pos = b.off + key;
+                    const bool seen = key < b.end && (pos < a.sinks || pos >= t.lo_min);
+                    const bool whole = b.key + kKeys <= b.end && (b.off + b.key + kKeys <= a.sinks || b.off + b.key >= t.lo_min);
+                    if (!whole) {
+                        const int st = (put + 1) % NS;
+                        ok = wait(kv_full + st, (put + 1) / NS, 10);
+                        if (!seen)
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
+                                             : "memory");
+                        fence_proxy_async_smem();
+                    }
+                }
+                ok = ok && wait(s_full + g, step, 11);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float v[kKeys];
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, v + c);
+                tmem_ld_wait();
+                const int p0 = b.off + b.key;
+                const int end = min(hi, b.off + b.end);
+                if (!(p0 + kKeys <= end && (p0 >= lo || p0 + kKeys <= a.sinks))) {
+                    const int n = end - p0, from = lo - p0, sinks = a.sinks - p0;
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        v[c] = c < n && (c < sinks || c >= from) ? v[c] : -INFINITY;
+                }
+                float top[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int c = 4; c < kKeys; c += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
+                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const float mn = fmaxf(m, mx == -INFINITY ? -INFINITY : mx * scale);
+                const bool grows = mn > m + kGrow || m == -INFINITY;
+                if (i == s.first) {
+                    m = mn;
+                } else if (__any_sync(0xffffffffu, grows && mn > m)) {
+                    float f = 1.f;
+                    if (grows && mn > m) {
+                        f = exp2_approx(m - mn);
+                        m = mn;
+                        l *= f;
+                    }
+                    ok = wait(pv_done + g, step - 1, 12);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_at + c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st16(o_at + c, o);
+                    }
+                }
+                const float use = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kKeys; c += 32) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x = exp2_approx(fmaf(v[c + e], scale, -use)), y = exp2_approx(fmaf(v[c + e + 1], scale, -use));
+                        sum[e % 4] += x;
+                        sum[e % 4 + 1] += y;
+                        p[e / 2] = pack_bf16(x, y);
+                    }
+                    tmem_st16(s_at + c / 2, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(p_full + g);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 13));
+            if (!ok) break;
+            tc_fence_after();
+            const float inv = inverse(l);
+            const int64_t part_row =
+                split ? plan.unit_row[(int64_t)s.tile * a.Hk + s.hk] + (int64_t)blockIdx.x * kPartRows + r : 0;
+            if (split && real) plan.ml[part_row] = make_float2(m, l);
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_at + c, o);
+                tmem_ld_wait();
+                if (!real) continue;
+                if (split) {
+                    float4* to = reinterpret_cast<float4*>(plan.o + part_row * D + c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else {
+                    uint4* to = reinterpret_cast<uint4*>(a.out + ((int64_t)row * a.Hq + head_at) * D + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        to[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                           pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of a split prefill: one thread four values of a row.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan plan) {
+    const int64_t units = (int64_t)plan.head->tiles * a.Hk;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const RowTile& t = plan.tiles[u / a.Hk];
+        const int hk = (int)(u % a.Hk), rows = t.tokens * a.G;
+        const int2 seg = plan.unit_segs[u];
+        for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
+            const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+            const int64_t r0 = plan.unit_row[u] + (int64_t)seg.x * kPartRows + r;
+            float m = -INFINITY, l = 0.f;
+            for (int s = 0; s < seg.y; ++s) m = fmaxf(m, plan.ml[r0 + (int64_t)s * kPartRows].x);
+            const float use = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int s = 0; s < seg.y; ++s) {
+                const int64_t at = r0 + (int64_t)s * kPartRows;
+                const float2 ml = plan.ml[at];
+                const float f = exp2_approx(ml.x - use);
+                const float4 v = *reinterpret_cast<const float4*>(plan.o + at * D + col);
+                l += f * ml.y;
+                o.x += f * v.x;
+                o.y += f * v.y;
+                o.z += f * v.z;
+                o.w += f * v.w;
+            }
+            const float inv = inverse(l);
+            const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
+            *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        }
+    }
+}
+
+// The cache as a 4-D tensor whose dimensions follow their strides, whichever
+// layout it has; a dimension of one entry comes last.
+bool cache_map(CUtensorMap* map, MapOrder* order, const void* base, const Args& a, int D) {
+    struct Dim {
+        int64_t stride, size;
+        int32_t* place;
+        uint32_t box;
+    } d[3] = {{a.sh, a.Hk, &order->head, 1}, {a.st, a.capacity, &order->token, kKeys}, {a.ss, a.n_slots, &order->slot, 1}};
+    std::sort(d, d + 3, [](const Dim& x, const Dim& y) {
+        return (x.size == 1) != (y.size == 1) ? y.size == 1 : x.size > 1 && x.stride < y.stride;
+    });
+    uint64_t dims[4] = {(uint64_t)D}, strides[3];
+    uint32_t box[4] = {64};
+    int64_t next = D;
+    for (int i = 0; i < 3; ++i) {
+        const int64_t stride = d[i].size == 1 ? next : d[i].stride;
+        next = stride * d[i].size;
+        strides[i] = (uint64_t)stride * 2;
+        dims[i + 1] = (uint64_t)d[i].size;
+        box[i + 1] = d[i].box;
+        *d[i].place = i;
+    }
+    return make_tmap_bf16_4d_sw128(map, base, dims, strides, box);
+}
+
+template <int D>
+bd_status launch_shape(const Args& a, const TilePlan& plan, int64_t grid, int blocks, int split, cudaStream_t stream) {
+    const void* kernel = reinterpret_cast<const void*>(tile_kernel<D>);
+    if (!set_smem_attr(kernel, Tile<D>::kSmem, D == 128 ? 8 : 9)) return BD_ERR_CUDA;
+    CUtensorMap kmap, vmap;
+    MapOrder order{};
+    if (!cache_map(&kmap, &order, a.k, a, D) || !cache_map(&vmap, &order, a.v, a, D)) return BD_ERR_CUDA;
+    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, blocks, split);
+    bd_status st = launch_status();
+    if (st != BD_OK) return st;
+    tile_kernel<D><<<(unsigned)grid, kThreads, Tile<D>::kSmem, stream>>>(a, plan, kmap, vmap, order, split);
+    st = launch_status();
+    if (st != BD_OK || !a.cu_q || !split) return st;
+    join_kernel<D><<<dim3((unsigned)blocks, 8), 256, 0, stream>>>(a, plan);
+    return launch_status();
+}
+
+}  // namespace
+
+// Row tiles that a call can have at most.
+int64_t most_tiles(int64_t tokens, int64_t batch, int G) { return tokens / (kPartRows / G) + batch; }
+
+bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
+    const int blocks = tile_blocks();
+    const int64_t units = most_tiles(a.T, a.B, a.G) * a.Hk;
+    const int split = !a.cu_q || units < split_below();
+    const int64_t grid = split ? blocks : units;
+    return head_dim == 128 ? launch_shape<128>(a, plan, grid, blocks, split, stream)
+                           : launch_shape<64>(a, plan, grid, blocks, split, stream);
+}
+
+int tile_blocks() { return decode_blocks(); }
+int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
+
+}  // namespace attn
+}  // namespace bd

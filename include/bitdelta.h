@@ -53,6 +53,7 @@ extern "C" {
 
 #define BITDELTA_ABI_VERSION 1
 #define BITDELTA_MAX_VARIANTS 64
+#define BITDELTA_MAX_PREFIXES 8192
 
 typedef enum {
     BD_OK = 0,
@@ -266,7 +267,7 @@ bd_status bitdelta_linear_rows(const void *x, const int32_t *variant_ids,
  *   k, v  : device, bf16 [slots, capacity, kv_heads, head_dim] with the given
  *           strides (in elements, shared by k and v); the head_dim values of a
  *           key are contiguous.  Pointers 16-byte aligned, strides multiples of
- *           8 and positive; distinct (slot, token, head) rows do not overlap.
+ *           8 in [8, 2^38]; distinct (slot, token, head) rows do not overlap.
  *   slots, capacity, kv_heads >= 1; head_dim 64 or 128; capacity <= 2^24,
  *   slots <= 2^24.
  * A request owns one slot: its key j lies at token j of the slot.  What lies
@@ -288,8 +289,9 @@ typedef struct {
  *   Result.  out = sum_j p_j v_j, p = softmax of scale * q.k over the visible
  *     keys, statistics and sums in f32, the result rounded once to bf16.  A row
  *     that sees nothing, or whose visible scores are all -inf, gives zeros.
- *     Values at positions that no query of the request sees never reach a result,
- *     NaN and infinities included.
+ *     Cached values that no query of the call sees never reach a result, NaN and
+ *     infinities included.  (A non-finite value that some query of a prefill or
+ *     prefix call sees may reach others that are computed with it.)
  *   Requests.  slots: device int32 [B], the slot of each request (NULL: request
  *     b owns slot b).  lens: device int32 [B], its own keys in the cache,
  *     0 <= lens[b] <= capacity.  A request with a slot, length or prefix id
@@ -297,6 +299,7 @@ typedef struct {
  *   Prefixes.  prefix_slots, prefix_lens: device int32 [P], the slot that holds
  *     each prefix and its length (<= capacity); prefix_ids: device int32 [B],
  *     each in [-1, P), -1 for none.  All three NULL (P == 0): no prefixes.
+ *     P <= BITDELTA_MAX_PREFIXES.
  *   q         : device bf16, row t starts at q + t * q_stride elements and holds
  *               q_heads * head_dim contiguous values; q_stride a multiple of 8.
  *   out       : device bf16 [rows, q_heads, head_dim], contiguous.

@@ -7,8 +7,9 @@ import math
 
 import torch
 
-# A bf16 value has 8 significant bits: rounding to nearest is off by at most 2^-9 of it.
-BF16 = 2.0 ** -9
+# A bf16 value has 8 significant bits: neighbours are 2^-7 of a power of two apart, and
+# rounding to nearest is off by at most 2^-8 of the value.
+BF16 = 2.0 ** -8
 F32 = 2.0 ** -24
 
 
@@ -21,13 +22,15 @@ def visible(pos, t, window, sinks):
 
 
 def attention(q, k, v, lens, *, slots=None, cu_q=None, window=0, sinks=0, scale=None, prefix_ids=None,
-              prefix_slots=None, prefix_lens=None):
+              prefix_slots=None, prefix_lens=None, rounded=None):
     """(out, bound, weights): out f64 [rows, q_heads, d]; `bound` what each value
     may be off by; weights {b: f64 [kv_heads, len]} summed over the rows."""
     T, Hq, D = q.shape
     Hk = k.shape[2]
     G = Hq // Hk
     scale = D ** -0.5 if scale is None else scale
+    # prefill and prefixes multiply probabilities rounded to bf16, decode nearly exact ones
+    rounded = cu_q is not None or prefix_ids is not None if rounded is None else rounded
     out = torch.zeros(T, Hq, D, dtype=torch.float64, device=q.device)
     bound = torch.zeros_like(out)
     weights, weight_rel = {}, {}
@@ -61,12 +64,12 @@ def attention(q, k, v, lens, *, slots=None, cu_q=None, window=0, sinks=0, scale=
             p = torch.where(l > 0, e / l, 0.0)
             out[r0:r1, h * G:(h + 1) * G] = torch.einsum("rgn,nd->rgd", p, vv[:, h])
             amount = torch.einsum("rgn,nd->rgd", p, vv[:, h].abs())
-            # One rounding of p and one of the result to bf16.  In f32: a product sum of D
+            # One rounding of the result to bf16, and where p is rounded one of each p.  In f32: a product sum of D
             # terms is off by (D + 2) 2^-24 of its terms' sizes, which exp() turns into a
             # relative error of p -- of the score's and of the sum's, hence twice -- and a
             # few more roundings: the exponential, the sum, the division.
             rel = 2 * (D + 2) * F32 * float((size * mask[:, None]).amax()) + 64 * F32
-            bound[r0:r1, h * G:(h + 1) * G] = (2 * BF16 * (1 + BF16) + 4 * rel) * amount
+            bound[r0:r1, h * G:(h + 1) * G] = ((2 if rounded else 1) * BF16 * (1 + BF16 / 2) + 4 * rel) * amount
             weights[b][h] = p.sum((0, 1))[P:]
             weight_rel[b] = max(weight_rel.get(b, 0.0), 2 * rel)
     return out, bound, (weights, weight_rel)
