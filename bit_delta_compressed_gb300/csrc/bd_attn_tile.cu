@@ -4,14 +4,15 @@
 // A unit is up to 256 query rows on one key/value head: the rows are (token,
 // query head of the group) pairs, so that a group's heads read their keys once.
 // 4 head_dim flops a row and key against 4 head_dim bytes a key: with 256 rows
-// the tensor cores bound it.  One block a SM: one warp loads keys and values
-// by TMA through a ring, one thread issues the tcgen05 products, two groups of four
-// warps own 128 rows each, one thread a row.  Tensor memory holds the scores of
-// both groups (2 x 128 columns) and both outputs (2 x head_dim).  Per block of
-// 128 keys: S = Q K^T (both operands in shared memory), the row's thread takes its
-// 128 scores to registers, keeps the running maximum and sum, writes P as bf16
-// over the scores, and O += P V runs with P from tensor memory.  While one group
-// works on its softmax the products of the other run.
+// the tensor cores bound it.  One block a SM: one warp loads keys and values by TMA
+// through two rings, two threads issue the tcgen05 products, two groups of four warps
+// own 128 rows each, one thread a row.  Per block of 128 keys and group: S = Q K^T
+// (both operands in shared memory); the row's thread takes its 128 scores to
+// registers, keeps the running maximum and sum, and writes P as bf16 to tensor memory,
+// from where O += P V reads it.  Tensor memory: one S (128 columns) that both groups
+// take turns in -- it is free again as soon as it is in registers, so the next scores
+// never wait for a softmax or for the product before -- P (64) and O (head_dim) of
+// each group.  While one group works on its softmax the products of the other run.
 // The output is only rescaled when a row's maximum has grown by more than 2^8
 // since the last time; P is then at most 2^8 and rounds no worse.
 //
@@ -22,6 +23,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bd_attn_math.cuh"
 #include "bd_sm100.cuh"
@@ -47,8 +49,8 @@ template <int D>
 struct Tile {
     static constexpr int kHalves = D / 64;                 // 128-byte wide parts of a row
     static constexpr int kQ = 128 * D * 2;                 // bytes of 128 rows
-    static constexpr int kStages = D == 128 ? 5 : 8;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kQ;
+    static constexpr int kK = D == 128 ? 3 : 4, kV = D == 128 ? 2 : 4;   // stages
+    static constexpr int kSmem = 1024 + (2 + kK + kV) * kQ;
 };
 
 // Blocks [0, head) and [from, from + tail) of a source.
@@ -282,6 +284,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
+// Two floats in a register pair, and the operations on both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float first_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float second_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Shared-memory descriptor of a 16-key slice of V: rows of 64 head_dim values
 // (128 bytes, 128-byte swizzle), the reduction running over rows: groups of 8 rows
 // are 1024 bytes apart, the second 64 values of a row 128 rows further.
@@ -344,19 +370,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const Args a, const TilePlan plan, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const MapOrder order, int split) {
     using T = Tile<D>;
-    constexpr int NS = T::kStages;
+    constexpr int NK = T::kK, NV = T::kV;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t kv_full[NS], kv_empty[NS], q_full[2], s_full[2], p_full[2], pv_done[2], drained;
+    __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[2], s_full[2], s_free, p_full[2],
+        pv_done[2], drained[2];
     __shared__ uint32_t tmem_at;
     __shared__ int start[2];
     __shared__ int64_t line_at[2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
+    // All lanes poll: of a complete phase that costs ~100 cycles, one lane's poll handed
+    // on by a shuffle ~260.
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         return mbar_wait(bar, parity & 1, kLimit, status, where, status + 2);
     };
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
-    const uint32_t q_at = base, ring = base + 2 * T::kQ;
+    const uint32_t q_at = base, k_at = base + 2 * T::kQ, v_at = k_at + NK * T::kQ;
 
     const PlanHead head = *plan.head;
     Walk walk{};
@@ -390,17 +419,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 8) tmem_alloc(&tmem_at, 512);
     if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(kv_full + i, 1);
-            mbar_init(kv_empty + i, 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 1);
         }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 1);
+        }
+        mbar_init(&s_free, 4);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 128);
+            mbar_init(q_full + i, 4);
             mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 128);
+            mbar_init(p_full + i, 4);
             mbar_init(pv_done + i, 1);
+            mbar_init(drained + i, 1);
         }
-        mbar_init(&drained, 1);
         fence_mbar_init();
     }
     tc_fence_before();
@@ -409,114 +443,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = tmem_at;
 
     // registers: 3 x 168 for each lane of the three warp groups at launch; the loading
-    // and issuing group gives 48 of its own to each of the others, whose threads keep
+    // and issuing group gives 32 of its own to each of the others, whose threads keep
     // a row's 128 scores
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8 && lane == 0) {
-            // keys and values: stage 2 i holds the keys of the i-th block, stage 2 i + 1 its values
-            prefetch_tensormap(&kmap);
-            prefetch_tensormap(&vmap);
-            int put = 0;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if ((warp == 8 || warp == 11) && lane == 0) {
+            // keys (warp 8) and values (warp 11)
+            const bool keys = warp == 8;
+            const CUtensorMap* map = keys ? &kmap : &vmap;
+            uint64_t *full = keys ? k_full : v_full, *empty = keys ? k_empty : v_empty;
+            const int stages = keys ? NK : NV;
+            const uint32_t to = keys ? k_at : v_at;
+            prefetch_tensormap(map);
+            int st = 0, put = 0;
+            uint32_t phase = 1;                    // of the fill before the one to come
             bool ok = true;
             Segment s;
             while (ok && walk.next(a, plan, s)) {
                 const RowTile t = plan.tiles[s.tile];
-                for (int i = s.first; ok && i < s.last; ++i) {
+                for (int i = s.first; i < s.last; ++i, ++put) {
                     const Block b = block_of(t, i);
                     auto at = [&](int dim) { return dim == order.token ? b.key : dim == order.head ? s.hk : b.slot; };
-                    for (int kv = 0; ok && kv < 2; ++kv, ++put) {
-                        const int st = put % NS;
-                        if (put >= NS) ok = wait(kv_empty + st, put / NS - 1, 1);
-                        if (!ok) break;
-                        mbar_expect_tx(kv_full + st, T::kQ);
-                        for (int h = 0; h < T::kHalves; ++h)
-                            tma_load_4d(ring + st * T::kQ + h * kKeys * 128, kv ? &vmap : &kmap, kv_full + st, h * 64, at(0), at(1), at(2));
+                    if (put >= stages) ok = wait(empty + st, phase, 1);
+                    if (!ok) break;
+                    mbar_expect_tx(full + st, T::kQ);
+                    for (int h = 0; h < T::kHalves; ++h)
+                        tma_load_4d(to + st * T::kQ + h * kKeys * 128, map, full + st, h * 64, at(0), at(1), at(2));
+                    if (++st == stages) {
+                        st = 0;
+                        phase ^= 1;
                     }
                 }
             }
             // nothing may still be on its way into shared memory when the block ends
-            for (int i = max(0, put - NS); i < put; ++i) wait(kv_full + i % NS, i / NS, 2);
+            for (int i = max(0, put - stages); i < put; ++i) wait(full + i % stages, i / stages, 3);
         }
-        if (warp == 9 && lane == 0) {
-            const uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
-            int steps[2] = {0, 0}, segs[2] = {0, 0};
+        // Two warps issue the products, one the scores' and one the outputs': the waits of
+        // one overlap the other's.  (A product's issue takes as long as the product, 64
+        // cycles for 128 x 128 x 16.)
+        constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
+        if (warp == 9) {
+            const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
+            uint32_t st = 0, phase = 0, n = 0, begun0 = 0, begun1 = 0;
             bool ok = true;
-            auto scores = [&](int g, int st, bool fresh) {      // S of group g from the keys in stage st
-                if (fresh) ok = ok && wait(q_full + g, segs[g]++, 3);
-                // P of the block before lies where S goes
-                if (steps[g] > 0) ok = ok && wait(pv_done + g, steps[g] - 1, 4);
-                if (!ok) return;
-                tc_fence_after();
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * (kKeys * 128) + (k % 4) * 32;
-                    mma_ss(tmem + g * 128, desc_sw128(q_at + g * T::kQ + off), desc_sw128(ring + st * T::kQ + off), idesc_s, k > 0);
-                }
-                mma_commit(s_full + g);
-            };
-            auto values = [&](int g, int st, bool first) {      // O of group g += P V, the values in stage st
-                ok = ok && wait(p_full + g, steps[g]++, 5);
-                if (!ok) return;
-                tc_fence_after();
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tmem + 256 + g * D, tmem + g * 128 + k * 8, desc_v(ring + st * T::kQ + k * 2048), idesc_o, !first || k > 0);
-                mma_commit(pv_done + g);
-            };
-            Segment s, next;
-            int got = 0;
-            bool more = walk.next(a, plan, s);
-            int groups = more && plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
-            int i = s.first;
-            if (more) {
-                ok = wait(kv_full, 0, 6);
-                for (int g = 0; ok && g < groups; ++g) scores(g, 0, true);
-                if (ok) mma_commit(kv_empty);
-            }
-            while (ok && more) {
-                const bool same = i + 1 < s.last;
-                bool has_next = same;
-                next = s;
-                int next_groups = groups;
-                if (!same) {
-                    has_next = walk.next(a, plan, next);
-                    if (has_next) next_groups = plan.tiles[next.tile].tokens * a.G > 128 ? 2 : 1;
-                }
-                const int kst = (got + 2) % NS, vst = (got + 1) % NS;
-                const bool first = i == s.first;
-                ok = wait(kv_full + vst, (got + 1) / NS, 7);
-                if (ok && has_next) ok = wait(kv_full + kst, (got + 2) / NS, 8);
-                if (!ok) break;
-                if (same) {
-                    values(0, vst, first);
-                    scores(0, kst, false);
-                    if (groups == 2) values(1, vst, first);
-                    mma_commit(kv_empty + vst);
-                    if (groups == 2) scores(1, kst, false);
-                    mma_commit(kv_empty + kst);
-                } else {
-                    for (int g = 0; g < groups; ++g) values(g, vst, first);
-                    mma_commit(kv_empty + vst);
-                    if (has_next) {
-                        for (int g = 0; g < next_groups; ++g) scores(g, kst, true);
-                        mma_commit(kv_empty + kst);
+            Segment s;
+            while (ok && walk.next(a, plan, s)) {
+                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+                for (int i = s.first; ok && i < s.last; ++i) {
+                    ok = wait(k_full + st, phase, 4);
+                    for (int g = 0; ok && g < groups; ++g) {
+                        if (i == s.first) ok = wait(q_full + g, g ? begun1++ : begun0++, 5);
+                        // the scores before, of whichever group, are in registers
+                        if (n > 0) ok = ok && wait(&s_free, n - 1, 6);
+                        if (!ok) break;
+                        ++n;
+                        tc_fence_after();
+                        const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (st * T::kQ >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+                                mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
+                            }
+                            mma_commit(s_full + g);
+                            if (g == groups - 1) mma_commit(k_empty + st);
+                        }
+                        __syncwarp();
+                    }
+                    if (++st == NK) {
+                        st = 0;
+                        phase ^= 1;
                     }
                 }
-                more = has_next;
-                i = same ? i + 1 : next.first;
-                s = next;
-                groups = next_groups;
-                got += 2;
             }
             // the products in flight end before the tensor memory is given back
-            mma_commit(&drained);
-            wait(&drained, 0, 9);
+            if (elect_one()) mma_commit(drained);
+            __syncwarp();
+            wait(drained, 0, 7);
+        }
+        if (warp == 10) {
+            const uint64_t v_desc = desc_v(v_at);
+            uint32_t st = 0, phase = 0, done0 = 0, done1 = 0;
+            bool ok = true;
+            Segment s;
+            while (ok && walk.next(a, plan, s)) {
+                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+                for (int i = s.first; ok && i < s.last; ++i) {
+                    ok = wait(v_full + st, phase, 8);
+                    for (int g = 0; ok && g < groups; ++g) {
+                        ok = wait(p_full + g, g ? done1++ : done0++, 9);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + (st * T::kQ >> 4);
+                        const uint32_t o = tmem + 256 + g * D, p = tmem + 128 + g * 64;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(o, p + k * 8, vd + (k * 2048 >> 4), idesc_o, i > s.first || k > 0);
+                            mma_commit(pv_done + g);
+                            if (g == groups - 1) mma_commit(v_empty + st);
+                        }
+                        __syncwarp();
+                    }
+                    if (++st == NV) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (elect_one()) mma_commit(drained + 1);
+            __syncwarp();
+            wait(drained + 1, 0, 10);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // a group of 128 rows, one thread a row
         const int g = warp / 4, r = g * 128 + tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + g * 128, o_at = tmem + lanes + 256 + g * D;
+        const uint32_t s_at = tmem + lanes, p_at = s_at + 128 + g * 64, o_at = s_at + 256 + g * D;
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         const float scale = fmaxf(fabsf(a.scale_log2), 1.2e-38f);   // never 0: a hidden score's -inf stays -inf
         int step = 0, put = 0;
@@ -526,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const RowTile t = plan.tiles[s.tile];
             const int blocks = s.last - s.first;
             if (g == 1 && t.tokens * a.G <= 128) {
-                put += 2 * blocks;
+                put += blocks;
                 continue;
             }
             // this row's token, head and visible range
@@ -561,39 +605,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(q_full + g);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + g);
 
             float m = -INFINITY, l = 0.f;
-            for (int i = s.first; i < s.last; ++i, ++step, put += 2) {
+            for (int i = s.first; i < s.last; ++i, ++step, ++put) {
                 const Block b = block_of(t, i);
-                if (g == 0) {
-                    // values that no row of the unit sees may be anything: they are
-                    // multiplied by zero, so they have to be finite
-                    const int key = b.key + tid;
-                    const int pos = b.off + key;
-                    const bool seen = key < b.end && (pos < a.sinks || pos >= t.lo_min);
-                    const bool whole = b.key + kKeys <= b.end && (b.off + b.key + kKeys <= a.sinks || b.off + b.key >= t.lo_min);
-                    if (!whole) {
-                        const int st = (put + 1) % NS;
-                        ok = wait(kv_full + st, (put + 1) / NS, 10);
-                        if (!seen)
-#pragma unroll
-                            for (int c = 0; c < D / 8; ++c)
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ring + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
-                                             : "memory");
-                        fence_proxy_async_smem();
-                    }
-                }
-                ok = ok && wait(s_full + g, step, 11);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, wait(s_full + g, step, 11));
+                if (!ok) break;
                 tc_fence_after();
                 float v[kKeys];
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) tmem_ld32(s_at + c, v + c);
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free);
                 const int p0 = b.off + b.key;
                 const int end = min(hi, b.off + b.end);
                 if (!(p0 + kKeys <= end && (p0 >= lo || p0 + kKeys <= a.sinks))) {
@@ -602,25 +629,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kKeys; ++c)
                         v[c] = c < n && (c < sinks || c >= from) ? v[c] : -INFINITY;
                 }
-                float top[4] = {v[0], v[1], v[2], v[3]};
+                float top[4];
 #pragma unroll
-                for (int c = 4; c < kKeys; c += 4)
+                for (int e = 0; e < 4; ++e) {
+                    top[e] = fmaxf(v[e], v[4 + e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], v[c + e]);
-                const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int c = 8; c < kKeys; c += 8) top[e] = max3(top[e], v[c + e], v[c + 4 + e]);
+                }
+                const float mx = max3(top[0], top[1], fmaxf(top[2], top[3]));
                 const float mn = fmaxf(m, mx == -INFINITY ? -INFINITY : mx * scale);
-                const bool grows = mn > m + kGrow || m == -INFINITY;
+                const bool grows = mn > m + kGrow || (m == -INFINITY && mn > m);
+                // P and O are free when the block before is done
+                if (step > 0) ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 12));
+                if (!ok) break;
+                tc_fence_after();
+                if (g == 0) {
+                    // values that no row of the unit sees may be anything: they are
+                    // multiplied by zero, so they have to be finite.  (The first group
+                    // has a part in every unit and its product comes first.)
+                    const int key = b.key + tid;
+                    const int pos = b.off + key;
+                    const bool seen = key < b.end && (pos < a.sinks || pos >= t.lo_min);
+                    const bool whole = b.key + kKeys <= b.end && (b.off + b.key + kKeys <= a.sinks || b.off + b.key >= t.lo_min);
+                    if (!whole) {
+                        const int st = put % NV;
+                        ok = __all_sync(0xffffffffu, wait(v_full + st, put / NV, 13));
+                        if (!ok) break;
+                        if (!seen)
+#pragma unroll
+                            for (int c = 0; c < D / 8; ++c)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
+                                             : "memory");
+                        fence_proxy_async_smem();
+                    }
+                }
                 if (i == s.first) {
                     m = mn;
-                } else if (__any_sync(0xffffffffu, grows && mn > m)) {
+                } else if (__any_sync(0xffffffffu, grows)) {
                     float f = 1.f;
-                    if (grows && mn > m) {
+                    if (grows) {
                         f = exp2_approx(m - mn);
                         m = mn;
                         l *= f;
                     }
-                    ok = wait(pv_done + g, step - 1, 12);
-                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D; c += 16) {
                         uint32_t o[16];
@@ -632,27 +683,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float use = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t scale2 = pair(scale, scale), use2 = pair(-use, -use);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 32) {
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float x = exp2_approx(fmaf(v[c + e], scale, -use)), y = exp2_approx(fmaf(v[c + e + 1], scale, -use));
-                        sum[e % 4] += x;
-                        sum[e % 4 + 1] += y;
-                        p[e / 2] = pack_bf16(x, y);
+                        const uint64_t x = fma2(pair(v[c + e], v[c + e + 1]), scale2, use2);
+                        const float y0 = exp2_approx(first_of(x)), y1 = exp2_approx(second_of(x));
+                        sum[e / 2 % 2] = add2(sum[e / 2 % 2], pair(y0, y1));
+                        p[e / 2] = pack_bf16(y0, y1);
                     }
-                    tmem_st16(s_at + c / 2, p);
+                    tmem_st16(p_at + c / 2, p);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += first_of(sum[0]) + second_of(sum[0]);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(p_full + g);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + g);
             }
-            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 13));
+            ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 14));
             if (!ok) break;
             tc_fence_after();
             const float inv = inverse(l);
