@@ -4,8 +4,8 @@
 // A unit is up to 256 query rows on one key/value head: the rows are (token,
 // query head of the group) pairs, so that a group's heads read their keys once.
 // 4 head_dim flops a row and key against 4 head_dim bytes a key: with 256 rows
-// the tensor cores bound it.  One block a SM: one warp loads keys and values by TMA
-// through two rings, two threads issue the tcgen05 products, two groups of four warps
+// the tensor cores bound it.  One block a SM: two warps load keys and values by TMA
+// through two rings, one issues the tcgen05 products, two groups of four warps
 // own 128 rows each, one thread a row.  Per block of 128 keys and group: S = Q K^T
 // (both operands in shared memory); the row's thread takes its 128 scores to
 // registers, keeps the running maximum and sum, and writes P as bf16 to tensor memory,
@@ -284,6 +284,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
+// Whether a phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The n lowest bits of a word (none below 0, all from 32).
+__device__ __forceinline__ uint32_t first_bits(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;
+}
+
 // Two floats in a register pair, and the operations on both at once.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t r;
@@ -351,7 +369,7 @@ struct Walk {
 
 // Block i of a row tile: its source, first key and the source's end.
 struct Block {
-    int src, slot, key, end, off;
+    int src, slot, key, end, off, run;       // run: blocks from this one on that follow one another
 };
 __device__ __forceinline__ Block block_of(const RowTile& t, int i) {
     Block b;
@@ -360,9 +378,35 @@ __device__ __forceinline__ Block block_of(const RowTile& t, int i) {
     const int head = b.src ? t.head[1] : t.head[0], from = b.src ? t.from[1] : t.from[0];
     b.key = (i < head ? i : from + i - head) * kKeys;
     b.slot = b.src ? t.slot[1] : t.slot[0];
+    b.run = i < head ? head - i : head + (b.src ? t.tail[1] : t.tail[0]) - i;
+    if (b.run < 1) b.run = 1;
     b.off = b.src ? t.off : 0;
     b.end = b.src ? t.own_hi : t.off;
     return b;
+}
+
+// A thread's row of a unit: its row of q (-1: none), its head and the positions
+// [lo, hi) that it sees; a row that is none sees all.
+struct RowOf {
+    int row, head, lo, hi;
+    int lo_unit;                               // the least lo of the unit's rows
+    int skipped;                               // blocks of units before it without a part of its group
+};
+__device__ __forceinline__ RowOf row_of(const Args& a, const TilePlan& plan, const RowTile& t, int hk, int r) {
+    RowOf o{-1, hk * a.G, 0, 0x7fffffff, t.lo_min, 0};
+    const int token = r / a.G;
+    if (token >= t.tokens) return o;
+    o.head += r - token * a.G;
+    o.row = t.row0 + token;
+    int pos = t.t0 + token;
+    if (!a.cu_q) {
+        o.row = plan.order[o.row];
+        const Request rq = read_request(a, o.row);
+        pos = rq.plen + rq.len - 1;
+    }
+    o.hi = pos + 1;
+    o.lo = window_lo(a, pos);
+    return o;
 }
 
 template <int D>
@@ -373,15 +417,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NK = T::kK, NV = T::kV;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[2], s_full[2], s_free, p_full[2],
-        pv_done[2], drained[2];
+        pv_done[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ int start[2];
     __shared__ int64_t line_at[2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
-    // All lanes poll: of a complete phase that costs ~100 cycles, one lane's poll handed
-    // on by a shuffle ~260.
+    // Waits of a whole warp.  All lanes poll (a complete phase costs ~100 cycles so, one
+    // lane's poll handed on by a shuffle ~260); two phases are asked for at once.
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
+        return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity & 1, kLimit, status, where, status + 2));
+    };
+    auto wait2 = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2, unsigned where) {
+        const bool one = mbar_test(bar, parity & 1), other = mbar_test(bar2, parity2 & 1);
+        if (__all_sync(0xffffffffu, one && other)) return true;
+        return wait(bar, parity, where) && wait(bar2, parity2, where + 32);
+    };
+    auto lane_wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         return mbar_wait(bar, parity & 1, kLimit, status, where, status + 2);
     };
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
@@ -428,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_empty + i, 1);
         }
         mbar_init(&s_free, 4);
+        mbar_init(&drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 4);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
             mbar_init(pv_done + i, 1);
-            mbar_init(drained + i, 1);
         }
         fence_mbar_init();
     }
@@ -464,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = s.first; i < s.last; ++i, ++put) {
                     const Block b = block_of(t, i);
                     auto at = [&](int dim) { return dim == order.token ? b.key : dim == order.head ? s.hk : b.slot; };
-                    if (put >= stages) ok = wait(empty + st, phase, 1);
+                    if (put >= stages) ok = lane_wait(empty + st, phase, 1);
                     if (!ok) break;
                     mbar_expect_tx(full + st, T::kQ);
                     for (int h = 0; h < T::kHalves; ++h)
@@ -476,84 +529,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // nothing may still be on its way into shared memory when the block ends
-            for (int i = max(0, put - stages); i < put; ++i) wait(full + i % stages, i / stages, 3);
+            for (int i = max(0, put - stages); i < put; ++i) lane_wait(full + i % stages, i / stages, 3);
         }
-        // Two warps issue the products, one the scores' and one the outputs': the waits of
-        // one overlap the other's.  (A product's issue takes as long as the product, 64
-        // cycles for 128 x 128 x 16.)
-        constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
         if (warp == 9) {
-            const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
-            uint32_t st = 0, phase = 0, n = 0, begun0 = 0, begun1 = 0;
+            // One warp issues all products, in the order scores 0 of block i + 1, output 0
+            // of block i, scores 1, output 1: a product's issue takes as long as the product
+            // (64 cycles for 128 x 128 x 16), and while an output's runs, the scores before
+            // it reach the registers of their group and leave their place to the next.
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
+            const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at), v_desc = desc_v(v_at);
+            uint32_t ks = 0, k_phase = 0, vs = 0, v_phase = 0, n = 0;
+            uint32_t begun[2] = {0, 0}, done[2] = {0, 0};
             bool ok = true;
+            auto scores = [&](auto group, bool fresh, bool last) {
+                constexpr int g = decltype(group)::value;
+                if (fresh) ok = ok && wait(q_full + g, begun[g]++, 5);
+                // the keys; the scores before, of whichever group, are in registers
+                ok = ok && (n > 0 ? wait2(k_full + ks, k_phase, &s_free, n - 1, 4) : wait(k_full + ks, k_phase, 4));
+                if (!ok) return;
+                ++n;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (ks * T::kQ >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+                        mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
+                    }
+                    mma_commit(s_full + g);
+                    if (last) mma_commit(k_empty + ks);
+                }
+                __syncwarp();
+            };
+            auto output = [&](auto group, bool first, bool last) {
+                constexpr int g = decltype(group)::value;
+                ok = ok && wait2(v_full + vs, v_phase, p_full + g, done[g]++, 8);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t vd = v_desc + (vs * T::kQ >> 4);
+                    const uint32_t o = tmem + 256 + g * D, p = tmem + 128 + g * 64;
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(o, p + k * 8, vd + (k * 2048 >> 4), idesc_o, !first || k > 0);
+                    mma_commit(pv_done + g);
+                    if (last) mma_commit(v_empty + vs);
+                }
+                __syncwarp();
+            };
+            auto next_keys = [&]() {
+                if (++ks == NK) {
+                    ks = 0;
+                    k_phase ^= 1;
+                }
+            };
+            constexpr std::integral_constant<int, 0> g0{};
+            constexpr std::integral_constant<int, 1> g1{};
             Segment s;
             while (ok && walk.next(a, plan, s)) {
-                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+                const bool two = plan.tiles[s.tile].tokens * a.G > 128;
+                scores(g0, true, !two);
+                if (two) scores(g1, true, true);
+                next_keys();
                 for (int i = s.first; ok && i < s.last; ++i) {
-                    ok = wait(k_full + st, phase, 4);
-                    for (int g = 0; ok && g < groups; ++g) {
-                        if (i == s.first) ok = wait(q_full + g, g ? begun1++ : begun0++, 5);
-                        // the scores before, of whichever group, are in registers
-                        if (n > 0) ok = ok && wait(&s_free, n - 1, 6);
-                        if (!ok) break;
-                        ++n;
-                        tc_fence_after();
-                        const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (st * T::kQ >> 4);
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
-                                mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
-                            }
-                            mma_commit(s_full + g);
-                            if (g == groups - 1) mma_commit(k_empty + st);
-                        }
-                        __syncwarp();
+                    const bool more = i + 1 < s.last, first = i == s.first;
+                    if (more) scores(g0, false, !two);
+                    output(g0, first, !two);
+                    if (two) {
+                        if (more) scores(g1, false, true);
+                        output(g1, first, true);
                     }
-                    if (++st == NK) {
-                        st = 0;
-                        phase ^= 1;
+                    if (more) next_keys();
+                    if (++vs == NV) {
+                        vs = 0;
+                        v_phase ^= 1;
                     }
                 }
             }
             // the products in flight end before the tensor memory is given back
-            if (elect_one()) mma_commit(drained);
+            if (elect_one()) mma_commit(&drained);
             __syncwarp();
-            wait(drained, 0, 7);
-        }
-        if (warp == 10) {
-            const uint64_t v_desc = desc_v(v_at);
-            uint32_t st = 0, phase = 0, done0 = 0, done1 = 0;
-            bool ok = true;
-            Segment s;
-            while (ok && walk.next(a, plan, s)) {
-                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
-                for (int i = s.first; ok && i < s.last; ++i) {
-                    ok = wait(v_full + st, phase, 8);
-                    for (int g = 0; ok && g < groups; ++g) {
-                        ok = wait(p_full + g, g ? done1++ : done0++, 9);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + (st * T::kQ >> 4);
-                        const uint32_t o = tmem + 256 + g * D, p = tmem + 128 + g * 64;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                mma_ts(o, p + k * 8, vd + (k * 2048 >> 4), idesc_o, i > s.first || k > 0);
-                            mma_commit(pv_done + g);
-                            if (g == groups - 1) mma_commit(v_empty + st);
-                        }
-                        __syncwarp();
-                    }
-                    if (++st == NV) {
-                        st = 0;
-                        phase ^= 1;
-                    }
-                }
-            }
-            if (elect_one()) mma_commit(drained + 1);
-            __syncwarp();
-            wait(drained + 1, 0, 10);
+            wait(&drained, 0, 7);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -564,54 +620,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         const float scale = fmaxf(fabsf(a.scale_log2), 1.2e-38f);   // never 0: a hidden score's -inf stays -inf
         int step = 0, put = 0;
-        bool ok = true;
-        Segment s;
-        while (ok && walk.next(a, plan, s)) {
-            const RowTile t = plan.tiles[s.tile];
-            const int blocks = s.last - s.first;
-            if (g == 1 && t.tokens * a.G <= 128) {
-                put += blocks;
-                continue;
-            }
-            // this row's token, head and visible range
-            const int token = r / a.G;
-            const bool real = token < t.tokens;
-            int row = 0, hi = 0, lo = 0;
-            if (real) {
-                row = t.row0 + token;
-                int pos = t.t0 + token;
-                if (!a.cu_q) {
-                    row = plan.order[row];
-                    const Request rq = read_request(a, row);
-                    pos = rq.plen + rq.len - 1;
+        bool ok = true, more = true;
+        Segment s, coming;
+        RowOf now{}, next{};
+        // this thread's row of the next unit that its group has a part in: its query
+        // goes to shared memory, where the products read it
+        auto begin_next = [&]() {
+            while ((more = walk.next(a, plan, coming))) {
+                const RowTile& t = plan.tiles[coming.tile];
+                const int tokens = t.tokens;
+                if (g == 0 || tokens * a.G > 128) {
+                    const int skipped = next.skipped;
+                    next = row_of(a, plan, t, coming.hk, r);
+                    next.skipped = skipped;
+                    break;
                 }
-                hi = pos + 1;
-                lo = window_lo(a, pos);
+                next.skipped += coming.last - coming.first;
             }
-            const int head_at = s.hk * a.G + r - token * a.G;
-            {
-                const uint4* from = reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.q_stride + (int64_t)head_at * D);
-                const uint32_t to = q_at + g * T::kQ + (tid % 128) * 128;
+            if (!more) return;
+            const uint4* from = reinterpret_cast<const uint4*>(a.q + (int64_t)max(next.row, 0) * a.q_stride + (int64_t)next.head * D);
+            const uint32_t to = q_at + g * T::kQ + (tid % 128) * 128;
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = real ? from[c] : make_uint4(0, 0, 0, 0);
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + (c / 8) * (kKeys * 128) + (((c % 8) ^ (tid % 8)) << 4)),
-                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
-                }
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = next.row >= 0 ? from[c] : make_uint4(0, 0, 0, 0);
+                v.x ^= flip;
+                v.y ^= flip;
+                v.z ^= flip;
+                v.w ^= flip;
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + (c / 8) * (kKeys * 128) + (((c % 8) ^ (tid % 8)) << 4)),
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + g);
-
+        };
+        begin_next();
+        while (more) {
+            s = coming;
+            now = next;
+            next.skipped = 0;
+            put += now.skipped;
+            // the warp's rows all see [lo_all, hi_all)
+            const int hi_all = __reduce_min_sync(0xffffffffu, now.hi), lo_all = __reduce_max_sync(0xffffffffu, now.lo);
             float m = -INFINITY, l = 0.f;
+            int p0 = 0, src_end = 0, run = 0;      // the block's first position, its source's end, blocks until another source or a gap
             for (int i = s.first; i < s.last; ++i, ++step, ++put) {
-                const Block b = block_of(t, i);
-                ok = __all_sync(0xffffffffu, wait(s_full + g, step, 11));
+                if (run == 0) {
+                    const RowTile t = plan.tiles[s.tile];
+                    const Block b = block_of(t, i);
+                    p0 = b.off + b.key;
+                    src_end = b.off + b.end;
+                    run = b.run;
+                }
+                ok = wait(s_full + g, step, 11);
                 if (!ok) break;
                 tc_fence_after();
                 float v[kKeys];
@@ -621,13 +683,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free);
-                const int p0 = b.off + b.key;
-                const int end = min(hi, b.off + b.end);
-                if (!(p0 + kKeys <= end && (p0 >= lo || p0 + kKeys <= a.sinks))) {
-                    const int n = end - p0, from = lo - p0, sinks = a.sinks - p0;
+                // asked now, needed later: P and O are free when the block before is done
+                const bool free = step == 0 || mbar_test(pv_done + g, (step - 1) & 1);
+                if (!(p0 + kKeys <= min(src_end, hi_all) && (p0 >= lo_all || p0 + kKeys <= a.sinks))) {
+                    const int n = min(now.hi, src_end) - p0, from = now.lo - p0, sinks = a.sinks - p0;
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        v[c] = c < n && (c < sinks || c >= from) ? v[c] : -INFINITY;
+                    for (int c = 0; c < kKeys; c += 32) {
+                        uint32_t seen = first_bits(n - c) & (first_bits(sinks - c) | ~first_bits(from - c));
+                        // (opaque, or the compiler evaluates the masks of all blocks)
+                        asm volatile("" : "+r"(seen));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[c + e] = seen >> e & 1 ? v[c + e] : -INFINITY;
+                    }
                 }
                 float top[4];
 #pragma unroll
@@ -639,29 +706,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mx = max3(top[0], top[1], fmaxf(top[2], top[3]));
                 const float mn = fmaxf(m, mx == -INFINITY ? -INFINITY : mx * scale);
                 const bool grows = mn > m + kGrow || (m == -INFINITY && mn > m);
-                // P and O are free when the block before is done
-                if (step > 0) ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 12));
+                ok = __all_sync(0xffffffffu, free) || wait(pv_done + g, step - 1, 12);
                 if (!ok) break;
                 tc_fence_after();
-                if (g == 0) {
+                if (g == 0 && !(p0 + kKeys <= src_end && (p0 >= now.lo_unit || p0 + kKeys <= a.sinks))) {
                     // values that no row of the unit sees may be anything: they are
                     // multiplied by zero, so they have to be finite.  (The first group
                     // has a part in every unit and its product comes first.)
-                    const int key = b.key + tid;
-                    const int pos = b.off + key;
-                    const bool seen = key < b.end && (pos < a.sinks || pos >= t.lo_min);
-                    const bool whole = b.key + kKeys <= b.end && (b.off + b.key + kKeys <= a.sinks || b.off + b.key >= t.lo_min);
-                    if (!whole) {
-                        const int st = put % NV;
-                        ok = __all_sync(0xffffffffu, wait(v_full + st, put / NV, 13));
-                        if (!ok) break;
-                        if (!seen)
+                    const int pos = p0 + tid, st = put % NV;
+                    ok = wait(v_full + st, put / NV, 13);
+                    if (!ok) break;
+                    if (!(pos < src_end && (pos < a.sinks || pos >= now.lo_unit)))
 #pragma unroll
-                            for (int c = 0; c < D / 8; ++c)
-                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
-                                             : "memory");
-                        fence_proxy_async_smem();
-                    }
+                        for (int c = 0; c < D / 8; ++c)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
+                                         : "memory");
+                    fence_proxy_async_smem();
                 }
                 if (i == s.first) {
                     m = mn;
@@ -703,11 +763,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + g);
+                p0 += kKeys;
+                --run;
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, wait(pv_done + g, step - 1, 14));
+            // the last scores are in registers: the next query may take this one's place
+            begin_next();
+            ok = wait(pv_done + g, step - 1, 14);
             if (!ok) break;
             tc_fence_after();
+            const bool real = now.row >= 0;
+            const int row = now.row, head_at = now.head;
             const float inv = inverse(l);
             const int64_t part_row =
                 split ? plan.unit_row[(int64_t)s.tile * a.Hk + s.hk] + (int64_t)blockIdx.x * kPartRows + r : 0;
