@@ -5,7 +5,7 @@
 // query head of the group) pairs, so that a group's heads read their keys once.
 // 4 head_dim flops a row and key against 4 head_dim bytes a key: with 256 rows
 // the tensor cores bound it.  One block a SM: two warps load keys and values by TMA
-// through two rings, one issues the tcgen05 products, two groups of four warps
+// through two rings, two issue the tcgen05 products, two groups of four warps
 // own 128 rows each, one thread a row.  Per block of 128 keys and group: S = Q K^T
 // (both operands in shared memory); the row's thread takes its 128 scores to
 // registers, keeps the running maximum and sum, and writes P as bf16 to tensor memory,
@@ -23,7 +23,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <type_traits>
 
 #include "bd_attn_math.cuh"
 #include "bd_sm100.cuh"
@@ -417,22 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int NK = T::kK, NV = T::kV;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[2], s_full[2], s_free, p_full[2],
-        pv_done[2], drained;
+        pv_done[2], drained[2];
     __shared__ uint32_t tmem_at;
     __shared__ int start[2];
     __shared__ int64_t line_at[2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
     // Waits of a whole warp.  All lanes poll (a complete phase costs ~100 cycles so, one
-    // lane's poll handed on by a shuffle ~260); two phases are asked for at once.
+    // lane's poll handed on by a shuffle ~260).
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
         return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity & 1, kLimit, status, where, status + 2));
-    };
-    auto wait2 = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2, unsigned where) {
-        const bool one = mbar_test(bar, parity & 1), other = mbar_test(bar2, parity2 & 1);
-        if (__all_sync(0xffffffffu, one && other)) return true;
-        return wait(bar, parity, where) && wait(bar2, parity2, where + 32);
     };
     auto lane_wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         return mbar_wait(bar, parity & 1, kLimit, status, where, status + 2);
@@ -481,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_empty + i, 1);
         }
         mbar_init(&s_free, 4);
-        mbar_init(&drained, 1);
+        mbar_init(drained, 1);
+        mbar_init(drained + 1, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 4);
             mbar_init(s_full + i, 1);
@@ -531,85 +526,83 @@ __global__ void __launch_bounds__(kThreads, 1)
             // nothing may still be on its way into shared memory when the block ends
             for (int i = max(0, put - stages); i < put; ++i) lane_wait(full + i % stages, i / stages, 3);
         }
+        // Two warps issue the products, one the scores' and one the outputs'.  A product's
+        // issue takes as long as the product (64 cycles for 128 x 128 x 16), and the waits
+        // and the bookkeeping between two batches half as long as a batch: so they overlap
+        // the other warp's products.
+        constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
         if (warp == 9) {
-            // One warp issues all products, in the order scores 0 of block i + 1, output 0
-            // of block i, scores 1, output 1: a product's issue takes as long as the product
-            // (64 cycles for 128 x 128 x 16), and while an output's runs, the scores before
-            // it reach the registers of their group and leave their place to the next.
-            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
-            const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at), v_desc = desc_v(v_at);
-            uint32_t ks = 0, k_phase = 0, vs = 0, v_phase = 0, n = 0;
-            uint32_t begun[2] = {0, 0}, done[2] = {0, 0};
+            const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
+            uint32_t st = 0, phase = 0, n = 0, begun0 = 0, begun1 = 0;
             bool ok = true;
-            auto scores = [&](auto group, bool fresh, bool last) {
-                constexpr int g = decltype(group)::value;
-                if (fresh) ok = ok && wait(q_full + g, begun[g]++, 5);
-                // the keys; the scores before, of whichever group, are in registers
-                ok = ok && (n > 0 ? wait2(k_full + ks, k_phase, &s_free, n - 1, 4) : wait(k_full + ks, k_phase, 4));
-                if (!ok) return;
-                ++n;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (ks * T::kQ >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
-                        mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
-                    }
-                    mma_commit(s_full + g);
-                    if (last) mma_commit(k_empty + ks);
-                }
-                __syncwarp();
-            };
-            auto output = [&](auto group, bool first, bool last) {
-                constexpr int g = decltype(group)::value;
-                ok = ok && wait2(v_full + vs, v_phase, p_full + g, done[g]++, 8);
-                if (!ok) return;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t vd = v_desc + (vs * T::kQ >> 4);
-                    const uint32_t o = tmem + 256 + g * D, p = tmem + 128 + g * 64;
-#pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(o, p + k * 8, vd + (k * 2048 >> 4), idesc_o, !first || k > 0);
-                    mma_commit(pv_done + g);
-                    if (last) mma_commit(v_empty + vs);
-                }
-                __syncwarp();
-            };
-            auto next_keys = [&]() {
-                if (++ks == NK) {
-                    ks = 0;
-                    k_phase ^= 1;
-                }
-            };
-            constexpr std::integral_constant<int, 0> g0{};
-            constexpr std::integral_constant<int, 1> g1{};
             Segment s;
             while (ok && walk.next(a, plan, s)) {
-                const bool two = plan.tiles[s.tile].tokens * a.G > 128;
-                scores(g0, true, !two);
-                if (two) scores(g1, true, true);
-                next_keys();
+                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
                 for (int i = s.first; ok && i < s.last; ++i) {
-                    const bool more = i + 1 < s.last, first = i == s.first;
-                    if (more) scores(g0, false, !two);
-                    output(g0, first, !two);
-                    if (two) {
-                        if (more) scores(g1, false, true);
-                        output(g1, first, true);
+                    ok = wait(k_full + st, phase, 4);
+                    for (int g = 0; ok && g < groups; ++g) {
+                        if (i == s.first) ok = wait(q_full + g, g ? begun1++ : begun0++, 5);
+                        // the scores before, of whichever group, are in registers
+                        if (n > 0) ok = ok && wait(&s_free, n - 1, 6);
+                        if (!ok) break;
+                        ++n;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (st * T::kQ >> 4);
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
+                                mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
+                            }
+                            mma_commit(s_full + g);
+                            if (g == groups - 1) mma_commit(k_empty + st);
+                        }
+                        __syncwarp();
                     }
-                    if (more) next_keys();
-                    if (++vs == NV) {
-                        vs = 0;
-                        v_phase ^= 1;
+                    if (++st == NK) {
+                        st = 0;
+                        phase ^= 1;
                     }
                 }
             }
             // the products in flight end before the tensor memory is given back
-            if (elect_one()) mma_commit(&drained);
+            if (elect_one()) mma_commit(drained);
             __syncwarp();
-            wait(&drained, 0, 7);
+            wait(drained, 0, 7);
+        }
+        if (warp == 10) {
+            const uint64_t v_desc = desc_v(v_at);
+            uint32_t st = 0, phase = 0, done0 = 0, done1 = 0;
+            bool ok = true;
+            Segment s;
+            while (ok && walk.next(a, plan, s)) {
+                const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+                for (int i = s.first; ok && i < s.last; ++i) {
+                    ok = wait(v_full + st, phase, 8);
+                    for (int g = 0; ok && g < groups; ++g) {
+                        ok = wait(p_full + g, g ? done1++ : done0++, 9);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t vd = v_desc + (st * T::kQ >> 4);
+                            const uint32_t o = tmem + 256 + g * D, p = tmem + 128 + g * 64;
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(o, p + k * 8, vd + (k * 2048 >> 4), idesc_o, i > s.first || k > 0);
+                            mma_commit(pv_done + g);
+                            if (g == groups - 1) mma_commit(v_empty + st);
+                        }
+                        __syncwarp();
+                    }
+                    if (++st == NV) {
+                        st = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (elect_one()) mma_commit(drained + 1);
+            __syncwarp();
+            wait(drained + 1, 0, 10);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -706,42 +699,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float mx = max3(top[0], top[1], fmaxf(top[2], top[3]));
                 const float mn = fmaxf(m, mx == -INFINITY ? -INFINITY : mx * scale);
                 const bool grows = mn > m + kGrow || (m == -INFINITY && mn > m);
-                ok = __all_sync(0xffffffffu, free) || wait(pv_done + g, step - 1, 12);
-                if (!ok) break;
-                tc_fence_after();
-                if (g == 0 && !(p0 + kKeys <= src_end && (p0 >= now.lo_unit || p0 + kKeys <= a.sinks))) {
-                    // values that no row of the unit sees may be anything: they are
-                    // multiplied by zero, so they have to be finite.  (The first group
-                    // has a part in every unit and its product comes first.)
-                    const int pos = p0 + tid, st = put % NV;
-                    ok = wait(v_full + st, put / NV, 13);
+                const bool edge = g == 0 && !(p0 + kKeys <= src_end && (p0 >= now.lo_unit || p0 + kKeys <= a.sinks));
+                const bool rescales = i > s.first && grows;
+                if (i == s.first) m = mn;
+                if (__any_sync(0xffffffffu, rescales || edge || !free)) {
+                    if (step > 0) ok = wait(pv_done + g, step - 1, 12);
                     if (!ok) break;
-                    if (!(pos < src_end && (pos < a.sinks || pos >= now.lo_unit)))
+                    if (edge) {
+                        // values that no row of the unit sees may be anything: they are
+                        // multiplied by zero, so they have to be finite.  (The first group
+                        // has a part in every unit and its product comes first.)
+                        const int pos = p0 + tid, st = put % NV;
+                        ok = wait(v_full + st, put / NV, 13);
+                        if (!ok) break;
+                        if (!(pos < src_end && (pos < a.sinks || pos >= now.lo_unit)))
 #pragma unroll
-                        for (int c = 0; c < D / 8; ++c)
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
-                                         : "memory");
-                    fence_proxy_async_smem();
-                }
-                if (i == s.first) {
-                    m = mn;
-                } else if (__any_sync(0xffffffffu, grows)) {
-                    float f = 1.f;
-                    if (grows) {
-                        f = exp2_approx(m - mn);
-                        m = mn;
-                        l *= f;
+                            for (int c = 0; c < D / 8; ++c)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(v_at + st * T::kQ + (c / 8) * (kKeys * 128) + tid * 128 + (c % 8) * 16), "r"(0u)
+                                             : "memory");
+                        fence_proxy_async_smem();
                     }
+                    if (__any_sync(0xffffffffu, rescales)) {
+                        tc_fence_after();
+                        float f = 1.f;
+                        if (rescales) {
+                            f = exp2_approx(m - mn);
+                            m = mn;
+                            l *= f;
+                        }
 #pragma unroll
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_at + c, o);
-                        tmem_ld_wait();
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o_at + c, o);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st16(o_at + c, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(o_at + c, o);
+                        }
                     }
                 }
+                tc_fence_after();
                 const float use = m == -INFINITY ? 0.f : m;
                 const uint64_t scale2 = pair(scale, scale), use2 = pair(-use, -use);
                 uint64_t sum[2] = {0, 0};
