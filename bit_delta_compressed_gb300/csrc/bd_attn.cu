@@ -50,6 +50,8 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
     };
     w.decode.tickets = reinterpret_cast<int*>(take(kMaxBlocks * sizeof(int)));
     w.decode.parts = reinterpret_cast<float*>(take(decode_parts_bytes(head_dim)));
+    w.decode.own = reinterpret_cast<float*>(take((size_t)batch * q_heads * head_dim * sizeof(float)));
+    w.decode.own_ml = reinterpret_cast<float2*>(take((size_t)batch * q_heads * sizeof(float2)));
     if (weigh_len > 0) {
         w.decode.score_stride = (int64_t)round_up((size_t)weigh_len, 4);
         w.decode.lse = reinterpret_cast<float*>(take((size_t)batch * q_heads * sizeof(float)));
@@ -123,16 +125,17 @@ bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32
     a.weights = weights;
     a.status = static_cast<unsigned*>(workspace);
     const Workspace w = layout(workspace, T, B, q_heads, c->kv_heads, c->head_dim, weights ? c->capacity : 0);
-    if (cu_q) return launch_tiles(a, c->head_dim, w.plan, stream);
-    PrefixParts parts{};
-    if (P > 0) {
-        const bd_status done = launch_tiles(a, c->head_dim, w.plan, stream);
-        if (done != BD_OK) return done;
-        parts = {w.plan.o, w.plan.ml, w.plan.req_unit, w.plan.req_row, w.plan.unit_row, w.plan.unit_segs};
-    }
+    if (cu_q) return launch_prefill(a, c->head_dim, w.plan, stream);
     DecodeBuffers buf = w.decode;
-    buf.least_tiles = 32;
-    return launch_decode(a, c->head_dim, buf, parts, stream);
+    buf.with_prefix = P > 0;
+    if (P > 0) {
+        const bd_status done = launch_plan(a, w.plan, 1, stream);
+        if (done != BD_OK) return done;
+    }
+    bd_status done = launch_decode(a, c->head_dim, buf, stream);
+    if (done == BD_OK && P > 0) done = launch_prefixes(a, c->head_dim, w.plan, buf, stream);
+    if (done == BD_OK && weights) done = launch_weigh(a, buf, stream);
+    return done;
 }
 
 }  // namespace

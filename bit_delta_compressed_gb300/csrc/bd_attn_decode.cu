@@ -27,6 +27,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                 // keys of a tile
+constexpr int kLeastTiles = 32;           // of a block
 constexpr int kRuns = 128;                // runs of requests that a block looks its place up in
 
 // R: rows of a unit (8 or 16 query heads).  A probability is multiplied as two
@@ -106,9 +107,6 @@ __device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int ch
     }
 }
 
-// log2 of a row's denominator; a row without keys weighs nothing.
-__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? m + log2f(l) : (l == 0.f ? INFINITY : l); }
-
 // Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
 // gives a part's base, O [R][D] then (m, l) [R].
 template <int D, int R, typename F>
@@ -133,49 +131,25 @@ __device__ __forceinline__ void join(int row, int col, int count, F part, float&
     m = top;
 }
 
-// Adds what the shared prefix gave row `row` of a group: n pairs of neighbouring
-// values, the pairs `step` apart.
-template <int N>
-__device__ __forceinline__ void join_prefix(const PrefixParts& pp, int D, int b, int hk, int row, int col, float& m,
-                                            float& l, float* o, int o_step, int step) {
-    const int unit0 = pp.req_unit[b];
-    if (unit0 < 0) return;
-    const int2 seg = pp.unit_segs[unit0 + hk];
-    const int64_t r0 = pp.unit_row[unit0 + hk] + pp.req_row[b] + row;
-#pragma unroll 2
-    for (int s = 0; s < seg.y; ++s) {
-        const int64_t r = r0 + (int64_t)(seg.x + s) * kPartRows;
-        const float2 ml = pp.ml[r];
-        const float top = fmaxf(m, ml.x);
-        const float use = top == -INFINITY ? 0.f : top;
-        const float f = exp2_approx(m - use), g = exp2_approx(ml.x - use);
-        l = l * f + ml.y * g;
-        const float* from = pp.o + r * D + col;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float2 v = *reinterpret_cast<const float2*>(from + i * step);
-            o[i * o_step] = o[i * o_step] * f + g * v.x;
-            o[i * o_step + 1] = o[i * o_step + 1] * f + g * v.y;
-        }
-        m = top;
-    }
-}
-
-// A row's joined sums become its result: row r of the group, four values.
+// A row's joined sums become its result, or wait for the prefix's: row r of the
+// group, four values.
 template <int D>
-__device__ __forceinline__ void finish(const Args& a, const DecodeBuffers& buf, const PrefixParts& pp, int b, int hk,
-                                       int r, int col, float m, float l, float4 v) {
-    float o[4] = {v.x, v.y, v.z, v.w};
-    if (pp.o) join_prefix<2>(pp, D, b, hk, r, col, m, l, o, 2, 2);
-    const float inv = inverse(l);
+__device__ __forceinline__ void finish(const Args& a, const DecodeBuffers& buf, int b, int hk, int r, int col, float m,
+                                       float l, float4 o) {
     const int64_t at = (int64_t)b * a.Hq + hk * a.G + r;
+    if (buf.with_prefix) {
+        *reinterpret_cast<float4*>(buf.own + at * D + col) = o;
+        if (col == 0) buf.own_ml[at] = make_float2(m, l);
+        return;
+    }
+    const float inv = inverse(l);
     *reinterpret_cast<uint2*>(a.out + at * D + col) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     if (a.weights && col == 0) buf.lse[at] = log_sum(m, l);
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf, const PrefixParts pp) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf) {
     using S = Shape<D, R>;
     constexpr int NT = D / 8;              // 8-wide column tiles of the output
     extern __shared__ __align__(128) uint8_t smem[];
@@ -186,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
     const int units = a.Hk * chunks;
 
+    grid_go_on();
     // the line: tiles of the requests before each of kRuns runs of requests
     const int run = (a.B + kRuns - 1) / kRuns;
     {
@@ -208,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     }
     const int64_t total = sums[kRuns] * units;
     int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    per = per < buf.least_tiles ? buf.least_tiles : per;
+    per = per < kLeastTiles ? kLeastTiles : per;
     const int64_t block_lo = min(total, per * blockIdx.x), block_hi = min(total, block_lo + per);
     const int64_t lo = block_lo + (block_hi - block_lo) * warp / kWarps;
     const int64_t hi = block_lo + (block_hi - block_lo) * (warp + 1) / kWarps;
@@ -424,14 +399,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                 for (int i = 0; i < R / 8; ++i) {
                     const int r = g0 + row + 8 * i;
                     if (r >= a.G) continue;
-                    if (pp.o) join_prefix<NT>(pp, D, c.b, hk, r, col, m[i], l[i], &o[0][2 * i], 4, 8);
+                    const int64_t row_at = (int64_t)c.b * a.Hq + hk * a.G + r;
+                    if (buf.with_prefix) {
+                        float* to = buf.own + row_at * D + col;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            *reinterpret_cast<float2*>(to + t * 8) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
+                        if (lane % 4 == 0) buf.own_ml[row_at] = make_float2(m[i], l[i]);
+                        continue;
+                    }
                     const float inv = inverse(l[i]);
-                    __nv_bfloat16* to = a.out + ((int64_t)c.b * a.Hq + hk * a.G + r) * D + col;
+                    __nv_bfloat16* to = a.out + row_at * D + col;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         *reinterpret_cast<uint32_t*>(to + t * 8) = pack_bf16(o[t][2 * i] * inv, o[t][2 * i + 1] * inv);
-                    if (a.weights && lane % 4 == 0)
-                        buf.lse[(int64_t)c.b * a.Hq + hk * a.G + r] = log_sum(m[i], l[i]);
+                    if (a.weights && lane % 4 == 0) buf.lse[row_at] = log_sum(m[i], l[i]);
                 }
             }
             seg_at = at;
@@ -477,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                 *reinterpret_cast<float4*>(part + r * D + col) = o;
                 if (col == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, l);
             } else if (g0 + r < a.G) {
-                finish<D>(a, buf, pp, rec.b, hk, g0 + r, col, m, l, o);
+                finish<D>(a, buf, rec.b, hk, g0 + r, col, m, l, o);
             }
         }
         if (before || after) {
@@ -500,13 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
                     join<D, R>(r, col, c1 - c0 + 1,
                                [&](int s) { return buf.parts + (int64_t)(2 * (c0 + s) + (s ? 0 : 1)) * (R * D + 2 * R); }, m, l, o);
-                    if (g0 + r < a.G) finish<D>(a, buf, pp, rec.b, hk, g0 + r, col, m, l, o);
+                    if (g0 + r < a.G) finish<D>(a, buf, rec.b, hk, g0 + r, col, m, l, o);
                 }
             }
             __syncthreads();
         }
         first = last + 1;
     }
+    if (buf.with_prefix) grid_wait();
 }
 
 // weights[slot, h, key] += sum over the group's heads of exp(score - log of the
@@ -514,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
 // to its size) instead of the keys: 4 bytes a head and key for 2 head_dim.
 __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBuffers buf) {
     const int b = blockIdx.z, hk = blockIdx.y;
+    grid_wait();
     const Request r = read_request(a, b);
     const Keys k = visible_keys(a, r);
     const int64_t row = (int64_t)b * a.Hq + (int64_t)hk * a.G;
@@ -527,11 +511,12 @@ __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBu
 }
 
 template <int D, int R>
-bd_status launch_shape(const Args& a, DecodeBuffers buf, const PrefixParts& pp, cudaStream_t stream) {
+bd_status launch_shape(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {
     const void* kernel = reinterpret_cast<const void*>(decode_kernel<D, R>);
     if (!set_smem_attr(kernel, Shape<D, R>::kSmem, D == 128 ? (R == 8 ? 4 : 5) : (R == 8 ? 6 : 7))) return BD_ERR_CUDA;
-    const int blocks = decode_blocks();
-    decode_kernel<D, R><<<blocks, kThreads, Shape<D, R>::kSmem, stream>>>(a, buf, pp);
+    if (buf.with_prefix)       // beside the one block that lays out the prefixes' tiles
+        return launch_close(decode_kernel<D, R>, decode_blocks() > 1 ? decode_blocks() - 1 : 1, kThreads, Shape<D, R>::kSmem, stream, a, buf);
+    decode_kernel<D, R><<<decode_blocks(), kThreads, Shape<D, R>::kSmem, stream>>>(a, buf);
     return launch_status();
 }
 
@@ -541,19 +526,16 @@ int decode_blocks() { return sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks; 
 
 size_t decode_parts_bytes(int head_dim) { return (size_t)2 * decode_blocks() * (16 * head_dim + 32) * sizeof(float); }
 
-bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const PrefixParts& pp,
-                        cudaStream_t stream) {
-    bd_status st;
-    if (a.G <= 8)
-        st = head_dim == 128 ? launch_shape<128, 8>(a, buf, pp, stream) : launch_shape<64, 8>(a, buf, pp, stream);
-    else
-        st = head_dim == 128 ? launch_shape<128, 16>(a, buf, pp, stream) : launch_shape<64, 16>(a, buf, pp, stream);
-    if (st != BD_OK || !a.weights) return st;
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, cudaStream_t stream) {
+    if (a.G <= 8) return head_dim == 128 ? launch_shape<128, 8>(a, buf, stream) : launch_shape<64, 8>(a, buf, stream);
+    return head_dim == 128 ? launch_shape<128, 16>(a, buf, stream) : launch_shape<64, 16>(a, buf, stream);
+}
+
+bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {
     const int64_t heads = (int64_t)a.B * a.Hk, most = (a.capacity + 255) / 256;
     int64_t x = (8 * (int64_t)sm_count() + heads - 1) / heads;
     x = x < most ? x : most;
-    weigh_kernel<<<dim3((unsigned)x, (unsigned)a.Hk, (unsigned)a.B), 256, 0, stream>>>(a, buf);
-    return launch_status();
+    return launch_close(weigh_kernel, dim3((unsigned)x, (unsigned)a.Hk, (unsigned)a.B), 256, 0, stream, a, buf);
 }
 
 }  // namespace attn

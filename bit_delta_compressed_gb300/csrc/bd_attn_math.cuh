@@ -64,6 +64,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // What a row's sum divides by: a row that saw nothing gives zeros, a NaN stays.
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
+// log2 of a row's denominator; a row without keys weighs nothing.
+__device__ __forceinline__ float log_sum(float m, float l) { return l > 0.f ? m + log2f(l) : (l == 0.f ? INFINITY : l); }
+
+// ---- launches that follow one another closely ------------------------------------
+// A kernel launched so may start while the one before it in the stream still runs;
+// grid_wait() returns when that one has ended and its writes are visible.  Every
+// kernel launched so calls it once at least, at its end if not before, so that its
+// own end implies the end of all before it.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next launch may begin as soon as blocks of this one leave room.
+__device__ __forceinline__ void grid_go_on() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Given>
+bd_status launch_close(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                       Given... given) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.dynamicSmemBytes = smem;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&config, kernel, Params(given)...);
+    const bd_status st = launch_status();
+    return e == cudaSuccess ? st : BD_ERR_CUDA;
+}
+
 // ---- the workspace -----------------------------------------------------------
 // header, then tickets of units that several blocks join (zero between calls),
 // then what one call needs.
@@ -75,20 +105,14 @@ struct DecodeBuffers {
     float* scores;       // [B, Hq, score_stride] scaled scores of the visible own keys, by place among them
     float* lse;          // [B, Hq] log2 of the softmax's denominator
     int64_t score_stride;
-    int32_t least_tiles; // of a block
+    float* own;          // [B, Hq, D], and
+    float2* own_ml;      // [B, Hq] with prefixes: what the own keys gave, not normalised
+    int32_t with_prefix;
 };
 
-// Unnormalised parts of rows that the tile kernel computed: part s of a unit's
-// row lies kPartRows rows behind part s - 1.
+// Rows of a unit of the tile kernel, and the distance of its parts: part s of a
+// unit's row lies kPartRows rows behind part s - 1.
 constexpr int kPartRows = 256;
-struct PrefixParts {
-    const float* o;          // [rows][D]; NULL: none
-    const float2* ml;        // [rows] maximum (log2) and sum
-    const int32_t* req_unit; // [B] unit of the request's row tile and head 0, -1: no prefix
-    const int32_t* req_row;  // [B] its first row in the unit
-    const int64_t* unit_row; // [units] first row of the unit's part from block 0
-    const int2* unit_segs;   // [units] first block and number of parts
-};
 
 // ---- the tile kernel's plan (in the workspace) ---------------------------------
 // A row tile: `tokens` tokens (their rows of q begin at row0; for prefixes row0 is
@@ -111,22 +135,24 @@ struct TilePlan {
     PlanHead* head;
     RowTile* tiles;
     int32_t* order;          // requests sorted by prefix
-    int32_t *req_unit, *req_row;
-    int64_t* unit_row;
-    int2* unit_segs;
-    float* o;                // unnormalised parts
-    float2* ml;
+    int32_t *req_unit, *req_row;  // of a request: unit of its row tile and head 0 (-1: no prefix), first row in it
+    int64_t* unit_row;       // first row of a unit's part from block 0
+    int2* unit_segs;         // first block and number of parts
+    float* o;                // unnormalised parts of rows,
+    float2* ml;              // their maximum (log2) and sum
 };
 
 int tile_blocks();
 int64_t split_below();       // units from which on a prefill is not split
 int64_t most_tiles(int64_t tokens, int64_t batch, int G);
-bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
+bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
+bd_status launch_plan(const Args& a, const TilePlan& plan, int split, cudaStream_t stream);
+bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, const DecodeBuffers& buf, cudaStream_t stream);
 
 int decode_blocks();
 size_t decode_parts_bytes(int head_dim);
-bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const PrefixParts& pp,
-                        cudaStream_t stream);
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, cudaStream_t stream);
+bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace bd

@@ -125,6 +125,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t*
 // prefix's requests in tiles.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const TilePlan plan, int blocks, int split) {
     extern __shared__ int32_t counts[];     // [P + 1] of each prefix, then its first place
+    grid_go_on();
     __shared__ int64_t part[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per_tile = tokens_of_tile(a.G);
@@ -344,19 +345,29 @@ struct Segment {
     int tile, hk, first, last;               // blocks [first, last) of the unit
 };
 
-// The segments of this block, in order.
+// The segments of this block, in order: its part of the line, or whole units from
+// the last one on.
 struct Walk {
-    int64_t at, end;                          // places on the line
+    int64_t at, end, stride;                  // places on the line; units
     int tile, hk, first;
     bool whole;
     __device__ __forceinline__ bool next(const Args& a, const TilePlan& plan, Segment& s) {
+        if (whole) {
+            if (at < 0) return false;
+            s.tile = (int)(at / a.Hk);
+            s.hk = (int)(at % a.Hk);
+            s.first = 0;
+            s.last = plan.tiles[s.tile].blocks;
+            at -= stride;
+            return true;
+        }
         if (at >= end) return false;
         const int n = plan.tiles[tile].blocks;
         s.tile = tile;
         s.hk = hk;
         s.first = first;
-        s.last = whole ? n : (int)min((int64_t)n, first + (end - at));
-        at += whole ? 1 : s.last - first;
+        s.last = (int)min((int64_t)n, first + (end - at));
+        at += s.last - first;
         first = 0;
         if (++hk == a.Hk) {
             hk = 0;
@@ -434,36 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t q_at = base, k_at = base + 2 * T::kQ, v_at = k_at + NK * T::kQ;
 
-    const PlanHead head = *plan.head;
-    Walk walk{};
-    if (split) {
-        walk.at = min(head.line, head.per * blockIdx.x);
-        walk.end = min(head.line, walk.at + head.per);
-        if (walk.at >= walk.end) return;
-        for (int i = tid; i < head.tiles; i += kThreads) {
-            const int64_t lo = plan.tiles[i].line * a.Hk, n = plan.tiles[i].blocks;
-            if (walk.at >= lo && walk.at < lo + n * a.Hk) {
-                start[0] = i;
-                line_at[0] = walk.at - lo;
-            }
-        }
-        __syncthreads();
-        walk.tile = start[0];
-        const int n = plan.tiles[walk.tile].blocks;
-        walk.hk = (int)(line_at[0] / n);
-        walk.first = (int)(line_at[0] % n);
-    } else {
-        // the last tile of a prompt has the most keys: begin there
-        const int64_t units = (int64_t)head.tiles * a.Hk;
-        if ((int64_t)blockIdx.x >= units) return;
-        const int64_t u = units - 1 - blockIdx.x;
-        walk.at = 0;
-        walk.end = 1;
-        walk.tile = (int)(u / a.Hk);
-        walk.hk = (int)(u % a.Hk);
-        walk.whole = true;
-    }
-
     if (warp == 8) tmem_alloc(&tmem_at, 512);
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) {
@@ -488,6 +469,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_wait();                              // the plan
+    grid_go_on();
+    const PlanHead head = *plan.head;
+    Walk walk{};
+    if (split) {
+        walk.at = min(head.line, head.per * blockIdx.x);
+        walk.end = min(head.line, walk.at + head.per);
+        for (int i = tid; i < head.tiles; i += kThreads) {
+            const int64_t lo = plan.tiles[i].line * a.Hk, n = plan.tiles[i].blocks;
+            if (walk.at < walk.end && walk.at >= lo && walk.at < lo + n * a.Hk) {
+                start[0] = i;
+                line_at[0] = walk.at - lo;
+            }
+        }
+        __syncthreads();
+        if (walk.at < walk.end) {
+            walk.tile = start[0];
+            const int n = plan.tiles[walk.tile].blocks;
+            walk.hk = (int)(line_at[0] / n);
+            walk.first = (int)(line_at[0] % n);
+        }
+    } else {
+        // the last tile of a prompt has the most keys: begin there
+        walk.at = head.tiles * a.Hk - 1 - blockIdx.x;
+        walk.stride = gridDim.x;
+        walk.whole = true;
+    }
     const uint32_t tmem = tmem_at;
 
     // registers: 3 x 168 for each lane of the three warp groups at launch; the loading
@@ -800,38 +808,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
+// Adds part s = 0 .. n - 1 of a row, kPartRows rows apart from row r0 on, four values.
+template <int D>
+__device__ __forceinline__ void add_parts(const TilePlan& plan, int64_t r0, int n, int col, float& m, float& l, float4& o) {
+    float top = m;
+    for (int s = 0; s < n; ++s) top = fmaxf(top, plan.ml[r0 + (int64_t)s * kPartRows].x);
+    const float use = top == -INFINITY ? 0.f : top;
+    float f = exp2_approx(m - use);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+        const int64_t at = r0 + (int64_t)s * kPartRows;
+        const float2 ml = plan.ml[at];
+        const float4 v = *reinterpret_cast<const float4*>(plan.o + at * D + col);
+        f = exp2_approx(ml.x - use);
+        l += f * ml.y;
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+    }
+    m = top;
+}
+
+__device__ __forceinline__ uint2 result(float4 o, float l) {
+    const float inv = inverse(l);
+    return make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+}
+
 // Joins the parts of a split prefill: one thread four values of a row.
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan plan) {
-    const int64_t units = (int64_t)plan.head->tiles * a.Hk;
+    grid_wait();
+    const int64_t units = plan.head->tiles * a.Hk;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const RowTile& t = plan.tiles[u / a.Hk];
         const int hk = (int)(u % a.Hk), rows = t.tokens * a.G;
         const int2 seg = plan.unit_segs[u];
         for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
             const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-            const int64_t r0 = plan.unit_row[u] + (int64_t)seg.x * kPartRows + r;
             float m = -INFINITY, l = 0.f;
-            for (int s = 0; s < seg.y; ++s) m = fmaxf(m, plan.ml[r0 + (int64_t)s * kPartRows].x);
-            const float use = m == -INFINITY ? 0.f : m;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int s = 0; s < seg.y; ++s) {
-                const int64_t at = r0 + (int64_t)s * kPartRows;
-                const float2 ml = plan.ml[at];
-                const float f = exp2_approx(ml.x - use);
-                const float4 v = *reinterpret_cast<const float4*>(plan.o + at * D + col);
-                l += f * ml.y;
-                o.x += f * v.x;
-                o.y += f * v.y;
-                o.z += f * v.z;
-                o.w += f * v.w;
-            }
-            const float inv = inverse(l);
+            add_parts<D>(plan, plan.unit_row[u] + (int64_t)seg.x * kPartRows + r, seg.y, col, m, l, o);
             const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
-            *reinterpret_cast<uint2*>(a.out + to) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+            *reinterpret_cast<uint2*>(a.out + to) = result(o, l);
         }
     }
+}
+
+// Joins a decode step's parts: what a row's own keys gave (the decode kernel) and
+// what its prefix gave.
+template <int D>
+__global__ void __launch_bounds__(256) join_prefix_kernel(const Args a, const TilePlan plan, const DecodeBuffers buf) {
+    grid_wait();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / (D / 4);
+    if (row >= (int64_t)a.B * a.Hq) return;
+    const int col = (int)(i % (D / 4)) * 4, b = (int)(row / a.Hq), h = (int)(row % a.Hq);
+    const float2 ml = buf.own_ml[row];
+    float m = ml.x, l = ml.y;
+    float4 o = *reinterpret_cast<const float4*>(buf.own + row * D + col);
+    const int unit0 = plan.req_unit[b];
+    if (unit0 >= 0) {
+        const int u = unit0 + h / a.G;
+        const int2 seg = plan.unit_segs[u];
+        add_parts<D>(plan, plan.unit_row[u] + (int64_t)seg.x * kPartRows + plan.req_row[b] + h % a.G, seg.y, col, m, l, o);
+    }
+    *reinterpret_cast<uint2*>(a.out + row * D + col) = result(o, l);
+    if (a.weights && col == 0) buf.lse[row] = log_sum(m, l);
 }
 
 // The cache as a 4-D tensor whose dimensions follow their strides, whichever
@@ -860,20 +904,13 @@ bool cache_map(CUtensorMap* map, MapOrder* order, const void* base, const Args& 
 }
 
 template <int D>
-bd_status launch_shape(const Args& a, const TilePlan& plan, int64_t grid, int blocks, int split, cudaStream_t stream) {
+bd_status launch_kernel(const Args& a, const TilePlan& plan, int split, cudaStream_t stream) {
     const void* kernel = reinterpret_cast<const void*>(tile_kernel<D>);
     if (!set_smem_attr(kernel, Tile<D>::kSmem, D == 128 ? 8 : 9)) return BD_ERR_CUDA;
     CUtensorMap kmap, vmap;
     MapOrder order{};
     if (!cache_map(&kmap, &order, a.k, a, D) || !cache_map(&vmap, &order, a.v, a, D)) return BD_ERR_CUDA;
-    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, blocks, split);
-    bd_status st = launch_status();
-    if (st != BD_OK) return st;
-    tile_kernel<D><<<(unsigned)grid, kThreads, Tile<D>::kSmem, stream>>>(a, plan, kmap, vmap, order, split);
-    st = launch_status();
-    if (st != BD_OK || !a.cu_q || !split) return st;
-    join_kernel<D><<<dim3((unsigned)blocks, 8), 256, 0, stream>>>(a, plan);
-    return launch_status();
+    return launch_close(tile_kernel<D>, tile_blocks(), kThreads, Tile<D>::kSmem, stream, a, plan, kmap, vmap, order, split);
 }
 
 }  // namespace
@@ -881,17 +918,33 @@ bd_status launch_shape(const Args& a, const TilePlan& plan, int64_t grid, int bl
 // Row tiles that a call can have at most.
 int64_t most_tiles(int64_t tokens, int64_t batch, int G) { return tokens / (kPartRows / G) + batch; }
 
-bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
-    const int blocks = tile_blocks();
-    const int64_t units = most_tiles(a.T, a.B, a.G) * a.Hk;
-    const int split = !a.cu_q || units < split_below();
-    const int64_t grid = split ? blocks : units;
-    return head_dim == 128 ? launch_shape<128>(a, plan, grid, blocks, split, stream)
-                           : launch_shape<64>(a, plan, grid, blocks, split, stream);
-}
-
 int tile_blocks() { return decode_blocks(); }
 int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
+
+bd_status launch_plan(const Args& a, const TilePlan& plan, int split, cudaStream_t stream) {
+    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, tile_blocks(), split);
+    return launch_status();
+}
+
+bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
+    const int split = most_tiles(a.T, a.B, a.G) * a.Hk < split_below();
+    bd_status st = launch_plan(a, plan, split, stream);
+    if (st != BD_OK) return st;
+    st = head_dim == 128 ? launch_kernel<128>(a, plan, split, stream) : launch_kernel<64>(a, plan, split, stream);
+    if (st != BD_OK || !split) return st;
+    const dim3 grid((unsigned)tile_blocks(), 8);
+    return head_dim == 128 ? launch_close(join_kernel<128>, grid, 256, 0, stream, a, plan)
+                           : launch_close(join_kernel<64>, grid, 256, 0, stream, a, plan);
+}
+
+bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, const DecodeBuffers& buf,
+                          cudaStream_t stream) {
+    const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, 1, stream) : launch_kernel<64>(a, plan, 1, stream);
+    if (st != BD_OK) return st;
+    const unsigned blocks = (unsigned)(((int64_t)a.B * a.Hq * (head_dim / 4) + 255) / 256);
+    return head_dim == 128 ? launch_close(join_prefix_kernel<128>, blocks, 256, 0, stream, a, plan, buf)
+                           : launch_close(join_prefix_kernel<64>, blocks, 256, 0, stream, a, plan, buf);
+}
 
 }  // namespace attn
 }  // namespace bd
