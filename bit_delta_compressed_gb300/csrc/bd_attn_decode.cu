@@ -27,7 +27,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                 // keys of a tile
-constexpr int kLeastTiles = 32;           // of a block
+constexpr int kUnitCost = 3;              // places of a unit besides its tiles
+constexpr int kLeast = 16;                // places of a block
+constexpr int kShort = 64;                // tiles up to which a unit may have a block of its own
 constexpr int kRuns = 128;                // runs of requests that a block looks its place up in
 
 // R: rows of a unit (8 or 16 query heads).  A probability is multiplied as two
@@ -64,9 +66,20 @@ __device__ __forceinline__ int tiles_of(const Args& a, const Request& r) {
     return max(1, (visible_keys(a, r).n + kTile - 1) / kTile);
 }
 
-// One position on the line of tiles and the geometry of its unit.
+// The line: every unit takes kUnitCost places (what a unit costs besides its tiles:
+// its query, its result) and one for each tile.  If all units are short and no more
+// than the blocks, each has a block of its own instead: `each` places.
+struct Line {
+    int64_t lo, hi;                        // this warp's places
+    int32_t each;                          // 0: units follow one another
+    __device__ __forceinline__ int length(int tiles) const { return each ? each : kUnitCost + tiles; }
+    __device__ __forceinline__ int lead() const { return each ? 0 : kUnitCost; }
+};
+
+// A unit on the line and its tiles [tile, end) that lie in the warp's part.
 struct Cursor {
-    int b, u, tile, tiles;
+    int b, u, tiles, tile, end;
+    int64_t start;                         // the unit's first place
     Request r;
     Keys k;
 };
@@ -77,58 +90,88 @@ __device__ __forceinline__ void load_request(const Args& a, Cursor& c) {
     c.tiles = max(1, (c.k.n + kTile - 1) / kTile);
 }
 
-__device__ __forceinline__ void advance(const Args& a, Cursor& c, int units) {
-    if (++c.tile < c.tiles) return;
-    c.tile = 0;
-    if (++c.u < units) return;
-    c.u = 0;
-    if (++c.b < a.B) load_request(a, c);
+// Goes on to the first unit from c on with tiles in the part; false if there is none.
+__device__ __forceinline__ bool seek(const Args& a, const Line& line, Cursor& c, int units) {
+    while (c.start < line.hi) {
+        const int64_t first = c.start + line.lead();
+        c.tile = (int)min(max(line.lo - first, (int64_t)0), (int64_t)c.tiles);
+        c.end = (int)min(max(line.hi - first, (int64_t)0), (int64_t)c.tiles);
+        if (c.tile < c.end) return true;
+        c.start += line.length(c.tiles);
+        if (++c.u == units) {
+            c.u = 0;
+            if (++c.b >= a.B) return false;
+            load_request(a, c);
+        }
+    }
+    return false;
+}
+__device__ __forceinline__ bool next_unit(const Args& a, const Line& line, Cursor& c, int units) {
+    c.start += line.length(c.tiles);
+    if (++c.u == units) {
+        c.u = 0;
+        if (++c.b >= a.B) return false;
+        load_request(a, c);
+    }
+    return seek(a, line, c, units);
 }
 
 struct Record {                            // an open unit of a warp
-    int valid, b, u, tile, tiles, open_end;
-    int64_t at;                            // its first tile's place on the line
+    int valid, b, u, tiles, open_start, open_end;
+    int64_t start;
 };
 
 template <int D>
 __device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int chunks, uint32_t stage, int lane) {
     constexpr int L = D / 8;               // lanes of a row
-    const int h = c.u / chunks;
-    const int64_t base = (int64_t)c.r.slot * a.ss + (int64_t)h * a.sh + (lane % L) * 8;
+    constexpr int rows = 32 / L;           // rows of one step
+    const int h = c.u / chunks, x0 = c.tile * kTile, row = lane / L;
+    const __nv_bfloat16* k = a.k + (int64_t)c.r.slot * a.ss + (int64_t)h * a.sh + (lane % L) * 8;
+    const int64_t v = a.v - a.k;
+    const uint32_t to = stage + row * (D * 2);
+    if (x0 + kTile <= c.k.n && (x0 >= c.k.head || x0 + kTile <= c.k.head)) {
+        k += (int64_t)(x0 + (x0 >= c.k.head ? c.k.gap : 0) + row) * a.st;
 #pragma unroll
-    for (int i = 0; i < kTile * L / 32; ++i) {
-        const int row = i * (32 / L) + lane / L;
-        const int x = c.tile * kTile + row;
+        for (int i = 0; i < kTile / rows; ++i) {
+            const uint32_t at = to + i * rows * (D * 2) + (((lane % L) ^ ((i * rows + row) & 7)) << 4);
+            cp_async16(at, k, true);
+            cp_async16(at + kTile * D * 2, k + v, true);
+            k += rows * a.st;
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < kTile / rows; ++i) {
+        const int x = x0 + i * rows + row;
         const bool in = x < c.k.n;
-        const int64_t off = in ? base + (int64_t)(x + (x >= c.k.head ? c.k.gap : 0)) * a.st : 0;
-        const uint32_t to = stage + row * (D * 2) + (((lane % L) ^ (row & 7)) << 4);
-        cp_async16(to, a.k + off, in);
-        cp_async16(to + kTile * D * 2, a.v + off, in);
+        const __nv_bfloat16* from = in ? k + (int64_t)(x + (x >= c.k.head ? c.k.gap : 0)) * a.st : a.k;
+        const uint32_t at = to + i * rows * (D * 2) + (((lane % L) ^ ((i * rows + row) & 7)) << 4);
+        cp_async16(at, from, in);
+        cp_async16(at + kTile * D * 2, from + v, in);
     }
 }
 
 // Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
-// gives a part's base, O [R][D] then (m, l) [R].
+// gives a part's base, O [R][D] then (m, l) [R], or NULL for one that is none.
 template <int D, int R, typename F>
 __device__ __forceinline__ void join(int row, int col, int count, F part, float& m, float& l, float4& o) {
-    float top = m;
-    for (int s = 0; s < count; ++s) top = fmaxf(top, part(s)[R * D + 2 * row]);
-    const float use = top == -INFINITY ? 0.f : top;
-    float f = exp2_approx(m - use);
-    l *= f;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll 4
+    for (int s = 0; s < count; ++s)
+        if (const float* p = part(s)) m = fmaxf(m, p[R * D + 2 * row]);
+    const float use = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
     for (int s = 0; s < count; ++s) {
         const float* p = part(s);
-        f = exp2_approx(p[R * D + 2 * row] - use);
-        l += f * p[R * D + 2 * row + 1];
+        if (!p) continue;
+        const float2 ml = *reinterpret_cast<const float2*>(p + R * D + 2 * row);
+        const float f = exp2_approx(ml.x - use);
+        l += f * ml.y;
         const float4 v = *reinterpret_cast<const float4*>(p + row * D + col);
         o.x += f * v.x;
         o.y += f * v.y;
         o.z += f * v.z;
         o.w += f * v.w;
     }
-    m = top;
 }
 
 // A row's joined sums become its result, or wait for the prefix's: row r of the
@@ -154,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     constexpr int NT = D / 8;              // 8-wide column tiles of the output
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sums[kRuns + 1];
+    __shared__ int longest[kRuns / 32];
     __shared__ Record records[2 * kWarps];
     __shared__ int last_block;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -161,61 +205,88 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     const int units = a.Hk * chunks;
 
     grid_go_on();
-    // the line: tiles of the requests before each of kRuns runs of requests
+    // the line: places of the requests before each of kRuns runs of requests
     const int run = (a.B + kRuns - 1) / kRuns;
     {
         int64_t mine = 0;
-        for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) mine += tiles_of(a, read_request(a, b));
+        int most = 0;
+        for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) {
+            const int n = tiles_of(a, read_request(a, b));
+            mine += kUnitCost + n;
+            most = max(most, n);
+        }
         int64_t incl = mine;
         for (int x = 1; x < 32; x <<= 1) {
             const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
             if (lane >= x) incl += o;
         }
-        if (lane == 31 && tid < kRuns) sums[warp] = incl;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 31 && tid < kRuns) {
+            sums[warp] = incl;
+            longest[warp] = most;
+        }
+        if (tid < 2 * kWarps) records[tid].valid = 0;
         __syncthreads();
         int64_t before = 0;
         for (int w = 0; w < warp && tid < kRuns; ++w) before += sums[w];
         __syncthreads();
         if (tid < kRuns) sums[tid + 1] = before + incl;
         if (tid == 0) sums[0] = 0;
-        if (tid < 2 * kWarps) records[tid].valid = 0;
         __syncthreads();
     }
-    const int64_t total = sums[kRuns] * units;
+    Line line;
+    line.each = 0;
+    if ((int64_t)a.B * units <= gridDim.x) {
+        int most = 0;
+        for (int w = 0; w < kRuns / 32; ++w) most = max(most, longest[w]);
+        if (most <= kShort) line.each = most;
+    }
+    const int64_t total = line.each ? (int64_t)a.B * units * line.each : sums[kRuns] * units;
     int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    per = per < kLeastTiles ? kLeastTiles : per;
+    if (line.each) per = line.each;
+    else per = per < kLeast ? kLeast : per;
     const int64_t block_lo = min(total, per * blockIdx.x), block_hi = min(total, block_lo + per);
-    const int64_t lo = block_lo + (block_hi - block_lo) * warp / kWarps;
-    const int64_t hi = block_lo + (block_hi - block_lo) * (warp + 1) / kWarps;
+    line.lo = block_lo + (block_hi - block_lo) * warp / kWarps;
+    line.hi = block_lo + (block_hi - block_lo) * (warp + 1) / kWarps;
 
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
     float* const head_part = reinterpret_cast<float*>(smem + kWarps * S::kRing + warp * S::kPart);
 
-    if (lo < hi) {
-        Cursor c;
-        {
+    Cursor c;
+    bool has = line.lo < line.hi;
+    if (has) {
+        if (line.each) {
+            const int unit = (int)(line.lo / line.each);
+            c.b = unit / units;
+            c.u = unit % units;
+            c.start = (int64_t)unit * line.each;
+            load_request(a, c);
+        } else {
             int s = 0;                     // the run that holds place lo
             for (int step = kRuns / 2; step; step /= 2)
-                if (sums[s + step] * units <= lo) s += step;
-            int64_t rest = lo - sums[s] * units;
+                if (sums[s + step] * units <= line.lo) s += step;
+            c.start = sums[s] * units;
             c.b = s * run;
             load_request(a, c);
-            while (rest >= (int64_t)c.tiles * units && c.b + 1 < a.B) {
-                rest -= (int64_t)c.tiles * units;
+            while (line.lo - c.start >= (int64_t)line.length(c.tiles) * units && c.b + 1 < a.B) {
+                c.start += (int64_t)line.length(c.tiles) * units;
                 ++c.b;
                 load_request(a, c);
             }
-            c.u = (int)(rest / c.tiles);
-            c.tile = (int)(rest % c.tiles);
+            c.u = min((int)((line.lo - c.start) / line.length(c.tiles)), units - 1);
+            c.start += (int64_t)c.u * line.length(c.tiles);
         }
+        has = seek(a, line, c, units);
+    }
+    if (has) {
         Cursor ahead = c;
-        int64_t ahead_at = lo;
+        bool more = true;
         int put = 0;
         auto prefetch = [&]() {
-            if (ahead_at < hi) {
+            if (more) {
                 load_tile<D>(a, ahead, chunks, ring + put * S::kStage, lane);
-                if (++ahead_at < hi) advance(a, ahead, units);
+                if (++ahead.tile == ahead.end) more = next_unit(a, line, ahead, units);
             }
             cp_async_commit();
             if (++put == S::kStages) put = 0;
@@ -224,15 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         for (int i = 0; i < S::kStages - 1; ++i) prefetch();
 
         int got = 0;
-        int64_t at = lo, seg_at = lo;
-        int seg_tile = c.tile;             // the unit's first tile in this warp
         uint32_t qf[D / 16][R == 8 ? 2 : 4];
         float o[NT][4], m[R / 8], l[R / 8];
         const int row = lane / 4, col = 2 * (lane % 4);
-        bool fresh = true;
-        while (at < hi) {
-            if (fresh) {
-                fresh = false;
+        do {
+            const int seg_tile = c.tile;
+            {
                 const int hk = c.u / chunks, head0 = hk * a.G + (c.u % chunks) * R;
                 const int rows = min(R, a.G - (c.u % chunks) * R);
                 const __nv_bfloat16* qp = a.q + (int64_t)c.b * a.q_stride + (int64_t)head0 * D;
@@ -248,112 +316,114 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
 #pragma unroll
                 for (int i = 0; i < R / 8; ++i) { m[i] = -INFINITY; l[i] = 0.f; }
             }
-            prefetch();
-            cp_async_wait<S::kStages - 1>();
-            __syncwarp();
-            const uint32_t ks = ring + got * S::kStage, vs = ks + kTile * D * 2;
-            if (++got == S::kStages) got = 0;
-            float s[2][4] = {};
+#pragma unroll 1
+            for (; c.tile < c.end; ++c.tile) {
+                prefetch();
+                cp_async_wait<S::kStages - 1>();
+                __syncwarp();
+                const uint32_t ks = ring + got * S::kStage, vs = ks + kTile * D * 2;
+                if (++got == S::kStages) got = 0;
+                float s[2][4] = {}, odd[2][4] = {};    // two chains of products each
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int key = (lane / 16) * 8 + lane % 8, chunk = 2 * kk + (lane / 8) % 2;
-                uint32_t kf[4];
-                ldmatrix4(kf, ks + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
-                if constexpr (R == 8) {
-                    mma16816(s[0], qf[kk][0], 0u, qf[kk][1], 0u, kf[0], kf[1]);
-                    mma16816(s[1], qf[kk][0], 0u, qf[kk][1], 0u, kf[2], kf[3]);
-                } else {
-                    mma16816(s[0], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[0], kf[1]);
-                    mma16816(s[1], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[2], kf[3]);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int key = (lane / 16) * 8 + lane % 8, chunk = 2 * kk + (lane / 8) % 2;
+                    uint32_t kf[4];
+                    ldmatrix4(kf, ks + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+                    if constexpr (R == 8) {
+                        mma16816(kk % 2 ? odd[0] : s[0], qf[kk][0], 0u, qf[kk][1], 0u, kf[0], kf[1]);
+                        mma16816(kk % 2 ? odd[1] : s[1], qf[kk][0], 0u, qf[kk][1], 0u, kf[2], kf[3]);
+                    } else {
+                        mma16816(kk % 2 ? odd[0] : s[0], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[0], kf[1]);
+                        mma16816(kk % 2 ? odd[1] : s[1], qf[kk][0], qf[kk][1], qf[kk][2], qf[kk][3], kf[2], kf[3]);
+                    }
                 }
-            }
-            const int x0 = c.tile * kTile + col;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool in = x0 + 8 * t + i < c.k.n;
-                    s[t][i] = in ? s[t][i] * a.scale_log2 : -INFINITY;
-                    if (R == 16) s[t][2 + i] = in ? s[t][2 + i] * a.scale_log2 : -INFINITY;
+                    for (int i = 0; i < 4; ++i) s[t][i] += odd[t][i];
+                const int x0 = c.tile * kTile + col;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool in = x0 + 8 * t + i < c.k.n;
+                        s[t][i] = in ? s[t][i] * a.scale_log2 : -INFINITY;
+                        if (R == 16) s[t][2 + i] = in ? s[t][2 + i] * a.scale_log2 : -INFINITY;
+                    }
+                if (a.weights) {
+                    // the raw scores, for the weights' pass over them
+                    const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
+#pragma unroll
+                    for (int i = 0; i < R / 8; ++i) {
+                        const int r = g0 + row + 8 * i;
+                        if (r >= a.G) continue;
+                        float* to = buf.scores + ((int64_t)c.b * a.Hq + hk * a.G + r) * buf.score_stride;
+                        if (x0 < c.k.n) to[x0] = s[0][2 * i];
+                        if (x0 + 1 < c.k.n) to[x0 + 1] = s[0][2 * i + 1];
+                        if (x0 + 8 < c.k.n) to[x0 + 8] = s[1][2 * i];
+                        if (x0 + 9 < c.k.n) to[x0 + 9] = s[1][2 * i + 1];
+                    }
                 }
-            if (a.weights) {
-                // the raw scores, for the weights' pass over them
-                const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
+                uint32_t pf[4], pl[4];
+                float top[R / 8];
+                bool grows = false;
 #pragma unroll
                 for (int i = 0; i < R / 8; ++i) {
-                    const int r = g0 + row + 8 * i;
-                    if (r >= a.G) continue;
-                    float* to = buf.scores + ((int64_t)c.b * a.Hq + hk * a.G + r) * buf.score_stride;
-                    if (x0 < c.k.n) to[x0] = s[0][2 * i];
-                    if (x0 + 1 < c.k.n) to[x0 + 1] = s[0][2 * i + 1];
-                    if (x0 + 8 < c.k.n) to[x0 + 8] = s[1][2 * i];
-                    if (x0 + 9 < c.k.n) to[x0 + 9] = s[1][2 * i + 1];
+                    float t = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                    top[i] = fmaxf(m[i], t);
+                    grows = grows || top[i] > m[i];
                 }
-            }
-            uint32_t pf[4], pl[4];
-            float top[R / 8];
-            bool grows = false;
+                if (__any_sync(0xffffffffu, grows)) {
+                    float f[R / 8];
 #pragma unroll
-            for (int i = 0; i < R / 8; ++i) {
-                float t = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-                top[i] = fmaxf(m[i], t);
-                grows = grows || top[i] > m[i];
-            }
-            if (__any_sync(0xffffffffu, grows)) {
-                float f[R / 8];
+                    for (int i = 0; i < R / 8; ++i) {
+                        f[i] = top[i] > m[i] ? exp2_approx(m[i] - top[i]) : 1.f;
+                        l[i] *= f[i];
+                        m[i] = top[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        o[i][0] *= f[0];
+                        o[i][1] *= f[0];
+                        o[i][2] *= f[R / 8 - 1];
+                        o[i][3] *= f[R / 8 - 1];
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < R / 8; ++i) {
-                    f[i] = top[i] > m[i] ? exp2_approx(m[i] - top[i]) : 1.f;
-                    l[i] *= f[i];
-                    m[i] = top[i];
+                    const float use = m[i] == -INFINITY ? 0.f : m[i];
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[e / 2][2 * i + e % 2] - use);
+                    l[i] += (p[0] + p[1]) + (p[2] + p[3]);
+                    const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
+                    if constexpr (R == 8) {
+                        pf[0] = h0;
+                        pf[1] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
+                        pf[2] = h1;
+                        pf[3] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
+                    } else {
+                        pf[i] = h0;
+                        pf[2 + i] = h1;
+                        pl[i] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
+                        pl[2 + i] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
+                    }
                 }
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    o[i][0] *= f[0];
-                    o[i][1] *= f[0];
-                    o[i][2] *= f[R / 8 - 1];
-                    o[i][3] *= f[R / 8 - 1];
+                for (int cc = 0; cc < D / 16; ++cc) {
+                    const int key = ((lane / 8) % 2) * 8 + lane % 8, chunk = 2 * cc + lane / 16;
+                    uint32_t vf[4];
+                    ldmatrix4_trans(vf, vs + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+                    mma16816(o[2 * cc], pf[0], pf[1], pf[2], pf[3], vf[0], vf[1]);
+                    mma16816(o[2 * cc + 1], pf[0], pf[1], pf[2], pf[3], vf[2], vf[3]);
+                    if constexpr (R == 16) {
+                        mma16816(o[2 * cc], pl[0], pl[1], pl[2], pl[3], vf[0], vf[1]);
+                        mma16816(o[2 * cc + 1], pl[0], pl[1], pl[2], pl[3], vf[2], vf[3]);
+                    }
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < R / 8; ++i) {
-                const float use = m[i] == -INFINITY ? 0.f : m[i];
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[e / 2][2 * i + e % 2] - use);
-                l[i] += (p[0] + p[1]) + (p[2] + p[3]);
-                const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
-                if constexpr (R == 8) {
-                    pf[0] = h0;
-                    pf[1] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
-                    pf[2] = h1;
-                    pf[3] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
-                } else {
-                    pf[i] = h0;
-                    pf[2 + i] = h1;
-                    pl[i] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
-                    pl[2 + i] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
-                }
-            }
-#pragma unroll
-            for (int cc = 0; cc < D / 16; ++cc) {
-                const int key = ((lane / 8) % 2) * 8 + lane % 8, chunk = 2 * cc + lane / 16;
-                uint32_t vf[4];
-                ldmatrix4_trans(vf, vs + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
-                mma16816(o[2 * cc], pf[0], pf[1], pf[2], pf[3], vf[0], vf[1]);
-                mma16816(o[2 * cc + 1], pf[0], pf[1], pf[2], pf[3], vf[2], vf[3]);
-                if constexpr (R == 16) {
-                    mma16816(o[2 * cc], pl[0], pl[1], pl[2], pl[3], vf[0], vf[1]);
-                    mma16816(o[2 * cc + 1], pl[0], pl[1], pl[2], pl[3], vf[2], vf[3]);
-                }
-            }
-            __syncwarp();
-            ++at;
-            if (c.tile + 1 < c.tiles && at < hi) {
-                ++c.tile;
-                continue;
+                __syncwarp();
             }
             // the unit, or this warp's part of it, is done
 #pragma unroll
@@ -368,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     o[i][1] += o[i][3];
                 }
             }
-            const bool open_start = seg_tile > 0, open_end = c.tile + 1 < c.tiles;
+            const bool open_start = seg_tile > 0, open_end = c.end < c.tiles;
             if (open_start || open_end) {
                 // one that began before is kept beside the ring, the last one (no
                 // tile follows it) in the ring
@@ -388,10 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     rec.valid = 1;
                     rec.b = c.b;
                     rec.u = c.u;
-                    rec.tile = seg_tile;
                     rec.tiles = c.tiles;
+                    rec.open_start = open_start;
                     rec.open_end = open_end;
-                    rec.at = seg_at;
+                    rec.start = c.start + line.lead();
                 }
             } else {
                 const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
@@ -416,11 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     if (a.weights && lane % 4 == 0) buf.lse[row_at] = log_sum(m[i], l[i]);
                 }
             }
-            seg_at = at;
-            seg_tile = 0;
-            fresh = true;
-            if (at < hi) advance(a, c, units);
-        }
+        } while (next_unit(a, line, c, units));
         cp_async_wait<0>();
     }
     __syncthreads();
@@ -431,25 +497,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
             ++first;
             continue;
         }
-        int last = first, next = first, count = 0;
-        int8_t chain[2 * kWarps];           // the unit's records
-        for (;;) {
-            chain[count++] = (int8_t)last;
-            if (!records[last].open_end) break;
+        int last = first, next = first;     // the unit's records: the valid ones of first .. last
+        while (records[last].open_end) {
             do ++next; while (next < 2 * kWarps && !records[next].valid);
             if (next >= 2 * kWarps) break;
             last = next;
         }
         const Record rec = records[first];
-        const bool before = rec.at - rec.tile < block_lo, after = records[last].open_end;
+        const bool before = rec.open_start, after = records[last].open_end;
         const int hk = rec.u / chunks, g0 = (rec.u % chunks) * R;
         for (int i = tid; i < R * D / 4; i += kThreads) {
             const int r = i / (D / 4), col = (i % (D / 4)) * 4;
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            join<D, R>(r, col, count,
-                       [&](int j) {
-                           const int k = chain[j];
+            join<D, R>(r, col, last - first + 1,
+                       [&](int j) -> const float* {
+                           const int k = first + j;
+                           if (!records[k].valid) return nullptr;
                            return reinterpret_cast<const float*>(
                                k % 2 ? smem + (k / 2) * S::kRing : smem + kWarps * S::kRing + (k / 2) * S::kPart);
                        },
@@ -464,8 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         }
         if (before || after) {
             // the block that brings a unit's last part joins them all
-            const int64_t start = rec.at - rec.tile;
-            const int c0 = (int)(start / per), c1 = (int)((start + rec.tiles - 1) / per);
+            const int c0 = (int)(rec.start / per), c1 = (int)((rec.start + rec.tiles - 1) / per);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
