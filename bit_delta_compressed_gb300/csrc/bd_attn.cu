@@ -57,14 +57,13 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
         w.decode.lse = reinterpret_cast<float*>(take((size_t)batch * q_heads * sizeof(float)));
         w.decode.scores = reinterpret_cast<float*>(take((size_t)batch * q_heads * w.decode.score_stride * sizeof(float)));
     }
-    const int64_t tiles = most_tiles(tokens, batch, q_heads / kv_heads), units = tiles * kv_heads;
+    const int64_t tiles = most_tiles(tokens, batch, q_heads / kv_heads);
     w.plan.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
     w.plan.tiles = reinterpret_cast<RowTile*>(take((size_t)tiles * sizeof(RowTile)));
-    w.plan.order = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
-    w.plan.req_unit = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
+    w.plan.starts = reinterpret_cast<int4*>(take((size_t)tile_blocks() * sizeof(int4)));
+    w.plan.order = reinterpret_cast<int2*>(take((size_t)batch * sizeof(int2)));
+    w.plan.req_tile = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
     w.plan.req_row = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
-    w.plan.unit_row = reinterpret_cast<int64_t*>(take((size_t)units * sizeof(int64_t)));
-    w.plan.unit_segs = reinterpret_cast<int2*>(take((size_t)units * sizeof(int2)));
     // parts: every row once, and one unit's rows more for each thread block; a prefill
     // of so many rows that it is not split leaves none
     int64_t rows = split_below() * kPartRows;
@@ -129,7 +128,7 @@ bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32
     DecodeBuffers buf = w.decode;
     buf.with_prefix = P > 0;
     if (P > 0) {
-        const bd_status done = launch_plan(a, w.plan, 1, stream);
+        const bd_status done = launch_plan(a, w.plan, stream);
         if (done != BD_OK) return done;
     }
     bd_status done = launch_decode(a, c->head_dim, buf, stream);

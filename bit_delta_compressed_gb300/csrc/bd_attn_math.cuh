@@ -130,23 +130,38 @@ struct RowTile {
 };
 struct PlanHead {
     int64_t tiles, line, per;// row tiles, blocks of all units, blocks of a thread block
+    int64_t split;           // whether the blocks are cut into equal parts
 };
 struct TilePlan {
     PlanHead* head;
     RowTile* tiles;
-    int32_t* order;          // requests sorted by prefix
-    int32_t *req_unit, *req_row;  // of a request: unit of its row tile and head 0 (-1: no prefix), first row in it
-    int64_t* unit_row;       // first row of a unit's part from block 0
-    int2* unit_segs;         // first block and number of parts
+    int4* starts;            // of each thread block: row tile, head and block that its part begins with
+    int2* order;             // requests sorted by prefix: request, position of its query
+    int32_t* req_tile;       // prefixes: a request's row tile, -1 for none; prefill: its first one
+    int32_t* req_row;        // prefixes: its first row of the unit
     float* o;                // unnormalised parts of rows,
     float2* ml;              // their maximum (log2) and sum
 };
+
+// Where a unit's parts lie: of thread blocks first .. first + n - 1, its row r in the
+// first of them at row0 + r, each next one kPartRows further.
+struct Parts {
+    int64_t row0;
+    int32_t n;
+};
+__device__ __forceinline__ Parts parts_of(const RowTile& t, const PlanHead& head, int Hk, int hk, int G) {
+    const int64_t start = t.line * Hk + (int64_t)hk * t.blocks, first = start / head.per;
+    Parts p;
+    p.n = (int32_t)((start + t.blocks - 1) / head.per - first) + 1;
+    p.row0 = t.rows_before * Hk + (int64_t)hk * t.tokens * G + first * kPartRows;
+    return p;
+}
 
 int tile_blocks();
 int64_t split_below();       // units from which on a prefill is not split
 int64_t most_tiles(int64_t tokens, int64_t batch, int G);
 bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
-bd_status launch_plan(const Args& a, const TilePlan& plan, int split, cudaStream_t stream);
+bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream);
 bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, const DecodeBuffers& buf, cudaStream_t stream);
 
 int decode_blocks();

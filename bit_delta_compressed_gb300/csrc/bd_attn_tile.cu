@@ -37,6 +37,7 @@ using namespace sm100;
 constexpr int kKeys = 128;                 // of a block
 constexpr int kThreads = 384;
 constexpr uint32_t kLimit = 1u << 20;      // polls of a wait
+constexpr int kSplitPrice = 8;             // blocks that joining the parts costs about as much as
 constexpr float kGrow = 8.f;               // powers of two that a maximum may grow before a rescale
 
 // Which of a tensor map's outer dimensions is which.
@@ -99,8 +100,10 @@ __device__ __forceinline__ int last_at_most(const T* table, int n, X x) {
     return lo;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
+constexpr int kCached = 512;              // requests that the plan keeps in shared memory
 
+// Sum of the threads before this one; the block's total.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t* total) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     int64_t incl = v;
@@ -122,57 +125,50 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t*
 
 // Lays out the row tiles of a call (one block).  Prefill: every request's rows in
 // tiles of whole tokens.  Prefixes: the requests sorted by prefix (stably), every
-// prefix's requests in tiles.
+// prefix's requests in tiles.  `split`: whether a prefill may be split; it is where
+// a block's equal part of the line, with the parts' price, is less than the longest
+// unit.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const TilePlan plan, int blocks, int split) {
     extern __shared__ int32_t counts[];     // [P + 1] of each prefix, then its first place
-    grid_go_on();
     __shared__ int64_t part[kPlanThreads / 32];
+    __shared__ Request cached[kCached];
+    __shared__ int32_t first_tile[kCached];
+    __shared__ int longest;
+    grid_go_on();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per_tile = tokens_of_tile(a.G);
     int tiles = 0;
+    for (int b = tid; b < min(a.B, kCached); b += kPlanThreads) cached[b] = read_request(a, b);
+    if (tid == 0) longest = 0;
+    if (!a.cu_q)
+        for (int p = tid; p <= a.P; p += kPlanThreads) counts[p] = 0;
+    __syncthreads();
+    auto request = [&](int b) { return b < kCached ? cached[b] : read_request(a, b); };
     if (a.cu_q) {
         for (int base = 0; base < a.B; base += kPlanThreads) {
             const int b = base + tid;
-            int n = 0;
-            if (b < a.B) n = (read_request(a, b).rows + per_tile - 1) / per_tile;
+            const int n = b < a.B ? (request(b).rows + per_tile - 1) / per_tile : 0;
             int64_t all;
             const int first = tiles + (int)block_scan(n, part, &all);
-            if (b < a.B) plan.req_unit[b] = first;
+            if (b < a.B) {
+                if (b < kCached) first_tile[b] = first;
+                plan.req_tile[b] = first;
+            }
             tiles += (int)all;
         }
-        __syncthreads();
-        for (int i = tid; i < tiles; i += kPlanThreads) {
-            const int b = last_at_most(plan.req_unit, a.B, i);
-            const Request r = read_request(a, b);
-            RowTile t{};
-            const int i0 = (i - plan.req_unit[b]) * per_tile;
-            t.slot[0] = r.pslot;
-            t.slot[1] = r.slot;
-            t.row0 = r.row0 + i0;
-            t.tokens = min(per_tile, r.rows - i0);
-            t.t0 = r.plen + r.len - r.rows + i0;
-            const int end = min(r.plen + r.len, t.t0 + t.tokens);
-            set_keys(a, t, r.plen, window_lo(a, t.t0), max(0, end - r.plen));
-            plan.tiles[i] = t;
-        }
     } else {
-        for (int p = tid; p <= a.P; p += kPlanThreads) counts[p] = 0;
-        __syncthreads();
         for (int b = tid; b < a.B; b += kPlanThreads) {
-            const Request r = read_request(a, b);
-            plan.req_unit[b] = -1;
-            if (r.plen > 0) atomicAdd(counts + a.prefix_ids[b], 1);
+            if (request(b).plen > 0) atomicAdd(counts + a.prefix_ids[b], 1);
+            else plan.req_tile[b] = -1;
         }
         __syncthreads();
         int first = 0;
         for (int base = 0; base < a.P; base += kPlanThreads) {
             const int p = base + tid;
             const int n = p < a.P ? counts[p] : 0;
-            int64_t all;
+            int64_t all, all_tiles;
             const int at = first + (int)block_scan(n, part, &all);
-            const int tile = tiles;
-            int64_t all_tiles;
-            const int t0 = tile + (int)block_scan((n + per_tile - 1) / per_tile, part, &all_tiles);
+            const int t0 = tiles + (int)block_scan((n + per_tile - 1) / per_tile, part, &all_tiles);
             if (p < a.P) counts[p] = at;
             // what every tile of the group shares
             for (int i = 0; i * per_tile < n; ++i) {
@@ -191,76 +187,92 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
             // stable placement, 32 requests at a time
             for (int base = 0; base < a.B; base += 32) {
                 const int b = base + lane;
-                int id = -1;
+                int id = -1, pos = 0;
                 if (b < a.B) {
-                    const Request r = read_request(a, b);
+                    const Request r = request(b);
                     id = r.plen > 0 ? a.prefix_ids[b] : -1;
+                    pos = r.plen + r.len - 1;
                 }
                 const unsigned same = __match_any_sync(0xffffffffu, id);
                 const int rank = __popc(same & ((1u << lane) - 1));
                 const int at = id >= 0 ? counts[id] : 0;
                 __syncwarp();
                 if (id >= 0) {
-                    plan.order[at + rank] = b;
+                    plan.order[at + rank] = make_int2(b, pos);
                     if (rank == 0) counts[id] = at + __popc(same);
                 }
                 __syncwarp();
             }
         }
         __syncthreads();
-        // a warp a tile: the earliest key that its requests see
+        // a warp a tile: where its requests are, and the earliest key that they see
         for (int i = warp; i < tiles; i += kPlanThreads / 32) {
-            RowTile t = plan.tiles[i];
-            int lo = a.window > 0 ? 0x7fffffff : 0;
-            for (int j = lane; j < t.tokens; j += 32) {
-                const int b = plan.order[t.row0 + j];
-                if (a.window > 0) {
-                    const Request r = read_request(a, b);
-                    lo = min(lo, window_lo(a, r.plen + r.len - 1));
-                }
-                plan.req_unit[b] = i * a.Hk;
-                plan.req_row[b] = j * a.G;
+            const int row0 = plan.tiles[i].row0, n = plan.tiles[i].tokens;
+            int lo = 0x7fffffff;
+            for (int j = lane; j < n; j += 32) {
+                const int2 r = plan.order[row0 + j];
+                lo = min(lo, window_lo(a, r.y));
+                plan.req_tile[r.x] = i;
+                plan.req_row[r.x] = j * a.G;
             }
-            for (int x = 16; x; x >>= 1) lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, x));
-            if (lane == 0) {
-                set_keys(a, t, t.off, lo, 0);
-                plan.tiles[i] = t;
-            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            if (lane == 0) plan.tiles[i].lo_min = lo;
         }
-        __syncthreads();
-    }
-    if (!split) {
-        if (tid == 0) *plan.head = PlanHead{tiles, 0, 0};
-        return;
     }
     __syncthreads();
-    // the line of blocks
+    // the tiles, and their places on the line of blocks
     int64_t line = 0, rows = 0;
+    int mine = 0;                           // blocks of this thread's tile among the first
+    int64_t mine_at = 0;
     for (int base = 0; base < tiles; base += kPlanThreads) {
         const int i = base + tid;
-        int64_t all, n = i < tiles ? plan.tiles[i].blocks : 0;
-        const int64_t at = line + block_scan(n, part, &all);
+        RowTile t{};
+        if (i < tiles) {
+            if (a.cu_q) {
+                const int b = a.B <= kCached ? last_at_most(first_tile, a.B, i) : last_at_most(plan.req_tile, a.B, i);
+                const Request r = request(b);
+                const int i0 = (i - (b < kCached ? first_tile[b] : plan.req_tile[b])) * per_tile;
+                t.slot[0] = r.pslot;
+                t.slot[1] = r.slot;
+                t.row0 = r.row0 + i0;
+                t.tokens = min(per_tile, r.rows - i0);
+                t.t0 = r.plen + r.len - r.rows + i0;
+                const int end = min(r.plen + r.len, t.t0 + t.tokens);
+                set_keys(a, t, r.plen, window_lo(a, t.t0), max(0, end - r.plen));
+            } else {
+                t = plan.tiles[i];
+                set_keys(a, t, t.off, t.lo_min, 0);
+            }
+        }
+        int64_t all, all_rows;
+        t.line = line + block_scan(t.blocks, part, &all);
+        t.rows_before = rows + block_scan(t.tokens * a.G, part, &all_rows);
         line += all;
-        int64_t all_rows;
-        const int64_t r = rows + block_scan(i < tiles ? plan.tiles[i].tokens * a.G : 0, part, &all_rows);
         rows += all_rows;
         if (i < tiles) {
-            plan.tiles[i].line = at;
-            plan.tiles[i].rows_before = r;
+            plan.tiles[i] = t;
+            atomicMax(&longest, t.blocks);
+        }
+        if (base == 0) {
+            mine = t.blocks;
+            mine_at = t.line;
         }
     }
     __syncthreads();
-    line *= a.Hk;
-    const int64_t per = max((int64_t)1, (line + blocks - 1) / blocks);
-    for (int64_t u = tid; u < (int64_t)tiles * a.Hk; u += kPlanThreads) {
-        const int i = (int)(u / a.Hk), hk = (int)(u % a.Hk);
-        const RowTile& t = plan.tiles[i];
-        const int64_t start = t.line * a.Hk + (int64_t)hk * t.blocks;
-        const int c0 = (int)(start / per), c1 = (int)((start + t.blocks - 1) / per);
-        plan.unit_segs[u] = make_int2(c0, c1 - c0 + 1);
-        plan.unit_row[u] = t.rows_before * a.Hk + (int64_t)hk * t.tokens * a.G;
+    const int64_t per = max((int64_t)1, (line * a.Hk + blocks - 1) / blocks);
+    if (split && (!a.cu_q || longest > per + kSplitPrice)) {
+        for (int i = tid; i < tiles; i += kPlanThreads) {
+            const int n = i < kPlanThreads ? mine : plan.tiles[i].blocks;
+            const int64_t at = (i < kPlanThreads ? mine_at : plan.tiles[i].line) * a.Hk, end = at + (int64_t)n * a.Hk;
+            for (int64_t c = (at + per - 1) / per; c * per < end; ++c) {
+                const int64_t in = c * per - at;
+                plan.starts[c] = make_int4(i, (int)(in / n), (int)(in % n), 0);
+            }
+        }
+    } else {
+        split = 0;
     }
-    if (tid == 0) *plan.head = PlanHead{tiles, line, per};
+    if (tid == 0) *plan.head = PlanHead{tiles, line * a.Hk, per, split};
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -410,9 +422,9 @@ __device__ __forceinline__ RowOf row_of(const Args& a, const TilePlan& plan, con
     o.row = t.row0 + token;
     int pos = t.t0 + token;
     if (!a.cu_q) {
-        o.row = plan.order[o.row];
-        const Request rq = read_request(a, o.row);
-        pos = rq.plen + rq.len - 1;
+        const int2 r = plan.order[o.row];
+        o.row = r.x;
+        pos = r.y;
     }
     o.hi = pos + 1;
     o.lo = window_lo(a, pos);
@@ -422,15 +434,13 @@ __device__ __forceinline__ RowOf row_of(const Args& a, const TilePlan& plan, con
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     tile_kernel(const Args a, const TilePlan plan, const __grid_constant__ CUtensorMap kmap,
-                const __grid_constant__ CUtensorMap vmap, const MapOrder order, int split) {
+                const __grid_constant__ CUtensorMap vmap, const MapOrder order) {
     using T = Tile<D>;
     constexpr int NK = T::kK, NV = T::kV;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[2], s_full[2], s_free, p_full[2],
         pv_done[2], drained[2];
     __shared__ uint32_t tmem_at;
-    __shared__ int start[2];
-    __shared__ int64_t line_at[2];
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
     // Waits of a whole warp.  All lanes poll (a complete phase costs ~100 cycles so, one
@@ -472,23 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     grid_wait();                              // the plan
     grid_go_on();
     const PlanHead head = *plan.head;
+    const bool split = head.split;
     Walk walk{};
     if (split) {
         walk.at = min(head.line, head.per * blockIdx.x);
         walk.end = min(head.line, walk.at + head.per);
-        for (int i = tid; i < head.tiles; i += kThreads) {
-            const int64_t lo = plan.tiles[i].line * a.Hk, n = plan.tiles[i].blocks;
-            if (walk.at < walk.end && walk.at >= lo && walk.at < lo + n * a.Hk) {
-                start[0] = i;
-                line_at[0] = walk.at - lo;
-            }
-        }
-        __syncthreads();
         if (walk.at < walk.end) {
-            walk.tile = start[0];
-            const int n = plan.tiles[walk.tile].blocks;
-            walk.hk = (int)(line_at[0] / n);
-            walk.first = (int)(line_at[0] % n);
+            const int4 start = plan.starts[blockIdx.x];
+            walk.tile = start.x;
+            walk.hk = start.y;
+            walk.first = start.z;
         }
     } else {
         // the last tile of a prompt has the most keys: begin there
@@ -639,16 +642,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next.skipped += coming.last - coming.first;
             }
             if (!more) return;
-            const uint4* from = reinterpret_cast<const uint4*>(a.q + (int64_t)max(next.row, 0) * a.q_stride + (int64_t)next.head * D);
-            const uint32_t to = q_at + g * T::kQ + (tid % 128) * 128;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = next.row >= 0 ? from[c] : make_uint4(0, 0, 0, 0);
+            // D / 8 lanes a row
+            constexpr int L = D / 8, at_once = 32 / L;
+#pragma unroll 8
+            for (int i = 0; i < 32 / at_once; ++i) {
+                const int in_warp = i * at_once + lane / L, rr = (warp % 4) * 32 + in_warp, c = lane % L;
+                const int row = __shfl_sync(0xffffffffu, next.row, in_warp), head = __shfl_sync(0xffffffffu, next.head, in_warp);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row >= 0) v = reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.q_stride + (int64_t)head * D)[c];
                 v.x ^= flip;
                 v.y ^= flip;
                 v.z ^= flip;
                 v.w ^= flip;
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + (c / 8) * (kKeys * 128) + (((c % 8) ^ (tid % 8)) << 4)),
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + g * T::kQ + rr * 128 + (c / 8) * (kKeys * 128) + (((c % 8) ^ (rr % 8)) << 4)),
                              "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                              : "memory");
             }
@@ -781,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = now.row, head_at = now.head;
             const float inv = inverse(l);
             const int64_t part_row =
-                split ? plan.unit_row[(int64_t)s.tile * a.Hk + s.hk] + (int64_t)blockIdx.x * kPartRows + r : 0;
+                split ? (plan.tiles[s.tile].rows_before * a.Hk + (int64_t)s.hk * plan.tiles[s.tile].tokens * a.G) + (int64_t)blockIdx.x * kPartRows + r : 0;
             if (split && real) plan.ml[part_row] = make_float2(m, l);
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
@@ -841,16 +847,18 @@ __device__ __forceinline__ uint2 result(float4 o, float l) {
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan plan) {
     grid_wait();
-    const int64_t units = plan.head->tiles * a.Hk;
+    const PlanHead head = *plan.head;
+    if (!head.split) return;
+    const int64_t units = head.tiles * a.Hk;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const RowTile& t = plan.tiles[u / a.Hk];
         const int hk = (int)(u % a.Hk), rows = t.tokens * a.G;
-        const int2 seg = plan.unit_segs[u];
+        const Parts parts = parts_of(t, head, a.Hk, hk, a.G);
         for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
             const int r = i / (D / 4), col = (i % (D / 4)) * 4;
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_parts<D>(plan, plan.unit_row[u] + (int64_t)seg.x * kPartRows + r, seg.y, col, m, l, o);
+            add_parts<D>(plan, parts.row0 + r, parts.n, col, m, l, o);
             const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
             *reinterpret_cast<uint2*>(a.out + to) = result(o, l);
         }
@@ -868,11 +876,10 @@ __global__ void __launch_bounds__(256) join_prefix_kernel(const Args a, const Ti
     const float2 ml = buf.own_ml[row];
     float m = ml.x, l = ml.y;
     float4 o = *reinterpret_cast<const float4*>(buf.own + row * D + col);
-    const int unit0 = plan.req_unit[b];
-    if (unit0 >= 0) {
-        const int u = unit0 + h / a.G;
-        const int2 seg = plan.unit_segs[u];
-        add_parts<D>(plan, plan.unit_row[u] + (int64_t)seg.x * kPartRows + plan.req_row[b] + h % a.G, seg.y, col, m, l, o);
+    const int tile = plan.req_tile[b];
+    if (tile >= 0) {
+        const Parts parts = parts_of(plan.tiles[tile], *plan.head, a.Hk, h / a.G, a.G);
+        add_parts<D>(plan, parts.row0 + plan.req_row[b] + h % a.G, parts.n, col, m, l, o);
     }
     *reinterpret_cast<uint2*>(a.out + row * D + col) = result(o, l);
     if (a.weights && col == 0) buf.lse[row] = log_sum(m, l);
@@ -904,13 +911,13 @@ bool cache_map(CUtensorMap* map, MapOrder* order, const void* base, const Args& 
 }
 
 template <int D>
-bd_status launch_kernel(const Args& a, const TilePlan& plan, int split, cudaStream_t stream) {
+bd_status launch_kernel(const Args& a, const TilePlan& plan, cudaStream_t stream) {
     const void* kernel = reinterpret_cast<const void*>(tile_kernel<D>);
     if (!set_smem_attr(kernel, Tile<D>::kSmem, D == 128 ? 8 : 9)) return BD_ERR_CUDA;
     CUtensorMap kmap, vmap;
     MapOrder order{};
     if (!cache_map(&kmap, &order, a.k, a, D) || !cache_map(&vmap, &order, a.v, a, D)) return BD_ERR_CUDA;
-    return launch_close(tile_kernel<D>, tile_blocks(), kThreads, Tile<D>::kSmem, stream, a, plan, kmap, vmap, order, split);
+    return launch_close(tile_kernel<D>, tile_blocks(), kThreads, Tile<D>::kSmem, stream, a, plan, kmap, vmap, order);
 }
 
 }  // namespace
@@ -921,17 +928,19 @@ int64_t most_tiles(int64_t tokens, int64_t batch, int G) { return tokens / (kPar
 int tile_blocks() { return decode_blocks(); }
 int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
 
-bd_status launch_plan(const Args& a, const TilePlan& plan, int split, cudaStream_t stream) {
-    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, tile_blocks(), split);
+// Whether a call's parts may be left in the workspace, which holds those of few rows.
+bool may_split(const Args& a) { return !a.cu_q || most_tiles(a.T, a.B, a.G) * a.Hk < split_below(); }
+
+bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream) {
+    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, tile_blocks(), may_split(a));
     return launch_status();
 }
 
 bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
-    const int split = most_tiles(a.T, a.B, a.G) * a.Hk < split_below();
-    bd_status st = launch_plan(a, plan, split, stream);
+    bd_status st = launch_plan(a, plan, stream);
     if (st != BD_OK) return st;
-    st = head_dim == 128 ? launch_kernel<128>(a, plan, split, stream) : launch_kernel<64>(a, plan, split, stream);
-    if (st != BD_OK || !split) return st;
+    st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
+    if (st != BD_OK || !may_split(a)) return st;
     const dim3 grid((unsigned)tile_blocks(), 8);
     return head_dim == 128 ? launch_close(join_kernel<128>, grid, 256, 0, stream, a, plan)
                            : launch_close(join_kernel<64>, grid, 256, 0, stream, a, plan);
@@ -939,7 +948,7 @@ bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cuda
 
 bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, const DecodeBuffers& buf,
                           cudaStream_t stream) {
-    const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, 1, stream) : launch_kernel<64>(a, plan, 1, stream);
+    const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
     if (st != BD_OK) return st;
     const unsigned blocks = (unsigned)(((int64_t)a.B * a.Hq * (head_dim / 4) + 255) / 256);
     return head_dim == 128 ? launch_close(join_prefix_kernel<128>, blocks, 256, 0, stream, a, plan, buf)
