@@ -64,6 +64,7 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
     w.plan.order = reinterpret_cast<int2*>(take((size_t)batch * sizeof(int2)));
     w.plan.req_tile = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
     w.plan.req_row = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
+    w.plan.sorted_q = reinterpret_cast<__nv_bfloat16*>(take((size_t)batch * q_heads * head_dim * sizeof(__nv_bfloat16)));
     // parts: every row once, and one unit's rows more for each thread block; a prefill
     // of so many rows that it is not split leaves none
     int64_t rows = split_below() * kPartRows;
@@ -131,7 +132,7 @@ bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32
         const bd_status done = launch_plan(a, w.plan, stream);
         if (done != BD_OK) return done;
     }
-    bd_status done = launch_decode(a, c->head_dim, buf, stream);
+    bd_status done = launch_decode(a, c->head_dim, buf, w.plan, stream);
     if (done == BD_OK && P > 0) done = launch_prefixes(a, c->head_dim, w.plan, buf, stream);
     if (done == BD_OK && weights) done = launch_weigh(a, buf, stream);
     return done;

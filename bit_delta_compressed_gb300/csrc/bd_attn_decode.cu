@@ -192,7 +192,7 @@ __device__ __forceinline__ void finish(const Args& a, const DecodeBuffers& buf, 
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf, const TilePlan plan) {
     using S = Shape<D, R>;
     constexpr int NT = D / 8;              // 8-wide column tiles of the output
     extern __shared__ __align__(128) uint8_t smem[];
@@ -552,7 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         }
         first = last + 1;
     }
-    if (buf.with_prefix) grid_wait();
+    if (buf.with_prefix) {
+        // the plan is there: the queries in the order of the prefixes, for the tiles
+        grid_wait();
+        const int sorted = plan.head->sorted, chunks_q = a.Hq * D / 8;
+        for (int i = blockIdx.x; i < sorted; i += gridDim.x) {
+            const uint4* from = reinterpret_cast<const uint4*>(a.q + (int64_t)plan.order[i].x * a.q_stride);
+            uint4* to = reinterpret_cast<uint4*>(plan.sorted_q + (int64_t)i * a.Hq * D);
+            for (int j = tid; j < chunks_q; j += kThreads) to[j] = from[j];
+        }
+    }
 }
 
 // weights[slot, h, key] += sum over the group's heads of exp(score - log of the
@@ -574,12 +583,12 @@ __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBu
 }
 
 template <int D, int R>
-bd_status launch_shape(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {
+bd_status launch_shape(const Args& a, const DecodeBuffers& buf, const TilePlan& plan, cudaStream_t stream) {
     const void* kernel = reinterpret_cast<const void*>(decode_kernel<D, R>);
     if (!set_smem_attr(kernel, Shape<D, R>::kSmem, D == 128 ? (R == 8 ? 4 : 5) : (R == 8 ? 6 : 7))) return BD_ERR_CUDA;
     if (buf.with_prefix)       // beside the one block that lays out the prefixes' tiles
-        return launch_close(decode_kernel<D, R>, decode_blocks() > 1 ? decode_blocks() - 1 : 1, kThreads, Shape<D, R>::kSmem, stream, a, buf);
-    decode_kernel<D, R><<<decode_blocks(), kThreads, Shape<D, R>::kSmem, stream>>>(a, buf);
+        return launch_close(decode_kernel<D, R>, decode_blocks() > 1 ? decode_blocks() - 1 : 1, kThreads, Shape<D, R>::kSmem, stream, a, buf, plan);
+    decode_kernel<D, R><<<decode_blocks(), kThreads, Shape<D, R>::kSmem, stream>>>(a, buf, plan);
     return launch_status();
 }
 
@@ -589,9 +598,9 @@ int decode_blocks() { return sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks; 
 
 size_t decode_parts_bytes(int head_dim) { return (size_t)2 * decode_blocks() * (16 * head_dim + 32) * sizeof(float); }
 
-bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, cudaStream_t stream) {
-    if (a.G <= 8) return head_dim == 128 ? launch_shape<128, 8>(a, buf, stream) : launch_shape<64, 8>(a, buf, stream);
-    return head_dim == 128 ? launch_shape<128, 16>(a, buf, stream) : launch_shape<64, 16>(a, buf, stream);
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const TilePlan& plan, cudaStream_t stream) {
+    if (a.G <= 8) return head_dim == 128 ? launch_shape<128, 8>(a, buf, plan, stream) : launch_shape<64, 8>(a, buf, plan, stream);
+    return head_dim == 128 ? launch_shape<128, 16>(a, buf, plan, stream) : launch_shape<64, 16>(a, buf, plan, stream);
 }
 
 bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {

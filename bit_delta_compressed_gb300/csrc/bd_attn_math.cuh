@@ -130,7 +130,8 @@ struct RowTile {
 };
 struct PlanHead {
     int64_t tiles, line, per;// row tiles, blocks of all units, blocks of a thread block
-    int64_t split;           // whether the blocks are cut into equal parts
+    int32_t split;           // whether the blocks are cut into equal parts
+    int32_t sorted;          // requests with a prefix
 };
 struct TilePlan {
     PlanHead* head;
@@ -139,6 +140,7 @@ struct TilePlan {
     int2* order;             // requests sorted by prefix: request, position of its query
     int32_t* req_tile;       // prefixes: a request's row tile, -1 for none; prefill: its first one
     int32_t* req_row;        // prefixes: its first row of the unit
+    __nv_bfloat16* sorted_q; // prefixes: the queries in the order of `order`
     float* o;                // unnormalised parts of rows,
     float2* ml;              // their maximum (log2) and sum
 };
@@ -166,7 +168,7 @@ bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, con
 
 int decode_blocks();
 size_t decode_parts_bytes(int head_dim);
-bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, cudaStream_t stream);
+bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, const TilePlan& plan, cudaStream_t stream);
 bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream);
 
 }  // namespace attn

@@ -5,7 +5,8 @@
 // query head of the group) pairs, so that a group's heads read their keys once.
 // 4 head_dim flops a row and key against 4 head_dim bytes a key: with 256 rows
 // the tensor cores bound it.  One block a SM: two warps load keys and values by TMA
-// through two rings, two issue the tcgen05 products, two groups of four warps
+// through two rings, two issue the tcgen05 products (one of them loads the
+// queries, too), two groups of four warps
 // own 128 rows each, one thread a row.  Per block of 128 keys and group: S = Q K^T
 // (both operands in shared memory); the row's thread takes its 128 scores to
 // registers, keeps the running maximum and sum, and writes P as bf16 to tensor memory,
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
     grid_go_on();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per_tile = tokens_of_tile(a.G);
-    int tiles = 0;
+    int tiles = 0, sorted = 0;
     for (int b = tid; b < min(a.B, kCached); b += kPlanThreads) cached[b] = read_request(a, b);
     if (tid == 0) longest = 0;
     if (!a.cu_q)
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
             first += (int)all;
             tiles += (int)all_tiles;
         }
+        sorted = first;
         __syncthreads();
         if (warp == 0) {
             // stable placement, 32 requests at a time
@@ -272,7 +274,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
     } else {
         split = 0;
     }
-    if (tid == 0) *plan.head = PlanHead{tiles, line * a.Hk, per, split};
+    if (tid == 0) *plan.head = PlanHead{tiles, line * a.Hk, per, split, sorted};
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
@@ -360,26 +370,28 @@ struct Segment {
 // The segments of this block, in order: its part of the line, or whole units from
 // the last one on.
 struct Walk {
-    int64_t at, end, stride;                  // places on the line; units
-    int tile, hk, first;
+    int64_t left;                             // places of the part that are left
+    int tile, hk, first;                      // the unit to come (tile < 0: none)
+    int back_tiles, back_heads;               // how far the next whole unit lies before it
     bool whole;
     __device__ __forceinline__ bool next(const Args& a, const TilePlan& plan, Segment& s) {
-        if (whole) {
-            if (at < 0) return false;
-            s.tile = (int)(at / a.Hk);
-            s.hk = (int)(at % a.Hk);
-            s.first = 0;
-            s.last = plan.tiles[s.tile].blocks;
-            at -= stride;
-            return true;
-        }
-        if (at >= end) return false;
+        if (whole ? tile < 0 : left <= 0) return false;
         const int n = plan.tiles[tile].blocks;
         s.tile = tile;
         s.hk = hk;
         s.first = first;
-        s.last = (int)min((int64_t)n, first + (end - at));
-        at += s.last - first;
+        s.last = n;
+        if (whole) {
+            tile -= back_tiles;
+            hk -= back_heads;
+            if (hk < 0) {
+                hk += a.Hk;
+                --tile;
+            }
+            return true;
+        }
+        if (n - first > left) s.last = first + (int)left;
+        left -= s.last - first;
         first = 0;
         if (++hk == a.Hk) {
             hk = 0;
@@ -433,12 +445,12 @@ __device__ __forceinline__ RowOf row_of(const Args& a, const TilePlan& plan, con
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    tile_kernel(const Args a, const TilePlan plan, const __grid_constant__ CUtensorMap kmap,
+    tile_kernel(const Args a, const TilePlan plan, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap, const MapOrder order) {
     using T = Tile<D>;
     constexpr int NK = T::kK, NV = T::kV;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full[2], s_full[2], s_free, p_full[2],
+    __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full, q_empty, s_full[2], s_free, p_full[2],
         pv_done[2], drained[2];
     __shared__ uint32_t tmem_at;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -466,10 +478,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_empty + i, 1);
         }
         mbar_init(&s_free, 4);
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
         mbar_init(drained, 1);
         mbar_init(drained + 1, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 4);
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 4);
             mbar_init(pv_done + i, 1);
@@ -485,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool split = head.split;
     Walk walk{};
     if (split) {
-        walk.at = min(head.line, head.per * blockIdx.x);
-        walk.end = min(head.line, walk.at + head.per);
-        if (walk.at < walk.end) {
+        const int64_t at = min(head.line, head.per * blockIdx.x);
+        walk.left = min(head.line - at, head.per);
+        if (walk.left > 0) {
             const int4 start = plan.starts[blockIdx.x];
             walk.tile = start.x;
             walk.hk = start.y;
@@ -495,8 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // the last tile of a prompt has the most keys: begin there
-        walk.at = head.tiles * a.Hk - 1 - blockIdx.x;
-        walk.stride = gridDim.x;
+        const int64_t u = head.tiles * a.Hk - 1 - blockIdx.x;
+        walk.tile = u < 0 ? -1 : (int)(u / a.Hk);
+        walk.hk = u < 0 ? 0 : (int)(u % a.Hk);
+        walk.back_tiles = gridDim.x / a.Hk;
+        walk.back_heads = gridDim.x % a.Hk;
         walk.whole = true;
     }
     const uint32_t tmem = tmem_at;
@@ -544,29 +560,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
         if (warp == 9) {
             const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
-            uint32_t st = 0, phase = 0, n = 0, begun0 = 0, begun1 = 0;
+            uint32_t st = 0, phase = 0, n = 0, units = 0;
             bool ok = true;
             Segment s;
+            if (lane == 0) prefetch_tensormap(&qmap);
             while (ok && walk.next(a, plan, s)) {
                 const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
+                const int row0 = plan.tiles[s.tile].row0;
+                // the unit's queries, in the order of its rows (the tile's whole room: what
+                // lies behind its tokens belongs to rows that are none)
+                if (units > 0) ok = wait(&q_empty, units - 1, 14);
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&q_full, T::kHalves * tokens_of_tile(a.G) * a.G * 128);
+                    for (int h = 0; h < T::kHalves; ++h) tma_load_3d(q_at + h * kPartRows * 128, &qmap, &q_full, h * 64, s.hk * a.G, row0);
+                }
+                __syncwarp();
+                ok = wait(&q_full, units++, 5);
                 for (int i = s.first; ok && i < s.last; ++i) {
+                    const uint64_t kd = k_desc + (st * T::kQ >> 4);
                     ok = wait(k_full + st, phase, 4);
                     for (int g = 0; ok && g < groups; ++g) {
-                        if (i == s.first) ok = wait(q_full + g, g ? begun1++ : begun0++, 5);
+                        const uint64_t qd = q_desc + (g * 128 * 128 >> 4);
+                        const bool last = g == groups - 1;
                         // the scores before, of whichever group, are in registers
                         if (n > 0) ok = ok && wait(&s_free, n - 1, 6);
                         if (!ok) break;
                         ++n;
                         tc_fence_after();
                         if (elect_one()) {
-                            const uint64_t qd = q_desc + (g * T::kQ >> 4), kd = k_desc + (st * T::kQ >> 4);
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t off = ((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4;
-                                mma_ss(tmem, qd + off, kd + off, idesc_s, k > 0);
-                            }
+                            for (int k = 0; k < D / 16; ++k)
+                                mma_ss(tmem, qd + (((k / 4) * (kPartRows * 128) + (k % 4) * 32) >> 4), kd + (((k / 4) * (kKeys * 128) + (k % 4) * 32) >> 4),
+                                       idesc_s, k > 0);
                             mma_commit(s_full + g);
-                            if (g == groups - 1) mma_commit(k_empty + st);
+                            if (last) mma_commit(k_empty + st);
+                            if (last && i + 1 == s.last) mma_commit(&q_empty);
                         }
                         __syncwarp();
                     }
@@ -621,14 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = warp / 4, r = g * 128 + tid % 128;
         const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
         const uint32_t s_at = tmem + lanes, p_at = s_at + 128 + g * 64, o_at = s_at + 256 + g * D;
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
         const float scale = fmaxf(fabsf(a.scale_log2), 1.2e-38f);   // never 0: a hidden score's -inf stays -inf
         int step = 0, put = 0;
         bool ok = true, more = true;
         Segment s, coming;
         RowOf now{}, next{};
-        // this thread's row of the next unit that its group has a part in: its query
-        // goes to shared memory, where the products read it
+        // this thread's row of the next unit that its group has a part in
         auto begin_next = [&]() {
             while ((more = walk.next(a, plan, coming))) {
                 const RowTile& t = plan.tiles[coming.tile];
@@ -641,26 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 next.skipped += coming.last - coming.first;
             }
-            if (!more) return;
-            // D / 8 lanes a row
-            constexpr int L = D / 8, at_once = 32 / L;
-#pragma unroll 8
-            for (int i = 0; i < 32 / at_once; ++i) {
-                const int in_warp = i * at_once + lane / L, rr = (warp % 4) * 32 + in_warp, c = lane % L;
-                const int row = __shfl_sync(0xffffffffu, next.row, in_warp), head = __shfl_sync(0xffffffffu, next.head, in_warp);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row >= 0) v = reinterpret_cast<const uint4*>(a.q + (int64_t)row * a.q_stride + (int64_t)head * D)[c];
-                v.x ^= flip;
-                v.y ^= flip;
-                v.z ^= flip;
-                v.w ^= flip;
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(q_at + g * T::kQ + rr * 128 + (c / 8) * (kKeys * 128) + (((c % 8) ^ (rr % 8)) << 4)),
-                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full + g);
         };
         begin_next();
         while (more) {
@@ -692,6 +699,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(&s_free);
                 // asked now, needed later: P and O are free when the block before is done
                 const bool free = step == 0 || mbar_test(pv_done + g, (step - 1) & 1);
+                if (a.scale_log2 < 0.f) {
+                    // scores are scaled by its size
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c) {
+                        asm volatile("" : "+f"(v[c]));
+                        v[c] = -v[c];
+                    }
+                }
                 if (!(p0 + kKeys <= min(src_end, hi_all) && (p0 >= lo_all || p0 + kKeys <= a.sinks))) {
                     const int n = min(now.hi, src_end) - p0, from = now.lo - p0, sinks = a.sinks - p0;
 #pragma unroll
@@ -778,7 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 --run;
             }
             if (!ok) break;
-            // the last scores are in registers: the next query may take this one's place
             begin_next();
             ok = wait(pv_done + g, step - 1, 14);
             if (!ok) break;
@@ -907,17 +921,27 @@ bool cache_map(CUtensorMap* map, MapOrder* order, const void* base, const Args& 
         box[i + 1] = d[i].box;
         *d[i].place = i;
     }
-    return make_tmap_bf16_4d_sw128(map, base, dims, strides, box);
+    return make_tmap_bf16_sw128_nd(map, base, 4, dims, strides, box);
+}
+
+// Rows of q: a box is the heads of a group of a tile's tokens.
+bool query_map(CUtensorMap* map, const void* q, int64_t q_stride, const Args& a, int D) {
+    const uint64_t dims[3] = {(uint64_t)D, (uint64_t)a.Hq, (uint64_t)a.T};
+    const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)q_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)(kPartRows / a.G)};
+    return make_tmap_bf16_sw128_nd(map, q, 3, dims, strides, box);
 }
 
 template <int D>
 bd_status launch_kernel(const Args& a, const TilePlan& plan, cudaStream_t stream) {
     const void* kernel = reinterpret_cast<const void*>(tile_kernel<D>);
     if (!set_smem_attr(kernel, Tile<D>::kSmem, D == 128 ? 8 : 9)) return BD_ERR_CUDA;
-    CUtensorMap kmap, vmap;
+    CUtensorMap qmap, kmap, vmap;
     MapOrder order{};
+    // (a decode step's queries were put in the order of the prefixes)
+    if (!query_map(&qmap, a.cu_q ? a.q : plan.sorted_q, a.cu_q ? a.q_stride : (int64_t)a.Hq * D, a, D)) return BD_ERR_CUDA;
     if (!cache_map(&kmap, &order, a.k, a, D) || !cache_map(&vmap, &order, a.v, a, D)) return BD_ERR_CUDA;
-    return launch_close(tile_kernel<D>, tile_blocks(), kThreads, Tile<D>::kSmem, stream, a, plan, kmap, vmap, order);
+    return launch_close(tile_kernel<D>, tile_blocks(), kThreads, Tile<D>::kSmem, stream, a, plan, qmap, kmap, vmap, order);
 }
 
 }  // namespace

@@ -24,10 +24,10 @@ bool make_tmap_u8_sw128(CUtensorMap* map, const void* base, uint64_t rows, uint6
 // bytes per row), no swizzle.
 bool make_tmap_bits(CUtensorMap* map, const void* base, uint64_t rows, uint64_t words, uint32_t box_rows);
 
-// 4-D bf16 tensor with the 128-byte swizzle: dims and box innermost first
-// (box[0] is 64), the byte strides of dims 1 to 3.
-bool make_tmap_bf16_4d_sw128(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides[3],
-                             const uint32_t box[4]);
+// bf16 tensor of rank 2 to 4 with the 128-byte swizzle: dims and box innermost
+// first (box[0] is 64), the byte strides of the dims from the second on.
+bool make_tmap_bf16_sw128_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box);
 
 // Opt a kernel into `bytes` of dynamic shared memory (once per device).
 bool set_smem_attr(const void* kernel, int bytes, int slot);

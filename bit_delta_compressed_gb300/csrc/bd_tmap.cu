@@ -61,12 +61,18 @@ bool make_tmap_bits(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tmap_bf16_4d_sw128(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t strides[3],
-                             const uint32_t box[4]) {
-    if (!encoder()) return false;
-    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
-    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]}, es[4] = {1, 1, 1, 1};
-    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, s, b, es,
+bool make_tmap_bf16_sw128_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                             const uint32_t* box) {
+    if (rank < 2 || rank > 4 || !encoder()) return false;
+    cuuint64_t d[4], s[3];
+    cuuint32_t b[4], es[4];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i) s[i - 1] = strides[i - 1];
+    }
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, s, b, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
