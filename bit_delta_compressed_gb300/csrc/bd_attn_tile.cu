@@ -423,11 +423,11 @@ __device__ __forceinline__ Block block_of(const RowTile& t, int i) {
 // [lo, hi) that it sees; a row that is none sees all.
 struct RowOf {
     int row, head, lo, hi;
-    int lo_unit;                               // the least lo of the unit's rows
+    int lo_unit, rows;                         // the least lo of the unit's rows, their number
     int skipped;                               // blocks of units before it without a part of its group
 };
 __device__ __forceinline__ RowOf row_of(const Args& a, const TilePlan& plan, const RowTile& t, int hk, int r) {
-    RowOf o{-1, hk * a.G, 0, 0x7fffffff, t.lo_min, 0};
+    RowOf o{-1, hk * a.G, 0, 0x7fffffff, t.lo_min, t.tokens * a.G, 0};
     const int token = r / a.G;
     if (token >= t.tokens) return o;
     o.head += r - token * a.G;
@@ -801,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = now.row, head_at = now.head;
             const float inv = inverse(l);
             const int64_t part_row =
-                split ? (plan.tiles[s.tile].rows_before * a.Hk + (int64_t)s.hk * plan.tiles[s.tile].tokens * a.G) + (int64_t)blockIdx.x * kPartRows + r : 0;
-            if (split && real) plan.ml[part_row] = make_float2(m, l);
+                split ? plan.tiles[s.tile].rows_before * a.Hk + (int64_t)s.hk * now.rows + (int64_t)blockIdx.x * kPartRows : 0;
+            if (split && real) plan.ml[part_row + r] = make_float2(m, l);
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -810,9 +810,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld_wait();
                 if (!real) continue;
                 if (split) {
-                    float4* to = reinterpret_cast<float4*>(plan.o + part_row * D + c);
+                    // four values of all rows, then the next four: a warp writes 512 bytes in a row
+                    float4* to = reinterpret_cast<float4*>(plan.o + part_row * D) + (int64_t)(c / 4) * now.rows + r;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int e = 0; e < 8; ++e) to[(int64_t)e * now.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 } else {
                     uint4* to = reinterpret_cast<uint4*>(a.out + ((int64_t)row * a.Hq + head_at) * D + c);
 #pragma unroll
@@ -828,20 +829,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Adds part s = 0 .. n - 1 of a row, kPartRows rows apart from row r0 on, four values.
+// Adds the parts of row r of a unit of `rows` rows, four values.
 template <int D>
-__device__ __forceinline__ void add_parts(const TilePlan& plan, int64_t r0, int n, int col, float& m, float& l, float4& o) {
+__device__ __forceinline__ void add_parts(const TilePlan& plan, const Parts& p, int rows, int r, int col, float& m, float& l, float4& o) {
     float top = m;
-    for (int s = 0; s < n; ++s) top = fmaxf(top, plan.ml[r0 + (int64_t)s * kPartRows].x);
+#pragma unroll 4
+    for (int s = 0; s < p.n; ++s) top = fmaxf(top, plan.ml[p.row0 + (int64_t)s * kPartRows + r].x);
     const float use = top == -INFINITY ? 0.f : top;
     float f = exp2_approx(m - use);
     l *= f;
     o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-        const int64_t at = r0 + (int64_t)s * kPartRows;
-        const float2 ml = plan.ml[at];
-        const float4 v = *reinterpret_cast<const float4*>(plan.o + at * D + col);
+    for (int s = 0; s < p.n; ++s) {
+        const int64_t at = p.row0 + (int64_t)s * kPartRows;
+        const float2 ml = plan.ml[at + r];
+        const float4 v = reinterpret_cast<const float4*>(plan.o + at * D)[(int64_t)(col / 4) * rows + r];
         f = exp2_approx(ml.x - use);
         l += f * ml.y;
         o.x += f * v.x;
@@ -869,10 +871,10 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan 
         const int hk = (int)(u % a.Hk), rows = t.tokens * a.G;
         const Parts parts = parts_of(t, head, a.Hk, hk, a.G);
         for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
-            const int r = i / (D / 4), col = (i % (D / 4)) * 4;
+            const int r = i % rows, col = i / rows * 4;
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_parts<D>(plan, parts.row0 + r, parts.n, col, m, l, o);
+            add_parts<D>(plan, parts, rows, r, col, m, l, o);
             const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
             *reinterpret_cast<uint2*>(a.out + to) = result(o, l);
         }
@@ -884,16 +886,18 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan 
 template <int D>
 __global__ void __launch_bounds__(256) join_prefix_kernel(const Args a, const TilePlan plan, const DecodeBuffers buf) {
     grid_wait();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / (D / 4);
+    // 8 rows of one column after the other, then the next column
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, eight = i / (8 * (D / 4));
+    const int64_t row = eight * 8 + i % 8;
     if (row >= (int64_t)a.B * a.Hq) return;
-    const int col = (int)(i % (D / 4)) * 4, b = (int)(row / a.Hq), h = (int)(row % a.Hq);
+    const int col = (int)(i / 8 % (D / 4)) * 4, b = (int)(row / a.Hq), h = (int)(row % a.Hq);
     const float2 ml = buf.own_ml[row];
     float m = ml.x, l = ml.y;
     float4 o = *reinterpret_cast<const float4*>(buf.own + row * D + col);
     const int tile = plan.req_tile[b];
     if (tile >= 0) {
-        const Parts parts = parts_of(plan.tiles[tile], *plan.head, a.Hk, h / a.G, a.G);
-        add_parts<D>(plan, parts.row0 + plan.req_row[b] + h % a.G, parts.n, col, m, l, o);
+        const RowTile& t = plan.tiles[tile];
+        add_parts<D>(plan, parts_of(t, *plan.head, a.Hk, h / a.G, a.G), t.tokens * a.G, plan.req_row[b] + h % a.G, col, m, l, o);
     }
     *reinterpret_cast<uint2*>(a.out + row * D + col) = result(o, l);
     if (a.weights && col == 0) buf.lse[row] = log_sum(m, l);
@@ -974,7 +978,7 @@ bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, con
                           cudaStream_t stream) {
     const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
     if (st != BD_OK) return st;
-    const unsigned blocks = (unsigned)(((int64_t)a.B * a.Hq * (head_dim / 4) + 255) / 256);
+    const unsigned blocks = (unsigned)((((int64_t)a.B * a.Hq + 7) / 8 * 8 * (head_dim / 4) + 255) / 256);
     return head_dim == 128 ? launch_close(join_prefix_kernel<128>, blocks, 256, 0, stream, a, plan, buf)
                            : launch_close(join_prefix_kernel<64>, blocks, 256, 0, stream, a, plan, buf);
 }
