@@ -23,6 +23,7 @@ Two layers:
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 
 _PKG = Path(__file__).resolve().parent
@@ -126,15 +127,25 @@ def check(code: int, where: str) -> None:
 
 # -- torch layer ---------------------------------------------------------------
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream=None) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
     torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    try:                                          # 0.1 us; the Stream object takes 3
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return int(torch.cuda.current_stream().cuda_stream)
 
 
 def _dtype_code(t) -> int:
@@ -292,55 +303,57 @@ def linear_grouped(x, w_base, alphas, bits_ptrs, V: int, y, workspace, path: str
 
 # -- attention over a key/value cache -----------------------------------------------
 
-def _cache_desc(k_cache, v_cache):
-    """``bd_kv_cache`` of two [slots, capacity, kv_heads, head_dim] bf16 CUDA
-    tensors; any strides the C ABI takes (a transposed view is one layout)."""
+# (A decode step of one request takes a few microseconds on the GPU: what a call
+# asks of its tensors it asks once, and the cache's description is packed, not built
+# as an object.)
+_DESC = struct.Struct("@PPqqiiqqq")        # KVCacheDesc's layout
+
+
+def _desc_of(k, v):
     torch = _torch()
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, strides = k.shape, k.stride()
+    if len(shape) != 4 or v.shape != shape or v.stride() != strides:
         raise ValueError("k and v must be 4-D [slots, capacity, kv_heads, head_dim] of one shape and strides")
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise TypeError("the cache must be bfloat16")
-    if not k_cache.is_cuda or not v_cache.is_cuda or k_cache.stride(3) != 1:
+    S, C, H, D = shape
+    ss, st, sh, sd = strides
+    if not (k.is_cuda and v.is_cuda) or sd != 1:
         raise ValueError("the cache must be CUDA tensors with contiguous head_dim")
-    S, C, H, D = k_cache.shape
     # the stride of a dimension of one entry is never used, and torch leaves it open
-    strides = [st if n > 1 else D for st, n in zip(k_cache.stride()[:3], (S, C, H))]
-    return KVCacheDesc(k_cache.data_ptr(), v_cache.data_ptr(), S, C, H, D, *strides)
+    return shape, _DESC.pack(k.data_ptr(), v.data_ptr(), S, C, H, D, ss if S > 1 else D, st if C > 1 else D,
+                             sh if H > 1 else D)
 
 
-def _int32(name, t, shape):
-    torch = _torch()
+def _int32(name, t, *shape):
     if t is None:
         return None
-    _need_cuda(t)
-    if t.dtype != torch.int32 or tuple(t.shape) != shape:
-        raise ValueError("%s must be an int32 tensor of shape %s" % (name, shape))
+    if t.dtype is not _torch().int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, shape))
     return t.data_ptr()
 
 
-def _attn_args(q, k_cache, out):
+def _attn_args(q, D, out):
     torch = _torch()
-    if q.dim() != 3 or q.shape[2] != k_cache.shape[3] or q.dtype != torch.bfloat16 or not q.is_cuda:
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_cuda:
         raise ValueError("q must be a bf16 CUDA tensor [rows, q_heads, head_dim]")
-    if q.stride(2) != 1 or (q.shape[1] > 1 and q.stride(1) != q.shape[2]):
+    T, H, _ = shape
+    if strides[2] != 1 or (H > 1 and strides[1] != D):
         raise ValueError("the heads of a row of q must be contiguous")
-    stride = q.stride(0) if q.shape[0] > 1 else q.shape[1] * q.shape[2]
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    _need_cuda(out)
-    if out.shape != q.shape or out.dtype != torch.bfloat16:
-        raise ValueError("out must be bf16 and of q's shape")
-    return stride, out
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    elif out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 CUDA tensor of q's shape")
+    return T, H, strides[0] if T > 1 else H * D, out
 
 
-def _weights_ptr(weights, k_cache):
-    torch = _torch()
+def _weights_ptr(weights, S, H, C):
     if weights is None:
         return None
-    _need_cuda(weights)
-    S, C, H, _ = k_cache.shape
-    if weights.dtype != torch.float32 or tuple(weights.shape) != (S, H, C):
-        raise ValueError("weights must be float32 [slots, kv_heads, capacity]")
+    if (weights.dtype is not _torch().float32 or weights.shape != (S, H, C) or not weights.is_cuda
+            or not weights.is_contiguous()):
+        raise ValueError("weights must be contiguous float32 [slots, kv_heads, capacity]")
     return weights.data_ptr()
 
 
@@ -350,8 +363,8 @@ def _prefix_args(prefix_ids, prefix_slots, prefix_lens, B):
     if prefix_ids is None or prefix_slots is None or prefix_lens is None:
         raise ValueError("prefix_ids, prefix_slots and prefix_lens go together")
     P = prefix_slots.numel()
-    return (_int32("prefix_ids", prefix_ids, (B,)), _int32("prefix_slots", prefix_slots, (P,)),
-            _int32("prefix_lens", prefix_lens, (P,)), P)
+    return (_int32("prefix_ids", prefix_ids, B), _int32("prefix_slots", prefix_slots, P),
+            _int32("prefix_lens", prefix_lens, P), P)
 
 
 def attn_workspace(tokens: int, batch: int, q_heads: int, kv_heads: int, head_dim: int, weigh_len: int = 0,
@@ -382,18 +395,20 @@ def attn_decode_prefix(q, k_cache, v_cache, lens, prefix_ids, prefix_slots, pref
     the ``prefix_lens[p]`` keys in slot ``prefix_slots[p]``, p = ``prefix_ids[b]``
     (-1: none), which are read once for all requests that name them (see
     ``bitdelta_attn_decode_prefix``)."""
-    desc = _cache_desc(k_cache, v_cache)
-    stride, out = _attn_args(q, k_cache, out)
-    B, H, D = q.shape
+    (S, C, Hk, D), desc = _desc_of(k_cache, v_cache)
+    B, H, stride, out = _attn_args(q, D, out)
+    rest = (window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, S, Hk, C), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _stream(stream))
     ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
-    args = [q.data_ptr(), stride, B, H, ctypes.byref(desc), _int32("slots", slots, (B,)), _int32("lens", lens, (B,))]
-    rest = [window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, k_cache), out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(stream)]
+    lib = get_lib()
     if P == 0:
-        check(get_lib().bitdelta_attn_decode(*args, *rest), "bitdelta_attn_decode")
+        code = lib.bitdelta_attn_decode(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, B),
+                                        _int32("lens", lens, B), *rest)
     else:
-        check(get_lib().bitdelta_attn_decode_prefix(*args, ids, pslots, plens, P, *rest),
-              "bitdelta_attn_decode_prefix")
+        code = lib.bitdelta_attn_decode_prefix(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, B),
+                                               _int32("lens", lens, B), ids, pslots, plens, P, *rest)
+    if code != BD_OK:
+        check(code, "bitdelta_attn_decode" if P == 0 else "bitdelta_attn_decode_prefix")
     return out
 
 
@@ -403,15 +418,13 @@ def attn_prefill(q, k_cache, v_cache, cu_q, lens, workspace, slots=None, window:
     ``cu_q[b+1]`` of q [T, q_heads, head_dim] are request b's newest tokens,
     whose keys are the last of its ``lens[b]`` keys in the cache (see
     ``bitdelta_attn_prefill``).  Returns out [T, q_heads, head_dim]."""
-    desc = _cache_desc(k_cache, v_cache)
-    stride, out = _attn_args(q, k_cache, out)
-    T, H, D = q.shape
+    (_, _, _, D), desc = _desc_of(k_cache, v_cache)
+    T, H, stride, out = _attn_args(q, D, out)
     B = lens.numel()
     ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
-    check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, ctypes.byref(desc),
-                                          _int32("slots", slots, (B,)), _int32("cu_q", cu_q, (B + 1,)),
-                                          _int32("lens", lens, (B,)), ids, pslots, plens, P, window, sinks,
-                                          D ** -0.5 if scale is None else scale, out.data_ptr(),
+    check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, desc, _int32("slots", slots, B),
+                                          _int32("cu_q", cu_q, B + 1), _int32("lens", lens, B), ids, pslots, plens, P,
+                                          window, sinks, D ** -0.5 if scale is None else scale, out.data_ptr(),
                                           workspace.data_ptr(), workspace.numel(), _stream(stream)),
           "bitdelta_attn_prefill")
     return out
@@ -432,15 +445,13 @@ def cache_evict(k_cache, v_cache, weights, lens, src, dst, budget: int, workspac
     all, of every head (see ``bitdelta_cache_evict``).  ``lens`` holds a length
     for every slot.  ``kept`` (int32 [n, kv_heads, budget]) receives the kept
     keys' old places."""
-    desc = _cache_desc(k_cache, v_cache)
-    S, _, H, _ = k_cache.shape
+    (S, C, H, _), desc = _desc_of(k_cache, v_cache)
     n = src.numel()
     if weights is None:
         raise ValueError("weights are needed")
-    check(get_lib().bitdelta_cache_evict(ctypes.byref(desc), _weights_ptr(weights, k_cache),
-                                         _int32("lens", lens, (S,)), _int32("src", src, (n,)),
-                                         _int32("dst", dst, (n,)), n, budget, sinks, recent,
-                                         _int32("kept", kept, (n, H, budget)), workspace.data_ptr(),
+    check(get_lib().bitdelta_cache_evict(desc, _weights_ptr(weights, S, H, C), _int32("lens", lens, S),
+                                         _int32("src", src, n), _int32("dst", dst, n), n, budget, sinks, recent,
+                                         _int32("kept", kept, n, H, budget), workspace.data_ptr(),
                                          workspace.numel(), _stream(stream)), "bitdelta_cache_evict")
 
 
