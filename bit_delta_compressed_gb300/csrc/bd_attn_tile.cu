@@ -306,6 +306,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
         : "r"(taddr));
 }
 
+// The way of a wait that one try did not end.
+__device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, unsigned* status, unsigned where, volatile unsigned* dead) {
+    for (uint32_t i = 0; i < kLimit; ++i)
+        if (mbar_try_wait(bar, parity) || *dead) return;
+    *dead = 1;
+    report(status, BD_ERR_TIMEOUT);
+    atomicCAS(status + 2, 0u, where);
+}
+// The end of what is in flight, however the waits before went.
+__device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kLimit; ++i)
+        if (mbar_try_wait(bar, parity)) return;
+}
+
 // Whether a phase is complete, without waiting.
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -453,16 +467,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], q_full, q_empty, s_full[2], s_free, p_full[2],
         pv_done[2], drained[2];
     __shared__ uint32_t tmem_at;
+    __shared__ unsigned dead;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
-    // Waits of a whole warp.  All lanes poll (a complete phase costs ~100 cycles so, one
-    // lane's poll handed on by a shuffle ~260).
+    // Waits.  One that runs out ends all others at once; the roles then go through their
+    // steps without waiting, so that nothing hangs, and the status word tells.
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
-        return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity & 1, kLimit, status, where, status + 2));
+        if (!mbar_try_wait(bar, parity & 1)) wait_on(bar, parity & 1, status, where, &dead);
     };
-    auto lane_wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
-        return mbar_wait(bar, parity & 1, kLimit, status, where, status + 2);
+    auto warp_waits = [&](uint64_t* bar, uint32_t parity, unsigned where) {
+        wait(bar, parity, where);
+        __syncwarp();
     };
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t q_at = base, k_at = base + 2 * T::kQ, v_at = k_at + NK * T::kQ;
@@ -477,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(v_full + i, 1);
             mbar_init(v_empty + i, 1);
         }
+        dead = 0;
         mbar_init(&s_free, 4);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
@@ -532,15 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tensormap(map);
             int st = 0, put = 0;
             uint32_t phase = 1;                    // of the fill before the one to come
-            bool ok = true;
             Segment s;
-            while (ok && walk.next(a, plan, s)) {
+            while (walk.next(a, plan, s)) {
                 const RowTile t = plan.tiles[s.tile];
                 for (int i = s.first; i < s.last; ++i, ++put) {
                     const Block b = block_of(t, i);
                     auto at = [&](int dim) { return dim == order.token ? b.key : dim == order.head ? s.hk : b.slot; };
-                    if (put >= stages) ok = lane_wait(empty + st, phase, 1);
-                    if (!ok) break;
+                    if (put >= stages) wait(empty + st, phase, 1);
                     mbar_expect_tx(full + st, T::kQ);
                     for (int h = 0; h < T::kHalves; ++h)
                         tma_load_4d(to + st * T::kQ + h * kKeys * 128, map, full + st, h * 64, at(0), at(1), at(2));
@@ -551,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // nothing may still be on its way into shared memory when the block ends
-            for (int i = max(0, put - stages); i < put; ++i) lane_wait(full + i % stages, i / stages, 3);
+            for (int i = max(0, put - stages); i < put; ++i) settle(full + i % stages, i / stages & 1);
         }
         // Two warps issue the products, one the scores' and one the outputs'.  A product's
         // issue takes as long as the product (64 cycles for 128 x 128 x 16), and the waits
@@ -561,31 +575,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 9) {
             const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
             uint32_t st = 0, phase = 0, n = 0, units = 0;
-            bool ok = true;
             Segment s;
             if (lane == 0) prefetch_tensormap(&qmap);
-            while (ok && walk.next(a, plan, s)) {
+            while (walk.next(a, plan, s)) {
                 const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
                 const int row0 = plan.tiles[s.tile].row0;
                 // the unit's queries, in the order of its rows (the tile's whole room: what
                 // lies behind its tokens belongs to rows that are none)
-                if (units > 0) ok = wait(&q_empty, units - 1, 14);
-                if (!ok) break;
+                if (units > 0) warp_waits(&q_empty, units - 1, 2);
                 if (elect_one()) {
                     mbar_expect_tx(&q_full, T::kHalves * tokens_of_tile(a.G) * a.G * 128);
                     for (int h = 0; h < T::kHalves; ++h) tma_load_3d(q_at + h * kPartRows * 128, &qmap, &q_full, h * 64, s.hk * a.G, row0);
                 }
                 __syncwarp();
-                ok = wait(&q_full, units++, 5);
-                for (int i = s.first; ok && i < s.last; ++i) {
+                wait(&q_full, units++, 3);
+                for (int i = s.first; i < s.last; ++i) {
                     const uint64_t kd = k_desc + (st * T::kQ >> 4);
-                    ok = wait(k_full + st, phase, 4);
-                    for (int g = 0; ok && g < groups; ++g) {
+                    wait(k_full + st, phase, 4);
+                    for (int g = 0; g < groups; ++g) {
                         const uint64_t qd = q_desc + (g * 128 * 128 >> 4);
                         const bool last = g == groups - 1;
                         // the scores before, of whichever group, are in registers
-                        if (n > 0) ok = ok && wait(&s_free, n - 1, 6);
-                        if (!ok) break;
+                        if (n > 0) wait(&s_free, n - 1, 5);
+                        __syncwarp();
                         ++n;
                         tc_fence_after();
                         if (elect_one()) {
@@ -608,20 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the products in flight end before the tensor memory is given back
             if (elect_one()) mma_commit(drained);
             __syncwarp();
-            wait(drained, 0, 7);
+            settle(drained, 0);
         }
         if (warp == 10) {
             const uint64_t v_desc = desc_v(v_at);
             uint32_t st = 0, phase = 0, done0 = 0, done1 = 0;
-            bool ok = true;
             Segment s;
-            while (ok && walk.next(a, plan, s)) {
+            while (walk.next(a, plan, s)) {
                 const int groups = plan.tiles[s.tile].tokens * a.G > 128 ? 2 : 1;
-                for (int i = s.first; ok && i < s.last; ++i) {
-                    ok = wait(v_full + st, phase, 8);
-                    for (int g = 0; ok && g < groups; ++g) {
-                        ok = wait(p_full + g, g ? done1++ : done0++, 9);
-                        if (!ok) break;
+                for (int i = s.first; i < s.last; ++i) {
+                    wait(v_full + st, phase, 6);
+                    for (int g = 0; g < groups; ++g) {
+                        warp_waits(p_full + g, g ? done1++ : done0++, 7);
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t vd = v_desc + (st * T::kQ >> 4);
@@ -642,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (elect_one()) mma_commit(drained + 1);
             __syncwarp();
-            wait(drained + 1, 0, 10);
+            settle(drained + 1, 0);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -652,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_at = tmem + lanes, p_at = s_at + 128 + g * 64, o_at = s_at + 256 + g * D;
         const float scale = fmaxf(fabsf(a.scale_log2), 1.2e-38f);   // never 0: a hidden score's -inf stays -inf
         int step = 0, put = 0;
-        bool ok = true, more = true;
+        bool more = true;
         Segment s, coming;
         RowOf now{}, next{};
         // this thread's row of the next unit that its group has a part in
@@ -687,8 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     src_end = b.off + b.end;
                     run = b.run;
                 }
-                ok = wait(s_full + g, step, 11);
-                if (!ok) break;
+                warp_waits(s_full + g, step, 8);
                 tc_fence_after();
                 float v[kKeys];
 #pragma unroll
@@ -732,15 +741,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool rescales = i > s.first && grows;
                 if (i == s.first) m = mn;
                 if (__any_sync(0xffffffffu, rescales || edge || !free)) {
-                    if (step > 0) ok = wait(pv_done + g, step - 1, 12);
-                    if (!ok) break;
+                    if (step > 0) warp_waits(pv_done + g, step - 1, 9);
                     if (edge) {
                         // values that no row of the unit sees may be anything: they are
                         // multiplied by zero, so they have to be finite.  (The first group
                         // has a part in every unit and its product comes first.)
                         const int pos = p0 + tid, st = put % NV;
-                        ok = wait(v_full + st, put / NV, 13);
-                        if (!ok) break;
+                        warp_waits(v_full + st, put / NV, 10);
                         if (!(pos < src_end && (pos < a.sinks || pos >= now.lo_unit)))
 #pragma unroll
                             for (int c = 0; c < D / 8; ++c)
@@ -792,10 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p0 += kKeys;
                 --run;
             }
-            if (!ok) break;
             begin_next();
-            ok = wait(pv_done + g, step - 1, 14);
-            if (!ok) break;
+            warp_waits(pv_done + g, step - 1, 11);
             tc_fence_after();
             const bool real = now.row >= 0;
             const int row = now.row, head_at = now.head;
