@@ -53,7 +53,7 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
     w.decode.own = reinterpret_cast<float*>(take((size_t)batch * q_heads * head_dim * sizeof(float)));
     w.decode.own_ml = reinterpret_cast<float2*>(take((size_t)batch * q_heads * sizeof(float2)));
     if (weigh_len > 0) {
-        w.decode.score_stride = (int64_t)round_up((size_t)weigh_len, 4);
+        w.decode.score_stride = (int64_t)round_up((size_t)weigh_len, 16);   // whole tiles
         w.decode.lse = reinterpret_cast<float*>(take((size_t)batch * q_heads * sizeof(float)));
         w.decode.scores = reinterpret_cast<float*>(take((size_t)batch * q_heads * w.decode.score_stride * sizeof(float)));
     }

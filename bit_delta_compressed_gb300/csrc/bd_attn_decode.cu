@@ -351,17 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                         if (R == 16) s[t][2 + i] = in ? s[t][2 + i] * a.scale_log2 : -INFINITY;
                     }
                 if (a.weights) {
-                    // the raw scores, for the weights' pass over them
+                    // the scores, for the weights' pass over them (rows have room for whole tiles)
                     const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
 #pragma unroll
                     for (int i = 0; i < R / 8; ++i) {
                         const int r = g0 + row + 8 * i;
                         if (r >= a.G) continue;
-                        float* to = buf.scores + ((int64_t)c.b * a.Hq + hk * a.G + r) * buf.score_stride;
-                        if (x0 < c.k.n) to[x0] = s[0][2 * i];
-                        if (x0 + 1 < c.k.n) to[x0 + 1] = s[0][2 * i + 1];
-                        if (x0 + 8 < c.k.n) to[x0 + 8] = s[1][2 * i];
-                        if (x0 + 9 < c.k.n) to[x0 + 9] = s[1][2 * i + 1];
+                        float* to = buf.scores + ((int64_t)c.b * a.Hq + hk * a.G + r) * buf.score_stride + x0;
+                        *reinterpret_cast<float2*>(to) = make_float2(s[0][2 * i], s[0][2 * i + 1]);
+                        *reinterpret_cast<float2*>(to + 8) = make_float2(s[1][2 * i], s[1][2 * i + 1]);
                     }
                 }
                 uint32_t pf[4], pl[4];
@@ -605,7 +603,7 @@ bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, c
 
 bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {
     const int64_t heads = (int64_t)a.B * a.Hk, most = (a.capacity + 255) / 256;
-    int64_t x = (8 * (int64_t)sm_count() + heads - 1) / heads;
+    int64_t x = (64 * (int64_t)sm_count() + heads - 1) / heads;
     x = x < most ? x : most;
     return launch_close(weigh_kernel, dim3((unsigned)x, (unsigned)a.Hk, (unsigned)a.B), 256, 0, stream, a, buf);
 }
