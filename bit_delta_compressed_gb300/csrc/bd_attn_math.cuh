@@ -117,8 +117,8 @@ constexpr int kPartRows = 256;
 // ---- the tile kernel's plan (in the workspace) ---------------------------------
 // A row tile: `tokens` tokens (their rows of q begin at row0; for prefixes row0 is
 // a place in `order`) and the keys that any of them sees, as blocks of 128 of two
-// sources, the prefix (0) and the request's own keys (1): of each the blocks
-// [0, head) and [from, from + tail).
+// sources, the prefix (0) and the request's own keys (1): of each `head` blocks from
+// its first key on and `tail` blocks from key `from` on.
 struct RowTile {
     int32_t slot[2], head[2], from[2], tail[2];
     int32_t off;             // keys of the prefix: the own keys' positions begin there

@@ -54,20 +54,21 @@ struct Tile {
     static constexpr int kSmem = 1024 + (2 + kK + kV) * kQ;
 };
 
-// Blocks [0, head) and [from, from + tail) of a source.
+// Of a source: `head` blocks from its first key on, and `tail` blocks from key
+// `from` on (a copy may start at any key, so a window costs no block for its
+// alignment).
 struct Span {
     int32_t head, from, tail;
 };
 
+// Keys [0, min(sinks, hi)) and [lo, hi) of a source.
 __device__ __forceinline__ Span span_of(int lo, int hi, int sinks) {
-    // keys [0, min(sinks, hi)) and [lo, hi) of a source
     Span s;
     hi = max(hi, 0);
     lo = min(max(lo, 0), hi);
-    const int last = (hi + kKeys - 1) / kKeys;
-    s.head = min((min(max(sinks, 0), hi) + kKeys - 1) / kKeys, last);
-    s.from = max(lo / kKeys, s.head);
-    s.tail = max(last - s.from, 0);
+    s.head = (min(max(sinks, 0), hi) + kKeys - 1) / kKeys;
+    s.from = max(lo, s.head * kKeys);
+    s.tail = (max(hi - s.from, 0) + kKeys - 1) / kKeys;
     return s;
 }
 
@@ -424,7 +425,7 @@ __device__ __forceinline__ Block block_of(const RowTile& t, int i) {
     b.src = i >= t.head[0] + t.tail[0];
     if (b.src) i -= t.head[0] + t.tail[0];
     const int head = b.src ? t.head[1] : t.head[0], from = b.src ? t.from[1] : t.from[0];
-    b.key = (i < head ? i : from + i - head) * kKeys;
+    b.key = i < head ? i * kKeys : from + (i - head) * kKeys;
     b.slot = b.src ? t.slot[1] : t.slot[0];
     b.run = i < head ? head - i : head + (b.src ? t.tail[1] : t.tail[0]) - i;
     if (b.run < 1) b.run = 1;
