@@ -25,6 +25,7 @@ BAD_CACHES = [
     (dict(k=None), "BD_ERR_NULL"), (dict(v=None), "BD_ERR_NULL"), (dict(k=MISALIGNED), "BD_ERR_ALIGN"), (dict(v=MISALIGNED), "BD_ERR_ALIGN"),
     (dict(slots=0), "BD_ERR_SHAPE"), (dict(capacity=0), "BD_ERR_SHAPE"), (dict(capacity=2 ** 24 + 1), "BD_ERR_SHAPE"), (dict(kv_heads=0), "BD_ERR_SHAPE"),
     (dict(head_dim=96), "BD_ERR_SHAPE"), (dict(stride_token=0), "BD_ERR_SHAPE"), (dict(stride_slot=-8), "BD_ERR_SHAPE"), (dict(stride_head=132), "BD_ERR_ALIGN"),
+    (dict(stride_slot=2 ** 39), "BD_ERR_SHAPE"), (dict(slots=2 ** 24 + 1), "BD_ERR_SHAPE"),
 ]
 
 
@@ -82,6 +83,7 @@ def test_prefix_and_prefill_arguments(bd):
     assert prefix(bd, slots=None, ws=FAKE) == bd.BD_ERR_NULL
     assert prefix(bd, lens=None, ws=FAKE) == bd.BD_ERR_NULL
     assert prefix(bd, P=-1, ws=FAKE) == bd.BD_ERR_SHAPE
+    assert prefix(bd, P=8193, ws=FAKE) == bd.BD_ERR_SHAPE
     assert prefix(bd, ids=0x10001, ws=FAKE) == bd.BD_ERR_ALIGN
     assert prefix(bd) == bd.BD_ERR_WORKSPACE
     assert prefill(bd, cu=None) == bd.BD_ERR_NULL

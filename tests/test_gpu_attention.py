@@ -352,6 +352,51 @@ def test_workspace_is_reused_across_shapes(bd):
         ref.assert_close(bd.attn_prefill(q, k, v, cu, lens, ws), want, bound)
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30, 4.0])
+def test_scales(bd, scale):
+    """Negative scales, and zero: the mean of what is seen."""
+    g = gen(61)
+    n, hq, hk, d = 5, 8, 2, 64
+    k, v = make_cache(n + 1, 300, hk, d, g)
+    lens, ids, pslots, plens = i32([300, 1, 129, 20, 0]), i32([0, -1, 0, -1, 0]), i32([n]), i32([131])
+    how = dict(scale=scale, window=140, sinks=2)
+    q = queries(n, hq, d, g)
+    ws = bd.attn_workspace(300, n, hq, hk, d, device=DEV)
+    want, bound, _ = ref.attention(q, k, v, lens, **how)
+    ref.assert_close(bd.attn_decode(q, k, v, lens, ws, **how), want, bound)
+    how.update(prefix_ids=ids, prefix_slots=pslots, prefix_lens=plens)
+    want, bound, _ = ref.attention(q, k, v, lens, **how)
+    ref.assert_close(bd.attn_decode_prefix(q, k, v, lens, ids, pslots, plens, ws, scale=scale, window=140, sinks=2), want, bound)
+    q, cu = queries(260, hq, d, g), i32([0, 200, 201, 250, 260, 260])
+    want, bound, _ = ref.attention(q, k, v, lens, cu_q=cu, **how)
+    ref.assert_close(bd.attn_prefill(q, k, v, cu, lens, ws, **how), want, bound)
+
+
+def test_more_requests_than_the_plan_keeps(bd):
+    """700 requests, every one with a prefix of its own or of few, in decode and prefill."""
+    g = gen(67)
+    n, hq, hk, d = 700, 4, 2, 64
+    k, v = make_cache(2 * n, 50, hk, d, g)
+    lens = torch.randint(0, 51, (n,), generator=g, device=DEV, dtype=torch.int32)
+    plens = torch.randint(0, 51, (n,), generator=g, device=DEV, dtype=torch.int32)
+    pslots = (n + torch.randperm(n, generator=g, device=DEV)).to(torch.int32)
+    new = torch.minimum(torch.randint(0, 4, (n,), generator=g, device=DEV, dtype=torch.int32), lens)
+    cu = torch.cat([i32([0]), new.cumsum(0, dtype=torch.int32)])
+    ws = bd.attn_workspace(2100, n, hq, hk, d, device=DEV)
+    for few in (False, True):
+        ids = torch.randperm(n, generator=g, device=DEV).to(torch.int32)
+        if few:
+            ids = ids % 3 - 1
+        how = dict(window=60, sinks=3, prefix_ids=ids, prefix_slots=pslots, prefix_lens=plens)
+        q = queries(n, hq, d, g)
+        want, bound, _ = ref.attention(q, k, v, lens, **how)
+        ref.assert_close(bd.attn_decode_prefix(q, k, v, lens, ids, pslots, plens, ws, window=60, sinks=3), want, bound)
+        q = queries(int(cu[-1]), hq, d, g)
+        want, bound, _ = ref.attention(q, k, v, lens, cu_q=cu, **how)
+        ref.assert_close(bd.attn_prefill(q, k, v, cu, lens, ws, **how), want, bound)
+    assert bd.device_status(ws) == 0
+
+
 def test_empty_calls(bd):
     k, v = make_cache(2, 10, 2, 64, gen(1))
     ws = bd.attn_workspace(1, 1, 4, 2, 64, device=DEV)
