@@ -152,25 +152,40 @@ __device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int ch
 }
 
 // Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
-// gives a part's base, O [R][D] then (m, l) [R], or NULL for one that is none.
+// gives a part's base, O [R][D] then (m, l) [R].  Four at a time, so that their
+// loads are under way together.
 template <int D, int R, typename F>
 __device__ __forceinline__ void join(int row, int col, int count, F part, float& m, float& l, float4& o) {
-#pragma unroll 4
-    for (int s = 0; s < count; ++s)
-        if (const float* p = part(s)) m = fmaxf(m, p[R * D + 2 * row]);
-    const float use = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-    for (int s = 0; s < count; ++s) {
-        const float* p = part(s);
-        if (!p) continue;
-        const float2 ml = *reinterpret_cast<const float2*>(p + R * D + 2 * row);
-        const float f = exp2_approx(ml.x - use);
-        l += f * ml.y;
-        const float4 v = *reinterpret_cast<const float4*>(p + row * D + col);
-        o.x += f * v.x;
-        o.y += f * v.y;
-        o.z += f * v.z;
-        o.w += f * v.w;
+    for (int s0 = 0; s0 < count; s0 += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const float* p = part(min(s0 + s, count - 1));
+            ml[s] = *reinterpret_cast<const float2*>(p + R * D + 2 * row);
+            v[s] = *reinterpret_cast<const float4*>(p + row * D + col);
+        }
+        float top = m;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s0 + s >= count) ml[s] = make_float2(-INFINITY, 0.f);
+            top = fmaxf(top, ml[s].x);
+        }
+        const float use = top == -INFINITY ? 0.f : top;
+        float f = exp2_approx(m - use);
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s0 + s >= count) break;
+            f = exp2_approx(ml[s].x - use);
+            l += f * ml[s].y;
+            o.x += f * v[s].x;
+            o.y += f * v[s].y;
+            o.z += f * v[s].z;
+            o.w += f * v[s].w;
+        }
+        m = top;
     }
 }
 
@@ -199,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     __shared__ int64_t sums[kRuns + 1];
     __shared__ int longest[kRuns / 32];
     __shared__ Record records[2 * kWarps];
+    __shared__ int chain[2 * kWarps];
     __shared__ int last_block;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
@@ -489,31 +505,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     }
     __syncthreads();
 
-    // join the open units of this block's warps, run by run
-    for (int first = 0; first < 2 * kWarps;) {
-        if (!records[first].valid) {
-            ++first;
-            continue;
-        }
-        int last = first, next = first;     // the unit's records: the valid ones of first .. last
-        while (records[last].open_end) {
-            do ++next; while (next < 2 * kWarps && !records[next].valid);
-            if (next >= 2 * kWarps) break;
-            last = next;
-        }
-        const Record rec = records[first];
-        const bool before = rec.open_start, after = records[last].open_end;
-        const int hk = rec.u / chunks, g0 = (rec.u % chunks) * R;
+    // join the open units of this block's warps, one after the other: `chain` lists the
+    // records in their order, a unit's follow one another
+    unsigned valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && records[lane % (2 * kWarps)].valid);
+    if (warp == 0 && (valid >> lane & 1)) chain[__popc(valid & ((1u << lane) - 1))] = lane;
+    const int listed = __popc(valid);
+    __syncthreads();
+    for (int first = 0, next; first < listed; first = next) {
+        next = first + 1;
+        while (records[chain[next - 1]].open_end && next < listed) ++next;
+        const Record& rec = records[chain[first]];
+        const bool before = rec.open_start, after = records[chain[next - 1]].open_end;
+        const int hk = rec.u / chunks, g0 = (rec.u - hk * chunks) * R;
         for (int i = tid; i < R * D / 4; i += kThreads) {
             const int r = i / (D / 4), col = (i % (D / 4)) * 4;
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            join<D, R>(r, col, last - first + 1,
-                       [&](int j) -> const float* {
-                           const int k = first + j;
-                           if (!records[k].valid) return nullptr;
+            join<D, R>(r, col, next - first,
+                       [&](int j) {
+                           const int k = chain[first + j];
                            return reinterpret_cast<const float*>(
-                               k % 2 ? smem + (k / 2) * S::kRing : smem + kWarps * S::kRing + (k / 2) * S::kPart);
+                               smem + (k % 2 ? k / 2 * S::kRing : kWarps * S::kRing + k / 2 * S::kPart));
                        },
                        m, l, o);
             if (before || after) {
@@ -527,16 +539,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         if (before || after) {
             // the block that brings a unit's last part joins them all
             const int c0 = (int)(rec.start / per), c1 = (int)((rec.start + rec.tiles - 1) / per);
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
+                __threadfence();
                 const int n = atomicAdd(buf.tickets + c0, 1);
                 last_block = n == c1 - c0;
                 if (last_block) buf.tickets[c0] = 0;
+                __threadfence();
             }
             __syncthreads();
             if (last_block) {
-                __threadfence();
                 for (int i = tid; i < R * D / 4; i += kThreads) {
                     const int r = i / (D / 4), col = (i % (D / 4)) * 4;
                     float m = -INFINITY, l = 0.f;
@@ -548,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
             }
             __syncthreads();
         }
-        first = last + 1;
     }
     if (buf.with_prefix) {
         // the plan is there: the queries in the order of the prefixes, for the tiles
