@@ -804,28 +804,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_waits(pv_done + g, step - 1, 11);
             tc_fence_after();
             const bool real = now.row >= 0;
-            const int row = now.row, head_at = now.head;
             const float inv = inverse(l);
-            const int64_t part_row =
-                split ? plan.tiles[s.tile].rows_before * a.Hk + (int64_t)s.hk * now.rows + (int64_t)blockIdx.x * kPartRows : 0;
-            if (split && real) plan.ml[part_row + r] = make_float2(m, l);
+            if (split) {
+                const int64_t part_row = plan.tiles[s.tile].rows_before * a.Hk + (int64_t)s.hk * now.rows + (int64_t)blockIdx.x * kPartRows;
+                if (real) plan.ml[part_row + r] = make_float2(m, l);
+                // four values of all rows, then the next four: a warp writes 512 bytes in a row
+                float4* to = reinterpret_cast<float4*>(plan.o + part_row * D) + r;
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(o_at + c, o);
-                tmem_ld_wait();
-                if (!real) continue;
-                if (split) {
-                    // four values of all rows, then the next four: a warp writes 512 bytes in a row
-                    float4* to = reinterpret_cast<float4*>(plan.o + part_row * D) + (int64_t)(c / 4) * now.rows + r;
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_at + c, o);
+                    tmem_ld_wait();
+                    if (real)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) to[(int64_t)e * now.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
-                    uint4* to = reinterpret_cast<uint4*>(a.out + ((int64_t)row * a.Hq + head_at) * D + c);
+                        for (int e = 0; e < 8; ++e) to[(int64_t)(c / 4 + e) * now.rows] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            } else {
+                // four lanes exchange 16-byte pieces, so that they write 64 bytes of a row
+                // together: one lane a row would touch a line with every 16 bytes
+                int64_t at[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        to[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                           pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                for (int i = 0; i < 4; ++i) {
+                    const int row = __shfl_sync(0xffffffffu, now.row, lane / 4 * 4 + i), head_at = __shfl_sync(0xffffffffu, now.head, lane / 4 * 4 + i);
+                    at[i] = row < 0 ? -1 : ((int64_t)row * a.Hq + head_at) * D + lane % 4 * 8;
+                }
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(o_at + c, o);
+                    tmem_ld_wait();
+                    uint32_t x[4][4];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[e / 4][e % 4] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+                    for (int bit = 1; bit < 4; bit *= 2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(i & bit))
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const bool up = lane & bit;
+                                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[i][e] : x[i + bit][e], bit);
+                                    x[i][e] = up ? got : x[i][e];
+                                    x[i + bit][e] = up ? x[i + bit][e] : got;
+                                }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (at[i] >= 0) *reinterpret_cast<uint4*>(a.out + at[i] + c) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
                 }
             }
             tc_fence_before();
