@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
     __shared__ int64_t part[kPlanThreads / 32];
     __shared__ Request cached[kCached];
     __shared__ int32_t first_tile[kCached];
+    __shared__ int64_t lines[kPlanThreads];
     __shared__ int longest;
     grid_go_on();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -225,8 +226,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
     __syncthreads();
     // the tiles, and their places on the line of blocks
     int64_t line = 0, rows = 0;
-    int mine = 0;                           // blocks of this thread's tile among the first
-    int64_t mine_at = 0;
     for (int base = 0; base < tiles; base += kPlanThreads) {
         const int i = base + tid;
         RowTile t{};
@@ -256,21 +255,27 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
             plan.tiles[i] = t;
             atomicMax(&longest, t.blocks);
         }
-        if (base == 0) {
-            mine = t.blocks;
-            mine_at = t.line;
-        }
+        if (base == 0) lines[tid] = t.line;
     }
     __syncthreads();
     const int64_t per = max((int64_t)1, (line * a.Hk + blocks - 1) / blocks);
     if (split && (!a.cu_q || longest > per + kSplitPrice)) {
-        for (int i = tid; i < tiles; i += kPlanThreads) {
-            const int n = i < kPlanThreads ? mine : plan.tiles[i].blocks;
-            const int64_t at = (i < kPlanThreads ? mine_at : plan.tiles[i].line) * a.Hk, end = at + (int64_t)n * a.Hk;
-            for (int64_t c = (at + per - 1) / per; c * per < end; ++c) {
-                const int64_t in = c * per - at;
-                plan.starts[c] = make_int4(i, (int)(in / n), (int)(in % n), 0);
+        for (int c = tid; c < blocks && c * per < line * a.Hk; c += kPlanThreads) {
+            // (the tiles' places: on chip where they are few)
+            const int64_t x = c * per / a.Hk;
+            int i = last_at_most(lines, min(tiles, kPlanThreads), x);
+            if (tiles > kPlanThreads && plan.tiles[kPlanThreads].line <= x) {
+                int lo = kPlanThreads, hi = tiles;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (plan.tiles[mid].line <= x) lo = mid;
+                    else hi = mid;
+                }
+                i = lo;
             }
+            const int n = plan.tiles[i].blocks;
+            const int64_t in = c * per - plan.tiles[i].line * a.Hk;
+            plan.starts[c] = make_int4(i, (int)(in / n), (int)(in % n), 0);
         }
     } else {
         split = 0;
@@ -860,29 +865,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Adds the parts of row r of a unit of `rows` rows, four values.
+// Adds the parts of row r of a unit of `rows` rows, four values; four parts at a
+// time, so that their loads are under way together.
 template <int D>
 __device__ __forceinline__ void add_parts(const TilePlan& plan, const Parts& p, int rows, int r, int col, float& m, float& l, float4& o) {
-    float top = m;
-#pragma unroll 4
-    for (int s = 0; s < p.n; ++s) top = fmaxf(top, plan.ml[p.row0 + (int64_t)s * kPartRows + r].x);
-    const float use = top == -INFINITY ? 0.f : top;
-    float f = exp2_approx(m - use);
-    l *= f;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll 4
-    for (int s = 0; s < p.n; ++s) {
-        const int64_t at = p.row0 + (int64_t)s * kPartRows;
-        const float2 ml = plan.ml[at + r];
-        const float4 v = reinterpret_cast<const float4*>(plan.o + at * D)[(int64_t)(col / 4) * rows + r];
-        f = exp2_approx(ml.x - use);
-        l += f * ml.y;
-        o.x += f * v.x;
-        o.y += f * v.y;
-        o.z += f * v.z;
-        o.w += f * v.w;
+    for (int s0 = 0; s0 < p.n; s0 += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int64_t at = p.row0 + (int64_t)min(s0 + s, p.n - 1) * kPartRows;
+            ml[s] = plan.ml[at + r];
+            v[s] = reinterpret_cast<const float4*>(plan.o + at * D)[(int64_t)(col / 4) * rows + r];
+        }
+        float top = m;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s0 + s >= p.n) ml[s] = make_float2(-INFINITY, 0.f);
+            top = fmaxf(top, ml[s].x);
+        }
+        const float use = top == -INFINITY ? 0.f : top;
+        float f = exp2_approx(m - use);
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            if (s0 + s >= p.n) break;
+            f = exp2_approx(ml[s].x - use);
+            l += f * ml[s].y;
+            o.x += f * v[s].x;
+            o.y += f * v[s].y;
+            o.z += f * v[s].z;
+            o.w += f * v[s].w;
+        }
+        m = top;
     }
-    m = top;
 }
 
 __device__ __forceinline__ uint2 result(float4 o, float l) {
@@ -896,19 +913,18 @@ __global__ void __launch_bounds__(256) join_kernel(const Args a, const TilePlan 
     grid_wait();
     const PlanHead head = *plan.head;
     if (!head.split) return;
-    const int64_t units = head.tiles * a.Hk;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const RowTile& t = plan.tiles[u / a.Hk];
-        const int hk = (int)(u % a.Hk), rows = t.tokens * a.G;
-        const Parts parts = parts_of(t, head, a.Hk, hk, a.G);
-        for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
-            const int r = i % rows, col = i / rows * 4;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            add_parts<D>(plan, parts, rows, r, col, m, l, o);
-            const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
-            *reinterpret_cast<uint2*>(a.out + to) = result(o, l);
-        }
+    const int u = blockIdx.x;
+    if (u >= head.tiles * a.Hk) return;
+    const RowTile& t = plan.tiles[u / a.Hk];
+    const int hk = u % a.Hk, rows = t.tokens * a.G;
+    const Parts parts = parts_of(t, head, a.Hk, hk, a.G);
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * gridDim.y) {
+        const int r = i % rows, col = i / rows * 4;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        add_parts<D>(plan, parts, rows, r, col, m, l, o);
+        const int64_t to = ((int64_t)(t.row0 + r / a.G) * a.Hq + hk * a.G + r % a.G) * D + col;
+        *reinterpret_cast<uint2*>(a.out + to) = result(o, l);
     }
 }
 
@@ -1000,7 +1016,9 @@ bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cuda
     if (st != BD_OK) return st;
     st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
     if (st != BD_OK || !may_split(a)) return st;
-    const dim3 grid((unsigned)tile_blocks(), 8);
+    // (few units are joined by many blocks each)
+    const int64_t units = most_tiles(a.T, a.B, a.G) * a.Hk, each = 8 * (int64_t)tile_blocks() / units;
+    const dim3 grid((unsigned)units, (unsigned)(each < 4 ? 4 : each > 32 ? 32 : each));
     return head_dim == 128 ? launch_close(join_kernel<128>, grid, 256, 0, stream, a, plan)
                            : launch_close(join_kernel<64>, grid, 256, 0, stream, a, plan);
 }
