@@ -47,7 +47,7 @@ using namespace sm100;
 
 constexpr int kKeys = 128;                 // of a block
 constexpr int kThreads = 384;
-constexpr uint32_t kLimit = 1u << 20;      // polls of a wait
+constexpr uint32_t kLimit = 1u << 20;      // tries of a wait, of 1 us at most each
 // Blocks that joining the parts costs about as much as.  Split / whole: 64 new tokens on
 // 16,000 keys 42 / 197 us, on 2,000 25 / 36; but 700 tokens of a new prompt 48 / 24.
 constexpr int kSplitPrice = 8;
@@ -150,18 +150,42 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
     __shared__ int32_t first_tile[kCached];
     __shared__ int64_t lines[kPlanThreads];
     __shared__ int lengths[kLengths];       // tiles of each number of blocks
-    __shared__ int longest;
+    __shared__ int longest, broken;
     grid_go_on();
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per_tile = tokens_of_tile(a.G);
     int tiles = 0, sorted = 0;
-    for (int b = tid; b < min(a.B, kCached); b += kPlanThreads) cached[b] = read_request(a, b);
-    if (tid == 0) longest = 0;
+    if (tid == 0) {
+        longest = 0;
+        broken = a.B;
+    }
+    __syncthreads();
+    for (int b = tid; b < a.B; b += kPlanThreads) {
+        if (b < kCached) cached[b] = read_request(a, b);
+        // the first request whose rows do not follow from the ones before: it and those
+        // behind it have no keys, and the rows from its own on become zeros (so the
+        // tiles of a call never cover more than its rows)
+        if (a.cu_q && (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.T)) atomicMin(&broken, b);
+    }
     for (int i = tid; i < kLengths; i += kPlanThreads) lengths[i] = 0;
     if (!a.cu_q)
         for (int p = tid; p <= a.P; p += kPlanThreads) counts[p] = 0;
     __syncthreads();
-    auto request = [&](int b) { return b < kCached ? cached[b] : read_request(a, b); };
+    auto without_keys = [&](Request r, int b) {
+        r.row0 = b == broken ? min(max(a.cu_q[b], 0), a.T) : a.T;
+        r.rows = a.T - r.row0;
+        r.len = r.plen = 0;
+        return r;
+    };
+    if (broken < a.B) {
+        for (int b = broken + tid; b < min(a.B, kCached); b += kPlanThreads) cached[b] = without_keys(cached[b], b);
+        __syncthreads();
+    }
+    auto request = [&](int b) {
+        if (b < kCached) return cached[b];
+        const Request r = read_request(a, b);
+        return b < broken ? r : without_keys(r, b);
+    };
     if (a.cu_q) {
         for (int base = 0; base < a.B; base += kPlanThreads) {
             const int b = base + tid;
@@ -352,7 +376,7 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
 // The way of a wait that one try did not end.
 __device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, unsigned* status, unsigned where, volatile unsigned* dead) {
     for (uint32_t i = 0; i < kLimit; ++i)
-        if (mbar_try_wait(bar, parity) || *dead) return;
+        if (mbar_try_wait_ns(bar, parity, 1000) || *dead) return;
     *dead = 1;
     report(status, BD_ERR_TIMEOUT);
     atomicCAS(status + 2, 0u, where);
@@ -360,7 +384,7 @@ __device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, unsigned
 // The end of what is in flight, however the waits before went.
 __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
     for (uint32_t i = 0; i < kLimit; ++i)
-        if (mbar_try_wait(bar, parity)) return;
+        if (mbar_try_wait_ns(bar, parity, 1000)) return;
 }
 
 // Whether a phase is complete, without waiting.
@@ -1055,7 +1079,9 @@ int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
 bool may_split(const Args& a) { return !a.cu_q || most_tiles(a.T, a.B, a.G) * a.Hk < split_below(); }
 
 bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream) {
-    plan_kernel<<<1, kPlanThreads, a.cu_q ? 0 : (a.P + 1) * sizeof(int), stream>>>(a, plan, tile_blocks(), may_split(a));
+    const int counts = a.cu_q ? 0 : (a.P + 1) * (int)sizeof(int);
+    if (!set_smem_attr(reinterpret_cast<const void*>(plan_kernel), (kMaxPrefixes + 1) * (int)sizeof(int), 10)) return BD_ERR_CUDA;
+    plan_kernel<<<1, kPlanThreads, counts, stream>>>(a, plan, tile_blocks(), may_split(a));
     return launch_status();
 }
 

@@ -338,7 +338,8 @@ bd_status bitdelta_attn_decode_prefix(const void *q, int64_t q_stride, int64_t B
  * int32 [B + 1], ascending from 0 to T) are request b's newest tokens, the last
  * of them at its last position; their keys are already in the cache.  With a
  * prefix, the queries see it as decode does.  Rows outside every request's
- * range are left as they are. */
+ * range are left as they are.  From the first request on whose offsets do not
+ * ascend within [0, T], rows become zeros, and BD_ERR_SLOT is set. */
 bd_status bitdelta_attn_prefill(const void *q, int64_t q_stride, int64_t T, int64_t B, int32_t q_heads,
                                 const bd_kv_cache *cache, const int32_t *slots, const int32_t *cu_q,
                                 const int32_t *lens, const int32_t *prefix_ids,

@@ -286,6 +286,27 @@ def test_out_of_range_is_reported_and_harmless(bd):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("T", [8, 700])
+def test_broken_row_offsets(bd, T):
+    """Offsets that come back again and again name more rows than there are: the requests
+    before the first break are served, the rows from there on are zeros."""
+    g = gen(59)
+    B, hq, hk, d = 33, 64, 8, 128
+    k, v = make_cache(B, T, hk, d, g)
+    q = queries(T, hq, d, g)
+    ws = bd.attn_workspace(T, B, hq, hk, d, device=DEV)
+    for cu in ([0, 5] + [T, 0] * 16, [0, 5] + [T, 0, 1] * 11, [0, 5, T + 1] + [T] * 31, [0, 5, 4, -1] + [T] * 30):
+        cu = i32(cu[:B + 1])
+        out = torch.full_like(q, 3.0)
+        bd.attn_prefill(q, k, v, cu, i32([T] * B), ws, out=out)
+        assert bd.device_status(ws) == bd.BD_ERR_SLOT
+        served = T if int(cu[2]) == T else 5
+        ends = [0, 5, T] if served == T else [0, 5]
+        want, bound, _ = ref.attention(q[:served], k, v, i32([T] * (len(ends) - 1)), cu_q=ends)
+        ref.assert_close(out[:served], want, bound)
+        assert (out[served:] == 0).all()
+
+
 def test_offsets_past_32_bits(bd):
     """Slots, tokens and heads that lie more than 2^32 elements into the cache."""
     g = gen(43)
@@ -395,6 +416,21 @@ def test_more_requests_than_the_plan_keeps(bd):
         want, bound, _ = ref.attention(q, k, v, lens, cu_q=cu, **how)
         ref.assert_close(bd.attn_prefill(q, k, v, cu, lens, ws, **how), want, bound)
     assert bd.device_status(ws) == 0
+
+
+def test_most_prefixes(bd):
+    """As many prefixes as a call takes, two of them named."""
+    g = gen(71)
+    n, hq, hk, d, P = 5, 8, 2, 64, 8192
+    k, v = make_cache(n + 2, 90, hk, d, g)
+    lens, ids = i32([7, 0, 90, 33, 1]), i32([8191, 17, 8191, -1, 17])
+    pslots = torch.zeros(P, dtype=torch.int32, device=DEV)
+    plens = torch.zeros(P, dtype=torch.int32, device=DEV)
+    pslots[17], pslots[8191], plens[17], plens[8191] = n, n + 1, 90, 41
+    q = queries(n, hq, d, g)
+    ws = bd.attn_workspace(n, n, hq, hk, d, device=DEV)
+    want, bound, _ = ref.attention(q, k, v, lens, prefix_ids=ids, prefix_slots=pslots, prefix_lens=plens)
+    ref.assert_close(bd.attn_decode_prefix(q, k, v, lens, ids, pslots, plens, ws), want, bound)
 
 
 def test_empty_calls(bd):
