@@ -38,6 +38,7 @@ constexpr int kTile = 16;                 // keys of a tile
 constexpr int kUnitCost = 3;              // places of a unit besides its tiles
 constexpr int kLeast = 16;                // places of a block
 constexpr int kShort = 64;                // tiles up to which a unit may have a block of its own
+constexpr int kKept = 1024;               // requests that a block keeps on chip
 constexpr int kRuns = 128;                // runs of requests that a block looks its place up in
 
 // R: rows of a unit (8 or 16 query heads).  A probability is multiplied as two
@@ -95,14 +96,26 @@ struct Cursor {
     Keys k;
 };
 
-__device__ __forceinline__ void load_request(const Args& a, Cursor& c) {
-    c.r = read_request(a, c.b);
+// What a block keeps of the first requests: read once, at its beginning.  Later the
+// same loads would queue behind the keys' (2 to 4 thousand cycles each).
+struct Kept {
+    int32_t slot, len, plen;
+};
+
+__device__ __forceinline__ void load_request(const Args& a, const Kept* kept, Cursor& c) {
+    if (c.b < kKept) {
+        c.r.slot = kept[c.b].slot;
+        c.r.len = kept[c.b].len;
+        c.r.plen = kept[c.b].plen;
+    } else {
+        c.r = read_request(a, c.b);
+    }
     c.k = visible_keys(a, c.r);
     c.tiles = max(1, (c.k.n + kTile - 1) / kTile);
 }
 
 // Goes on to the first unit from c on with tiles in the part; false if there is none.
-__device__ __forceinline__ bool seek(const Args& a, const Line& line, Cursor& c, int units) {
+__device__ __forceinline__ bool seek(const Args& a, const Kept* kept, const Line& line, Cursor& c, int units) {
     while (c.start < line.hi) {
         const int64_t first = c.start + line.lead();
         c.tile = (int)min(max(line.lo - first, (int64_t)0), (int64_t)c.tiles);
@@ -112,19 +125,19 @@ __device__ __forceinline__ bool seek(const Args& a, const Line& line, Cursor& c,
         if (++c.u == units) {
             c.u = 0;
             if (++c.b >= a.B) return false;
-            load_request(a, c);
+            load_request(a, kept, c);
         }
     }
     return false;
 }
-__device__ __forceinline__ bool next_unit(const Args& a, const Line& line, Cursor& c, int units) {
+__device__ __forceinline__ bool next_unit(const Args& a, const Kept* kept, const Line& line, Cursor& c, int units) {
     c.start += line.length(c.tiles);
     if (++c.u == units) {
         c.u = 0;
         if (++c.b >= a.B) return false;
-        load_request(a, c);
+        load_request(a, kept, c);
     }
-    return seek(a, line, c, units);
+    return seek(a, kept, line, c, units);
 }
 
 struct Record {                            // an open unit of a warp
@@ -224,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sums[kRuns + 1];
     __shared__ int longest[kRuns / 32];
+    __shared__ Kept kept[kKept];
     __shared__ Record records[2 * kWarps];
     __shared__ int chain[2 * kWarps];
     __shared__ int last_block;
@@ -238,7 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         int64_t mine = 0;
         int most = 0;
         for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) {
-            const int n = tiles_of(a, read_request(a, b));
+            const Request r = read_request(a, b);
+            if (b < kKept) kept[b] = Kept{r.slot, r.len, r.plen};
+            const int n = tiles_of(a, r);
             mine += kUnitCost + n;
             most = max(most, n);
         }
@@ -288,23 +304,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
             c.b = unit / units;
             c.u = unit % units;
             c.start = (int64_t)unit * line.each;
-            load_request(a, c);
+            load_request(a, kept, c);
         } else {
             int s = 0;                     // the run that holds place lo
             for (int step = kRuns / 2; step; step /= 2)
                 if (sums[s + step] * units <= line.lo) s += step;
             c.start = sums[s] * units;
             c.b = s * run;
-            load_request(a, c);
+            load_request(a, kept, c);
             while (line.lo - c.start >= (int64_t)line.length(c.tiles) * units && c.b + 1 < a.B) {
                 c.start += (int64_t)line.length(c.tiles) * units;
                 ++c.b;
-                load_request(a, c);
+                load_request(a, kept, c);
             }
             c.u = min((int)((line.lo - c.start) / line.length(c.tiles)), units - 1);
             c.start += (int64_t)c.u * line.length(c.tiles);
         }
-        has = seek(a, line, c, units);
+        has = seek(a, kept, line, c, units);
     }
     if (has) {
         Cursor ahead = c;
@@ -313,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
         auto prefetch = [&]() {
             if (more) {
                 load_tile<D>(a, ahead, chunks, ring + put * S::kStage, lane);
-                if (++ahead.tile == ahead.end) more = next_unit(a, line, ahead, units);
+                if (++ahead.tile == ahead.end) more = next_unit(a, kept, line, ahead, units);
             }
             cp_async_commit();
             if (++put == S::kStages) put = 0;
@@ -511,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     if (a.weights && lane % 4 == 0) buf.lse[row_at] = log_sum(m[i], l[i]);
                 }
             }
-        } while (next_unit(a, line, c, units));
+        } while (next_unit(a, kept, line, c, units));
         cp_async_wait<0>();
     }
     __syncthreads();
