@@ -604,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
 // row's denominator).  Reads the scores that the decode kernel left (in L2, up
 // to its size) instead of the keys: 4 bytes a head and key for 2 head_dim a key.
 // A pass of its own because the denominator is only known when all parts of a row
-// are joined.  32 requests of 2,049 to 4,608 keys: 74 us without weights, 92 with the
-// scores' stores and this pass.
+// are joined.  32 requests of 2,049 to 4,608 keys: 74 us without weights, 87 with the
+// scores' stores and this pass (four keys a thread; with two 89, with one 90, where two
+// requests of some hundred keys take 13.1, 12.2 and 11.7).
 __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBuffers buf) {
     const int b = blockIdx.z, hk = blockIdx.y;
     grid_wait();
@@ -613,11 +614,22 @@ __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBu
     const Keys k = visible_keys(a, r);
     const int64_t row = (int64_t)b * a.Hq + (int64_t)hk * a.G;
     float* w = a.weights + ((int64_t)r.slot * a.Hk + hk) * a.capacity;
-    for (int x = blockIdx.x * 256 + threadIdx.x; x < k.n; x += gridDim.x * 256) {
-        float sum = 0.f;
+    // four keys a thread (rows of scores have room for whole tiles)
+    for (int x = (blockIdx.x * 256 + threadIdx.x) * 4; x < k.n; x += gridDim.x * 1024) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int g = 0; g < a.G; ++g) sum += exp2_approx(buf.scores[(row + g) * buf.score_stride + x] - buf.lse[row + g]);
-        w[x + (x >= k.head ? k.gap : 0)] += sum;
+        for (int g = 0; g < a.G; ++g) {
+            const float4 s = *reinterpret_cast<const float4*>(buf.scores + (row + g) * buf.score_stride + x);
+            const float lse = buf.lse[row + g];
+            sum.x += exp2_approx(s.x - lse);
+            sum.y += exp2_approx(s.y - lse);
+            sum.z += exp2_approx(s.z - lse);
+            sum.w += exp2_approx(s.w - lse);
+        }
+        const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (x + i < k.n) w[x + i + (x + i >= k.head ? k.gap : 0)] += v[i];
     }
 }
 
@@ -643,8 +655,8 @@ bd_status launch_decode(const Args& a, int head_dim, const DecodeBuffers& buf, c
 }
 
 bd_status launch_weigh(const Args& a, const DecodeBuffers& buf, cudaStream_t stream) {
-    const int64_t heads = (int64_t)a.B * a.Hk, most = (a.capacity + 255) / 256;
-    int64_t x = (64 * (int64_t)sm_count() + heads - 1) / heads;
+    const int64_t heads = (int64_t)a.B * a.Hk, most = (a.capacity + 1023) / 1024;
+    int64_t x = (16 * (int64_t)sm_count() + heads - 1) / heads;
     x = x < most ? x : most;
     return launch_close(weigh_kernel, dim3((unsigned)x, (unsigned)a.Hk, (unsigned)a.B), 256, 0, stream, a, buf);
 }
