@@ -1075,8 +1075,13 @@ int64_t most_tiles(int64_t tokens, int64_t batch, int G) { return tokens / (kPar
 int tile_blocks() { return decode_blocks(); }
 int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
 
-// Whether a call's parts may be left in the workspace, which holds those of few rows.
-bool may_split(const Args& a) { return !a.cu_q || most_tiles(a.T, a.B, a.G) * a.Hk < split_below(); }
+// Whether a call's parts may be left in the workspace, which holds those of few rows: a
+// prefill of few units, if a unit can be longer than the parts' price at all.
+bool may_split(const Args& a) {
+    if (!a.cu_q) return true;
+    const int source = (a.capacity + kKeys - 1) / kKeys + 1;
+    return most_tiles(a.T, a.B, a.G) * a.Hk < split_below() && source * (a.prefix_ids ? 2 : 1) > kSplitPrice + 1;
+}
 
 bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream) {
     const int counts = a.cu_q ? 0 : (a.P + 1) * (int)sizeof(int);
