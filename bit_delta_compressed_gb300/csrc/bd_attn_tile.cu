@@ -545,11 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ unsigned dead;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     unsigned* status = a.status;
-    // Waits.  One that runs out ends all others at once; the roles then go through their
-    // steps without waiting, so that nothing hangs, and the status word tells.
+    // Waits.  One that runs out ends all others at once, and the status word tells: no
+    // copy is started any more (a barrier that still expects one may not be armed
+    // again), the other roles go through their steps without waiting, on whatever is
+    // there, and the copies and products under way are waited for at the end.
     auto wait = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         if (!mbar_try_wait(bar, parity & 1)) wait_on(bar, parity & 1, status, where, &dead);
     };
+    auto is_dead = [&]() { return *static_cast<volatile unsigned*>(&dead) != 0; };
     auto warp_waits = [&](uint64_t* bar, uint32_t parity, unsigned where) {
         wait(bar, parity, where);
         __syncwarp();
@@ -627,12 +630,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int st = 0, put = 0;
             uint32_t phase = 1;                    // of the fill before the one to come
             Segment s;
-            while (walk.next(a, plan, s)) {
+            while (!is_dead() && walk.next(a, plan, s)) {
                 const RowTile t = plan.tiles[s.tile];
                 for (int i = s.first; i < s.last; ++i, ++put) {
                     const Block b = block_of(t, i);
                     auto at = [&](int dim) { return dim == order.token ? b.key : dim == order.head ? s.hk : b.slot; };
                     if (put >= stages) wait(empty + st, phase, 1);
+                    if (is_dead()) break;
                     mbar_expect_tx(full + st, T::kQ);
                     for (int h = 0; h < T::kHalves; ++h)
                         tma_load_4d(to + st * T::kQ + h * kKeys * 128, map, full + st, h * 64, at(0), at(1), at(2));
@@ -661,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the unit's queries, in the order of its rows (the tile's whole room: what
                 // lies behind its tokens belongs to rows that are none)
                 if (units > 0) warp_waits(&q_empty, units - 1, 2);
+                if (is_dead()) break;
                 if (elect_one()) {
                     mbar_expect_tx(&q_full, T::kHalves * tokens_of_tile(a.G) * a.G * 128);
                     for (int h = 0; h < T::kHalves; ++h) tma_load_3d(q_at + h * kPartRows * 128, &qmap, &q_full, h * 64, s.hk * a.G, row0);
@@ -699,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) mma_commit(drained);
             __syncwarp();
             settle(drained, 0);
+            if (units > 0) settle(&q_full, units - 1 & 1);
         }
         if (warp == 10) {
             const uint64_t v_desc = desc_v(v_at);
