@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_s = idesc_bf16(128, kKeys), idesc_o = idesc_bf16(128, D) | kTransposeB;
         if (warp == 9) {
             const uint64_t q_desc = desc_sw128(q_at), k_desc = desc_sw128(k_at);
-            uint32_t st = 0, phase = 0, n = 0, units = 0;
+            uint32_t st = 0, phase = 0, n = 0, n1 = 0, units = 0;
             Segment s;
             if (lane == 0) prefetch_tensormap(&qmap);
             while (walk.next(a, plan, s)) {
@@ -678,6 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int g = 0; g < groups; ++g) {
                         const uint64_t qd = q_desc + (g * 128 * 128 >> 4);
                         const bool last = g == groups - 1;
+                        // (so that the issuer of the outputs, which looks for the second group's
+                        // next scores, finds them one phase ahead at most)
+                        if (g == 1 && n1++ > 1 && i > s.first + 1) wait(pv_done + 1, n1 - 3, 12);
                         // the scores before, of whichever group, are in registers
                         if (n > 0) wait(&s_free, n - 1, 5);
                         __syncwarp();
@@ -716,6 +719,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(v_full + st, phase, 6);
                     for (int g = 0; g < groups; ++g) {
                         warp_waits(p_full + g, g ? done1++ : done0++, 7);
+                        // the second group's output after its next scores: these are the ones that
+                        // a hand-over waits for (8192 tokens 755 -> 716 us; the first group's would
+                        // be looked for too late at a unit's end)
+                        if (g == 1 && i + 1 < s.last) warp_waits(s_full + 1, done1, 13);
                         tc_fence_after();
                         if (elect_one()) {
                             const uint64_t vd = v_desc + (st * T::kQ >> 4);
