@@ -14,12 +14,12 @@
 // never wait for a softmax or for the product before -- P (64) and O (head_dim) of
 // each group.  While one group works on its softmax the products of the other run.
 // The output is only rescaled when a row's maximum has grown by more than 2^8
-// since the last time (8192 tokens 737 us, with every growth 750); P is then at most
+// since the last time (with every growth 750 us where this took 737 on 8192 tokens); P is then at most
 // 2^8 and rounds no worse.  Its rounding to bf16 is the one that the products ask for;
 // scores, maxima, sums and outputs stay f32.
-// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 740 us = 1.49 PFLOP/s,
-// 78% of the measured bf16 rate; 8 prompts of 333 to 2048 tokens behind up to 700, seeing
-// 4 + 1024 keys, 270 us (their visible pairs alone 133).  The tensor pipe is active 71% of
+// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 714 us = 1.54 PFLOP/s,
+// 81% of the measured bf16 rate; 8 prompts of 333 to 2048 tokens behind up to 700, seeing
+// 4 + 1024 keys, 267 us (their visible pairs alone 133).  The tensor pipe is active 71% of
 // an SM's busy cycles; what is left are the hand-overs of S -- product to softmax and back,
 // ~600 cycles each of ~1500 that a group's turn takes.  Blocks of 80 keys, for which both
 // groups' S have room, took 896 us where 128 took 768: a softmax step costs ~600 cycles
