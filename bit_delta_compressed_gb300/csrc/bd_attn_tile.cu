@@ -17,9 +17,11 @@
 // since the last time (with every growth 750 us where this took 737 on 8192 tokens); P is then at most
 // 2^8 and rounds no worse.  Its rounding to bf16 is the one that the products ask for;
 // scores, maxima, sums and outputs stay f32.
-// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 714 us = 1.54 PFLOP/s,
-// 81% of the measured bf16 rate; 8 prompts of 333 to 2048 tokens behind up to 700, seeing
-// 4 + 1024 keys, 267 us (their visible pairs alone 133).  The tensor pipe is active 71% of
+// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 670 us for the
+// first calls after a pause = 1.64 PFLOP/s, 86% of the measured bf16 burst rate, and 705-730 us
+// call after call = 1.53 PFLOP/s, 90% of the measured sustained rate (1360 W, the power cap
+// holds the clock at 1.8 GHz); 8 prompts of 333 to 2048 tokens behind up to 700, seeing
+// 4 + 1024 keys, 267 us (their visible pairs alone 133).  The tensor pipe is active 73% of
 // an SM's busy cycles; what is left are the hand-overs of S -- product to softmax and back,
 // ~600 cycles each of ~1500 that a group's turn takes.  Blocks of 80 keys, for which both
 // groups' S have room, took 896 us where 128 took 768: a softmax step costs ~600 cycles
