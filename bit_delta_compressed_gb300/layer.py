@@ -70,7 +70,11 @@ class CachedAttention:
     keys of every slot; weights : f32 [slots, kv_heads, capacity], what decode
     steps gave each key (None unless ``weigh``).  All on the device: a decode
     step can be captured in a CUDA graph.  A shared prefix lies in a slot of its
-    own, filled by ``prefill`` like any other."""
+    own, filled by ``prefill`` like any other.
+
+    A request whose slot is not there, or has no room for all its new tokens, is
+    left as it is: nothing is appended, its rows come out as zeros, and the status
+    word of ``ws`` holds ``BD_ERR_SLOT``."""
 
     def __init__(self, bd, slots: int, capacity: int, q_heads: int, kv_heads: int, head_dim: int, tokens: int,
                  batch: int, window: int = 0, sinks: int = 0, weigh: bool = False, device="cuda"):
@@ -78,47 +82,77 @@ class CachedAttention:
         self.bd, self.torch = bd, torch
         self.heads = (q_heads, kv_heads, head_dim)
         self.mask = {"window": window, "sinks": sinks}
+        # Behind the cache's places lies one more key, and a slot that is always full: what
+        # has no place of its own goes there, so that no index leaves its tensor (on a GPU
+        # that ends the context) and no step waits for the host.
         shape = (slots, capacity, kv_heads, head_dim)
-        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
-        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device)
-        self.lens = torch.zeros(slots, dtype=torch.int32, device=device)
-        self.weights = torch.zeros(slots, kv_heads, capacity, device=device) if weigh else None
+        self.rows_k = torch.zeros(slots * capacity + 1, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
+        self.rows_v = torch.zeros_like(self.rows_k)
+        self.k, self.v = self.rows_k[:-1].view(shape), self.rows_v[:-1].view(shape)
+        self.slot_lens = torch.zeros(slots + 1, dtype=torch.int32, device=device)
+        self.slot_lens[-1] = capacity
+        self.lens = self.slot_lens[:-1]
+        self.weights = None
+        if weigh:
+            self.slot_weights = torch.zeros(slots + 1, kv_heads, capacity, device=device)
+            self.weights = self.slot_weights[:-1]
         self.ws = bd.attn_workspace(tokens, batch, q_heads, kv_heads, head_dim, capacity if weigh else 0, device)
         self.evict_ws = bd.evict_workspace(batch, kv_heads, capacity, device)
 
-    def _append(self, k, v, slots, at):
+    def _slots(self, slots):
+        """Places in ``slot_lens``: those of no slot (-1 and ``slots``) are the one behind."""
+        return slots.clamp(-1, self.lens.shape[0]).long()
+
+    def _append(self, k, v, place):
+        """Rows of k and v become the keys at ``place``, counted through all slots (-1: the one behind)."""
         _, hk, d = self.heads
-        self.k[slots, at] = k.view(-1, hk, d)
-        self.v[slots, at] = v.view(-1, hk, d)
+        self.rows_k[place] = k.view(-1, hk, d)
+        self.rows_v[place] = v.view(-1, hk, d)
         if self.weights is not None:
-            self.weights[slots, :, at] = 0
+            capacity = self.k.shape[1]
+            self.slot_weights[place // capacity, :, place % capacity] = 0
+
+    def _prefix_lens(self, prefix_slots):
+        return None if prefix_slots is None else self.slot_lens[self._slots(prefix_slots)]
 
     def decode(self, q, k, v, slots, prefix_ids=None, prefix_slots=None):
-        """One token for each request: its slot in ``slots`` (int32 [M]); requests
+        """One token for each request: its slot in ``slots`` (int32 [M], none twice); requests
         may name shared prefixes by their index in ``prefix_slots``."""
+        torch, capacity = self.torch, self.k.shape[1]
         hq, _, d = self.heads
-        to = slots.long()
-        self._append(k, v, to, self.lens[to].long())
-        self.lens[to] += 1
-        lens = self.lens[to]
-        plens = None if prefix_slots is None else self.lens[prefix_slots.long()]
-        out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots, plens,
-                                         self.ws, slots=slots, weights=self.weights, **self.mask)
+        to = self._slots(slots)
+        have = self.slot_lens[to]
+        self._append(k, v, torch.where(have < capacity, torch.add(have, to, alpha=capacity), -1))
+        lens = have + 1                           # beyond a full slot's capacity: the call below reports it
+        self.slot_lens[to] = lens.clamp_max(capacity)
+        out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots,
+                                         self._prefix_lens(prefix_slots), self.ws, slots=slots, weights=self.weights,
+                                         **self.mask)
         return out.view(-1, hq * d)
 
     def prefill(self, q, k, v, slots, cu_q, prefix_ids=None, prefix_slots=None):
         """The next tokens of some requests: rows ``cu_q[b]`` to ``cu_q[b + 1]`` are
-        the request's in slot ``slots[b]``."""
-        torch = self.torch
+        the request's in slot ``slots[b]``.  Rows of no request are not written."""
+        torch, capacity = self.torch, self.k.shape[1]
         hq, _, d = self.heads
-        rows = torch.arange(q.shape[0], device=q.device)
-        of = torch.searchsorted(cu_q[1:].contiguous(), rows.to(torch.int32), right=True)
-        to = slots.long()
-        self._append(k, v, to[of], self.lens[to].long()[of] + rows - cu_q.long()[of])
-        self.lens[to] += cu_q[1:] - cu_q[:-1]
-        plens = None if prefix_slots is None else self.lens[prefix_slots.long()]
-        out = self.bd.attn_prefill(q.view(-1, hq, d), self.k, self.v, cu_q, self.lens[to], self.ws, slots=slots,
-                                   prefix_ids=prefix_ids, prefix_slots=prefix_slots, prefix_lens=plens, **self.mask)
+        T = q.shape[0]
+        to = self._slots(slots)
+        have = self.slot_lens[to]
+        # requests from the first whose offsets do not ascend on are not served (as the
+        # library's call has it), nor those whose tokens the slot has no room for
+        steady = cu_q.clamp(0, T).cummax(0).values
+        served = (steady == cu_q).cumprod(0, dtype=torch.int32)[1:]
+        lens = have + (cu_q[1:] - cu_q[:-1]) * served
+        fits = (lens <= capacity) & (served > 0)
+        # a request's first place less its first row; far below zero for rows that are appended nowhere
+        start = torch.where(fits, torch.add(have, to, alpha=capacity) - cu_q[:-1], -1 << 40)
+        start = torch.nn.functional.pad(start, (1, 1), value=-1 << 40)
+        row = torch.arange(T, dtype=torch.int32, device=q.device)
+        self._append(k, v, (start[torch.searchsorted(steady, row, right=True)] + row).clamp_min_(-1))
+        self.slot_lens[to] = torch.where(fits, lens, have)
+        out = self.bd.attn_prefill(q.view(-1, hq, d), self.k, self.v, cu_q, lens, self.ws, slots=slots,
+                                   prefix_ids=prefix_ids, prefix_slots=prefix_slots,
+                                   prefix_lens=self._prefix_lens(prefix_slots), **self.mask)
         return out.view(-1, hq * d)
 
     def evict(self, src, dst, budget: int, recent: int) -> None:

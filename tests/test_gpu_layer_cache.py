@@ -1,0 +1,94 @@
+"""GPU: ``CachedAttention`` at the ends of its slots: what fits is served, what
+does not comes out as zeros and is reported, eagerly and from a CUDA graph."""
+import pytest
+import torch
+
+from bit_delta_compressed_gb300 import layer
+from tests import attention_ref as ref
+from tests.gpu_util import load_bd
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SLOTS, CAP, HQ, HK, D = 5, 40, 8, 2, 64
+
+
+@pytest.fixture(scope="module")
+def bd():
+    return load_bd()
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32, device=DEV)
+
+
+def make(bd, lens, **how):
+    g = torch.Generator(DEV).manual_seed(sum(lens))
+    c = layer.CachedAttention(bd, SLOTS, CAP, HQ, HK, D, tokens=64, batch=4, device=DEV, **how)
+    c.k.copy_(torch.randn(c.k.shape, generator=g, device=DEV))
+    c.v.copy_(torch.randn(c.v.shape, generator=g, device=DEV))
+    c.lens.copy_(i32(lens))
+    return c, g
+
+
+def rows(n, g):
+    return [torch.randn(n, h * D, generator=g, device=DEV).to(torch.bfloat16) for h in (HQ, HK, HK)]
+
+
+def test_decode_at_the_end_of_a_slot(bd):
+    """Slots with one free place, none, and of no number at all; the step after that, too."""
+    c, g = make(bd, [CAP - 1, CAP, 7, 0, 12])
+    slots = i32([0, 1, -1, 2])
+    for step, lens in enumerate(([CAP, CAP, 8, 0, 12], [CAP, CAP, 9, 0, 12])):
+        old = c.k.clone()
+        q, k, v = rows(4, g)
+        out = c.decode(q, k, v, slots).view(4, HQ, D)
+        assert bd.device_status(c.ws) == bd.BD_ERR_SLOT
+        assert c.lens.tolist() == lens
+        good = [0, 3] if step == 0 else [3]
+        want, bound, _ = ref.attention(q.view(4, HQ, D)[good], c.k, c.v, i32([lens[int(slots[b])] for b in good]), slots=slots[good])
+        ref.assert_close(out[good], want, bound)
+        assert (out[[b for b in range(4) if b not in good]] == 0).all()
+        for b in good:
+            s = int(slots[b])
+            old[s, lens[s] - 1] = k[b].view(HK, D)
+        assert torch.equal(c.k, old)
+
+
+def test_prefill_beyond_the_end_of_a_slot(bd):
+    c, g = make(bd, [CAP - 3, CAP - 3, 0, 5, 12])
+    q, k, v = rows(30, g)
+    slots, cu = i32([1, 0, SLOTS, 2]), i32([0, 3, 7, 10, 30])
+    out = c.prefill(q, k, v, slots, cu).view(30, HQ, D)
+    assert bd.device_status(c.ws) == bd.BD_ERR_SLOT
+    assert c.lens.tolist() == [CAP - 3, CAP, 20, 5, 12]
+    mine = list(range(3)) + list(range(10, 30))
+    want, bound, _ = ref.attention(q.view(30, HQ, D)[mine], c.k, c.v, i32([CAP, 20]), slots=i32([1, 2]), cu_q=[0, 3, 23])
+    ref.assert_close(out[mine], want, bound)
+    assert (out[3:10] == 0).all()
+
+
+def test_decode_steps_from_a_graph(bd):
+    """The captured step goes on until its slot is full, then leaves it alone."""
+    c, g = make(bd, [CAP - 3, 4, 0, 0, 0])
+    slots = i32([0, 1])
+    q, k, v = rows(2, g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.decode(q, k, v, slots)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = c.decode(q, k, v, slots)
+    torch.cuda.current_stream().wait_stream(side)
+    for step in range(4):
+        for t, new in zip((q, k, v), rows(2, g)):
+            t.copy_(new)
+        graph.replay()
+        full = step >= 2
+        assert c.lens[:2].tolist() == [CAP if full else CAP - 1 + step, 6 + step]
+        assert bd.device_status(c.ws) == (bd.BD_ERR_SLOT if full else 0)
+        good = [1] if full else [0, 1]
+        want, bound, _ = ref.attention(q.view(2, HQ, D)[good], c.k, c.v, c.lens[good], slots=slots[good])
+        ref.assert_close(out.view(2, HQ, D)[good], want, bound)
+        if full:
+            assert (out[0] == 0).all()
