@@ -96,6 +96,7 @@ class CachedAttention:
         if weigh:
             self.slot_weights = torch.zeros(slots + 1, kv_heads, capacity, device=device)
             self.weights = self.slot_weights[:-1]
+            self.zero = torch.zeros((), device=device)
         self.ws = bd.attn_workspace(tokens, batch, q_heads, kv_heads, head_dim, capacity if weigh else 0, device)
         self.evict_ws = bd.evict_workspace(batch, kv_heads, capacity, device)
 
@@ -110,7 +111,8 @@ class CachedAttention:
         self.rows_v[place] = v.view(-1, hk, d)
         if self.weights is not None:
             capacity = self.k.shape[1]
-            self.slot_weights[place // capacity, :, place % capacity] = 0
+            # (a number would be copied from the host, which the capture of a graph refuses)
+            self.slot_weights[place // capacity, :, place % capacity] = self.zero
 
     def _prefix_lens(self, prefix_slots):
         return None if prefix_slots is None else self.slot_lens[self._slots(prefix_slots)]

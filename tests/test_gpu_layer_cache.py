@@ -67,9 +67,10 @@ def test_prefill_beyond_the_end_of_a_slot(bd):
     assert (out[3:10] == 0).all()
 
 
-def test_decode_steps_from_a_graph(bd):
+@pytest.mark.parametrize("weigh", [False, True], ids=["", "weigh"])
+def test_decode_steps_from_a_graph(bd, weigh):
     """The captured step goes on until its slot is full, then leaves it alone."""
-    c, g = make(bd, [CAP - 3, 4, 0, 0, 0])
+    c, g = make(bd, [CAP - 3, 4, 0, 0, 0], weigh=weigh)
     slots = i32([0, 1])
     q, k, v = rows(2, g)
     side = torch.cuda.Stream()
@@ -92,3 +93,11 @@ def test_decode_steps_from_a_graph(bd):
         ref.assert_close(out.view(2, HQ, D)[good], want, bound)
         if full:
             assert (out[0] == 0).all()
+        if weigh:
+            # this step's key has what this step gave it, and the head's weights sum to the steps' number
+            at = 5 + step
+            _, _, (added, rel) = ref.attention(q.view(2, HQ, D)[1:], c.k, c.v, i32([at + 1]), slots=i32([1]))
+            one = added[0][:, at]
+            assert ((c.weights[1, :, at].double() - one).abs() <= (rel[0] + (HQ // HK + 2) * ref.F32) * one).all()
+            most = (step + 2) * (HQ // HK)
+            assert ((c.weights[1, :, :at + 1].double().sum(-1) - most).abs() <= 1e-3 * most).all()
