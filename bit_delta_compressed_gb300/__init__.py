@@ -163,6 +163,13 @@ def _need_cuda(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
+def _workspace(ws, device: int):
+    """A workspace's address and bytes; `device` is the index of the other tensors'."""
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the CUDA device of the other tensors")
+    return ws.data_ptr(), ws.numel()
+
+
 def compress_workspace(N: int, K: int, device=None):
     torch = _torch()
     n = int(get_lib().bitdelta_compress_workspace(N, K))
@@ -183,7 +190,7 @@ def compress(w_ft, w_base, workspace=None, alpha_out=None, bits_out=None, stream
     alpha = torch.empty(1, dtype=torch.float32, device=dev) if alpha_out is None else alpha_out
     bits = torch.empty((N, K // 32), dtype=torch.int32, device=dev) if bits_out is None else bits_out
     check(get_lib().bitdelta_compress(w_ft.data_ptr(), w_base.data_ptr(), _dtype_code(w_ft.dtype), N, K,
-                                alpha.data_ptr(), bits.data_ptr(), ws.data_ptr(), ws.numel(),
+                                alpha.data_ptr(), bits.data_ptr(), *_workspace(ws, w_ft.get_device()),
                                 _stream(stream)), "bitdelta_compress")
     return alpha, bits
 
@@ -247,7 +254,7 @@ def linear(x, variant_ids, w_base, alphas, bits_list, out_dtype=None, workspace=
     al = alphas.data_ptr() if V > 0 else None
     check(get_lib().bitdelta_linear_ex(x.data_ptr(), variant_ids.data_ptr(), M, N, K, w_base.data_ptr(),
                                  al, ctypes.cast(ptrs, ctypes.c_void_p), V, y.data_ptr(),
-                                 _dtype_code(out_dtype), ws.data_ptr(), ws.numel(),
+                                 _dtype_code(out_dtype), *_workspace(ws, x.get_device()),
                                  _stream(stream), PATHS[path]), "bitdelta_linear")
     return y
 
@@ -273,7 +280,7 @@ def linear_rows(x, variant_ids, w_base, alpha_rows, bits_list, out_dtype=None, w
     al = alpha_rows.data_ptr() if V > 0 else None
     check(get_lib().bitdelta_linear_rows(x.data_ptr(), variant_ids.data_ptr(), M, N, K, w_base.data_ptr(),
                                          al, ctypes.cast(ptrs, ctypes.c_void_p), V, y.data_ptr(),
-                                         _dtype_code(out_dtype), ws.data_ptr(), ws.numel(),
+                                         _dtype_code(out_dtype), *_workspace(ws, x.get_device()),
                                          _stream(stream), PATHS[path]), "bitdelta_linear_rows")
     return y
 
@@ -282,7 +289,7 @@ def group(variant_ids, V: int, workspace, stream=None) -> None:
     """Group one batch's tokens by variant into ``workspace``."""
     _need_cuda(variant_ids)
     check(get_lib().bitdelta_group(variant_ids.data_ptr(), variant_ids.numel(), V,
-                                   workspace.data_ptr(), workspace.numel(), _stream(stream)),
+                                   *_workspace(workspace, variant_ids.get_device()), _stream(stream)),
           "bitdelta_group")
 
 
@@ -296,7 +303,7 @@ def linear_grouped(x, w_base, alphas, bits_ptrs, V: int, y, workspace, path: str
     check(get_lib().bitdelta_linear_grouped(x.data_ptr(), M, N, K, w_base.data_ptr(), al,
                                             ctypes.cast(bits_ptrs, ctypes.c_void_p), V,
                                             y.data_ptr(), _dtype_code(y.dtype),
-                                            workspace.data_ptr(), workspace.numel(),
+                                            *_workspace(workspace, x.get_device()),
                                             _stream(stream), PATHS[path]),
           "bitdelta_linear_grouped")
 
@@ -318,53 +325,54 @@ def _desc_of(k, v):
         raise TypeError("the cache must be bfloat16")
     S, C, H, D = shape
     ss, st, sh, sd = strides
-    if not (k.is_cuda and v.is_cuda) or sd != 1:
-        raise ValueError("the cache must be CUDA tensors with contiguous head_dim")
+    dev = k.get_device()                   # -1 on the CPU
+    if dev < 0 or v.get_device() != dev or sd != 1:
+        raise ValueError("the cache must be CUDA tensors on one device with contiguous head_dim")
     # the stride of a dimension of one entry is never used, and torch leaves it open
-    return shape, _DESC.pack(k.data_ptr(), v.data_ptr(), S, C, H, D, ss if S > 1 else D, st if C > 1 else D,
+    return shape, dev, _DESC.pack(k.data_ptr(), v.data_ptr(), S, C, H, D, ss if S > 1 else D, st if C > 1 else D,
                              sh if H > 1 else D)
 
 
-def _int32(name, t, *shape):
+def _int32(name, t, dev, *shape):
     if t is None:
         return None
-    if t.dtype is not _torch().int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 CUDA tensor of shape %s" % (name, shape))
+    if t.dtype is not _torch().int32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor of shape %s on the cache's device" % (name, shape))
     return t.data_ptr()
 
 
-def _attn_args(q, D, out):
+def _attn_args(q, D, out, dev):
     torch = _torch()
     shape, strides = q.shape, q.stride()
-    if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_cuda:
-        raise ValueError("q must be a bf16 CUDA tensor [rows, q_heads, head_dim]")
+    if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or q.get_device() != dev:
+        raise ValueError("q must be a bf16 tensor [rows, q_heads, head_dim] on the cache's device")
     T, H, _ = shape
     if strides[2] != 1 or (H > 1 and strides[1] != D):
         raise ValueError("the heads of a row of q must be contiguous")
     if out is None:
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    elif out.shape != shape or out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 CUDA tensor of q's shape")
+    elif out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape on the cache's device")
     return T, H, strides[0] if T > 1 else H * D, out
 
 
-def _weights_ptr(weights, S, H, C):
+def _weights_ptr(weights, dev, S, H, C):
     if weights is None:
         return None
-    if (weights.dtype is not _torch().float32 or weights.shape != (S, H, C) or not weights.is_cuda
+    if (weights.dtype is not _torch().float32 or weights.shape != (S, H, C) or weights.get_device() != dev
             or not weights.is_contiguous()):
-        raise ValueError("weights must be contiguous float32 [slots, kv_heads, capacity]")
+        raise ValueError("weights must be contiguous float32 [slots, kv_heads, capacity] on the cache's device")
     return weights.data_ptr()
 
 
-def _prefix_args(prefix_ids, prefix_slots, prefix_lens, B):
+def _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B):
     if prefix_ids is None and prefix_slots is None and prefix_lens is None:
         return None, None, None, 0
     if prefix_ids is None or prefix_slots is None or prefix_lens is None:
         raise ValueError("prefix_ids, prefix_slots and prefix_lens go together")
     P = prefix_slots.numel()
-    return (_int32("prefix_ids", prefix_ids, B), _int32("prefix_slots", prefix_slots, P),
-            _int32("prefix_lens", prefix_lens, P), P)
+    return (_int32("prefix_ids", prefix_ids, dev, B), _int32("prefix_slots", prefix_slots, dev, P),
+            _int32("prefix_lens", prefix_lens, dev, P), P)
 
 
 def attn_workspace(tokens: int, batch: int, q_heads: int, kv_heads: int, head_dim: int, weigh_len: int = 0,
@@ -395,18 +403,18 @@ def attn_decode_prefix(q, k_cache, v_cache, lens, prefix_ids, prefix_slots, pref
     the ``prefix_lens[p]`` keys in slot ``prefix_slots[p]``, p = ``prefix_ids[b]``
     (-1: none), which are read once for all requests that name them (see
     ``bitdelta_attn_decode_prefix``)."""
-    (S, C, Hk, D), desc = _desc_of(k_cache, v_cache)
-    B, H, stride, out = _attn_args(q, D, out)
-    rest = (window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, S, Hk, C), out.data_ptr(),
-            workspace.data_ptr(), workspace.numel(), _stream(stream))
-    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
+    (S, C, Hk, D), dev, desc = _desc_of(k_cache, v_cache)
+    B, H, stride, out = _attn_args(q, D, out, dev)
+    rest = (window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, dev, S, Hk, C), out.data_ptr(),
+            *_workspace(workspace, dev), _stream(stream))
+    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B)
     lib = get_lib()
     if P == 0:
-        code = lib.bitdelta_attn_decode(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, B),
-                                        _int32("lens", lens, B), *rest)
+        code = lib.bitdelta_attn_decode(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, dev, B),
+                                        _int32("lens", lens, dev, B), *rest)
     else:
-        code = lib.bitdelta_attn_decode_prefix(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, B),
-                                               _int32("lens", lens, B), ids, pslots, plens, P, *rest)
+        code = lib.bitdelta_attn_decode_prefix(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, dev, B),
+                                               _int32("lens", lens, dev, B), ids, pslots, plens, P, *rest)
     if code != BD_OK:
         check(code, "bitdelta_attn_decode" if P == 0 else "bitdelta_attn_decode_prefix")
     return out
@@ -418,14 +426,14 @@ def attn_prefill(q, k_cache, v_cache, cu_q, lens, workspace, slots=None, window:
     ``cu_q[b+1]`` of q [T, q_heads, head_dim] are request b's newest tokens,
     whose keys are the last of its ``lens[b]`` keys in the cache (see
     ``bitdelta_attn_prefill``).  Returns out [T, q_heads, head_dim]."""
-    (_, _, _, D), desc = _desc_of(k_cache, v_cache)
-    T, H, stride, out = _attn_args(q, D, out)
+    (_, _, _, D), dev, desc = _desc_of(k_cache, v_cache)
+    T, H, stride, out = _attn_args(q, D, out, dev)
     B = lens.numel()
-    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, B)
-    check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, desc, _int32("slots", slots, B),
-                                          _int32("cu_q", cu_q, B + 1), _int32("lens", lens, B), ids, pslots, plens, P,
+    ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B)
+    check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, desc, _int32("slots", slots, dev, B),
+                                          _int32("cu_q", cu_q, dev, B + 1), _int32("lens", lens, dev, B), ids, pslots, plens, P,
                                           window, sinks, D ** -0.5 if scale is None else scale, out.data_ptr(),
-                                          workspace.data_ptr(), workspace.numel(), _stream(stream)),
+                                          *_workspace(workspace, dev), _stream(stream)),
           "bitdelta_attn_prefill")
     return out
 
@@ -445,14 +453,14 @@ def cache_evict(k_cache, v_cache, weights, lens, src, dst, budget: int, workspac
     all, of every head (see ``bitdelta_cache_evict``).  ``lens`` holds a length
     for every slot.  ``kept`` (int32 [n, kv_heads, budget]) receives the kept
     keys' old places."""
-    (S, C, H, _), desc = _desc_of(k_cache, v_cache)
+    (S, C, H, _), dev, desc = _desc_of(k_cache, v_cache)
     n = src.numel()
     if weights is None:
         raise ValueError("weights are needed")
-    check(get_lib().bitdelta_cache_evict(desc, _weights_ptr(weights, S, H, C), _int32("lens", lens, S),
-                                         _int32("src", src, n), _int32("dst", dst, n), n, budget, sinks, recent,
-                                         _int32("kept", kept, n, H, budget), workspace.data_ptr(),
-                                         workspace.numel(), _stream(stream)), "bitdelta_cache_evict")
+    check(get_lib().bitdelta_cache_evict(desc, _weights_ptr(weights, dev, S, H, C), _int32("lens", lens, dev, S),
+                                         _int32("src", src, dev, n), _int32("dst", dst, dev, n), n, budget, sinks, recent,
+                                         _int32("kept", kept, dev, n, H, budget), *_workspace(workspace, dev),
+                                         _stream(stream)), "bitdelta_cache_evict")
 
 
 def device_status(workspace, stream=None) -> int:
