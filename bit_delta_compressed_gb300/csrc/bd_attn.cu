@@ -30,8 +30,8 @@ bool sizes_ok(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, 
            (head_dim == 64 || head_dim == 128);
 }
 
-// The workspace of one call: the header and the tickets lie where every call
-// expects them, the rest is scratch.
+// The workspace of one call: the header, which holds the tickets, lies where every
+// call expects it, the rest is scratch.
 struct Workspace {
     DecodeBuffers decode;
     TilePlan plan;
@@ -48,7 +48,7 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
         at += round_up(bytes, kAlign);
         return r;
     };
-    w.decode.tickets = reinterpret_cast<int*>(take(kMaxBlocks * sizeof(int)));
+    w.decode.tickets = reinterpret_cast<unsigned*>(p ? p + kTicketsAt : nullptr);
     w.decode.parts = reinterpret_cast<float*>(take(decode_parts_bytes(head_dim)));
     w.decode.own = reinterpret_cast<float*>(take((size_t)batch * q_heads * head_dim * sizeof(float)));
     w.decode.own_ml = reinterpret_cast<float2*>(take((size_t)batch * q_heads * sizeof(float2)));

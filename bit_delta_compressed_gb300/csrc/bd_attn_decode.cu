@@ -569,9 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
-                const int n = atomicAdd(buf.tickets + c0, 1);
+                unsigned* ticket = buf.tickets + c0 / 4;
+                const int at = 8 * (c0 % 4), n = atomicAdd(ticket, 1u << at) >> at & 255u;
                 last_block = n == c1 - c0;
-                if (last_block) buf.tickets[c0] = 0;
+                if (last_block) atomicAnd(ticket, ~(255u << at));
                 __threadfence();
             }
             __syncthreads();

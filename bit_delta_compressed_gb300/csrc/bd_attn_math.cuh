@@ -95,13 +95,17 @@ bd_status launch_close(void (*kernel)(Params...), dim3 grid, dim3 block, size_t 
 }
 
 // ---- the workspace -----------------------------------------------------------
-// header, then tickets of units that several blocks join (zero between calls),
-// then what one call needs.
-constexpr int kMaxBlocks = 2048;
+// The header, then what one call needs.  The tickets of units that several blocks
+// join have to be zero when a call begins, so they lie in the header, where no other
+// entry point writes: a byte for each block, four to a word.  A unit has no more parts
+// than there are blocks, so a byte never runs over.
+constexpr size_t kTicketsAt = 64;
+constexpr int kMaxBlocks = (int)(kHeaderBytes - kTicketsAt);
+static_assert(kMaxBlocks < 256, "a ticket is a byte");
 
 struct DecodeBuffers {
     float* parts;        // [2 * blocks] open units: O [R][D], (m, l) [R]
-    int* tickets;        // [kMaxBlocks]
+    unsigned* tickets;   // [kMaxBlocks / 4], a byte for each block
     float* scores;       // [B, Hq, score_stride] scaled scores of the visible own keys, by place among them
     float* lse;          // [B, Hq] log2 of the softmax's denominator
     int64_t score_stride;

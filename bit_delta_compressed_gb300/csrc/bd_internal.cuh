@@ -4,6 +4,9 @@
 //   u32 [0]  status word: device-detected errors, OR-ed as (1 << bd_status)
 //   u32 [1]  compress: ticket of the last-block-done reduction
 //   u32 [2]  diagnostic: where a bounded wait gave up (0 = never)
+//   u8 [64 .. 255]  attention decode: tickets of units that several blocks join
+//            (zero between calls; nothing behind the header outlives a call but a
+//            grouping, so calls of every kind may take turns in one workspace)
 #pragma once
 
 #include <cuda_runtime.h>

@@ -304,7 +304,9 @@ typedef struct {
  *               q_heads * head_dim contiguous values; q_stride a multiple of 8.
  *   out       : device bf16 [rows, q_heads, head_dim], contiguous.
  *   workspace : device, zero-filled once before its first use, ws_bytes >=
- *               bitdelta_attn_workspace(...).
+ *               bitdelta_attn_workspace(...).  Calls of this library that follow one
+ *               another may share one, whatever they do (but a grouping that is to
+ *               be used again needs one that no other kind of call writes to).
  * Every call is deterministic: equal inputs give equal bits. */
 
 /* Bytes of device workspace for calls of at most `tokens` query rows and
