@@ -159,6 +159,15 @@ class CachedAttention:
 
     def evict(self, src, dst, budget: int, recent: int) -> None:
         """Move requests from slots ``src`` to the free slots ``dst`` with at most
-        ``budget`` keys a head; the mask's first tokens stay."""
+        ``budget`` keys a head; the mask's first tokens stay.
+
+        A kept key stands at its new place from then on, nearer to the keys to come
+        than it was.  So that none comes back into the window, it has to lie among
+        the keys that stay: ``recent`` >= window - 1 (the next query sees itself and
+        as many before it)."""
+        window = self.mask["window"]
+        if window > 0 and recent < window - 1:
+            raise ValueError("recent must be at least window - 1 (%d): keys that left the window would come back into it"
+                             % (window - 1))
         self.bd.cache_evict(self.k, self.v, self.weights, self.lens, src, dst, budget, self.evict_ws,
                             sinks=self.mask["sinks"], recent=recent)

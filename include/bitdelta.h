@@ -365,7 +365,11 @@ size_t bitdelta_evict_workspace(int64_t n, int32_t kv_heads, int64_t capacity);
  *   budget   : 1 <= budget <= capacity, sinks + recent <= budget.
  *   kept     : NULL, or device int32 [n, kv_heads, budget]: the kept keys' old
  *              places, -1 behind the last.
- * K, V and weights of the kept keys are copied; src is left as it is. */
+ * K, V and weights of the kept keys are copied; src is left as it is.
+ * Positions are places in a slot, so a kept key's distance to later keys shrinks
+ * by the number of keys that went.  Under a window, keys that had left it come
+ * back into it, unless recent >= window - 1: then it shows the same keys before
+ * and after (with `sinks` own keys kept that the mask's first tokens hold). */
 bd_status bitdelta_cache_evict(const bd_kv_cache *cache, float *weights, int32_t *lens,
                                const int32_t *src, const int32_t *dst, int64_t n, int64_t budget,
                                int64_t sinks, int64_t recent, int32_t *kept, void *workspace,

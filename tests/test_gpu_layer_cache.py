@@ -101,3 +101,27 @@ def test_decode_steps_from_a_graph(bd, weigh):
             assert ((c.weights[1, :, at].double() - one).abs() <= (rel[0] + (HQ // HK + 2) * ref.F32) * one).all()
             most = (step + 2) * (HQ // HK)
             assert ((c.weights[1, :, :at + 1].double().sum(-1) - most).abs() <= 1e-3 * most).all()
+
+
+@pytest.mark.parametrize("window,sinks,prefix", [(9, 0, 0), (9, 3, 0), (1, 2, 0), (9, 4, 2), (9, 2, 12), (16, 0, 20)])
+def test_windowed_steps_after_an_eviction(bd, window, sinks, prefix):
+    """The steps see what they would see had nothing been evicted: the mask taken over the tokens' own positions."""
+    c, g = make(bd, [30, 0, 0, 0, prefix], window=window, sinks=sinks, weigh=True)
+    c.weights.copy_(torch.rand(c.weights.shape, generator=g, device=DEV))
+    how = (i32([0]), i32([4])) if prefix else (None, None)
+    front = [(c.k[4, j].double(), c.v[4, j].double()) for j in range(prefix)]
+    tokens = front + [(c.k[0, j].double(), c.v[0, j].double()) for j in range(30)]
+    c.evict(i32([0]), i32([2]), budget=24, recent=window + 2)
+    assert int(c.lens[2]) == 24
+    for _ in range(12):
+        q, k, v = rows(1, g)
+        out = c.decode(q, k, v, i32([2]), *how).view(HQ, D)
+        tokens.append((k.view(HK, D).double(), v.view(HK, D).double()))
+        t = len(tokens) - 1
+        seen = [p for p in range(t + 1) if p < sinks or p > t - window]
+        kk, vv = (torch.stack([tokens[p][i] for p in seen]) for i in (0, 1))
+        # the same keys in a cache of their own, all of them visible
+        kc, vc = (x[None].to(torch.bfloat16) for x in (kk, vv))
+        want, bound, _ = ref.attention(q.view(1, HQ, D), kc, vc, i32([len(seen)]), rounded=bool(prefix))
+        ref.assert_close(out[None], want, bound)
+        assert bd.device_status(c.ws) == 0

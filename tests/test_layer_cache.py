@@ -22,6 +22,9 @@ class Recorder:
         self.lens, self.slots, self.pslots, self.plens = lens, slots, pslots, plens
         return torch.zeros_like(q)
 
+    def cache_evict(self, k, v, weights, lens, src, dst, budget, ws, **rest):
+        self.evicted = dict(src=src, dst=dst, budget=budget, **rest)
+
     def attn_prefill(self, q, k, v, cu_q, lens, ws, slots=None, prefix_slots=None, prefix_lens=None, **rest):
         self.cu, self.lens, self.slots, self.pslots, self.plens = cu_q, lens, slots, prefix_slots, prefix_lens
         return torch.zeros_like(q)
@@ -146,3 +149,17 @@ def test_prefill_with_offsets_that_do_not_ascend(cu):
     want["lens"] = i32([2, 3, 1, 2])
     same(c, want)
     assert c.bd.cu.tolist() == cu
+
+
+def test_evict_under_a_window():
+    """Kept keys move nearer: keys that had left the window would be in it again unless it lies among the recent ones."""
+    for window, recent, ok in ((0, 0, True), (1, 0, True), (4, 2, False), (4, 3, True), (4, 5, True), (4, 0, False)):
+        c = layer.CachedAttention(Recorder(), SLOTS, CAP, HQ, HK, D, tokens=4, batch=4, window=window, sinks=1, weigh=True, device="cpu")
+        c.bd.evicted = None
+        if ok:
+            c.evict(i32([0]), i32([1]), 6, recent)
+            assert c.bd.evicted["recent"] == recent and c.bd.evicted["sinks"] == 1
+        else:
+            with pytest.raises(ValueError, match="window"):
+                c.evict(i32([0]), i32([1]), 6, recent)
+            assert c.bd.evicted is None
