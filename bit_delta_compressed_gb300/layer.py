@@ -157,9 +157,14 @@ class CachedAttention:
                                    prefix_lens=self._prefix_lens(prefix_slots), **self.mask)
         return out.view(-1, hq * d)
 
-    def evict(self, src, dst, budget: int, recent: int) -> None:
+    def evict(self, src, dst, budget: int, recent: int, sinks: int | None = None) -> None:
         """Move requests from slots ``src`` to the free slots ``dst`` with at most
-        ``budget`` keys a head; the mask's first tokens stay.
+        ``budget`` keys a head, the first ``sinks`` and the last ``recent`` among them.
+
+        ``sinks``: how many of the mask's first tokens are own keys of these requests:
+        all of them (None) without a prefix, max(0, mask's - P) behind one of P keys --
+        the rest lie in the prefix, and own keys kept in their stead would take the
+        places of heavier ones.
 
         A kept key stands at its new place from then on, nearer to the keys to come
         than it was.  So that none comes back into the window, it has to lie among
@@ -170,4 +175,4 @@ class CachedAttention:
             raise ValueError("recent must be at least window - 1 (%d): keys that left the window would come back into it"
                              % (window - 1))
         self.bd.cache_evict(self.k, self.v, self.weights, self.lens, src, dst, budget, self.evict_ws,
-                            sinks=self.mask["sinks"], recent=recent)
+                            sinks=self.mask["sinks"] if sinks is None else sinks, recent=recent)

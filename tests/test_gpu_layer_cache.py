@@ -125,3 +125,22 @@ def test_windowed_steps_after_an_eviction(bd, window, sinks, prefix):
         want, bound, _ = ref.attention(q.view(1, HQ, D), kc, vc, i32([len(seen)]), rounded=bool(prefix))
         ref.assert_close(out[None], want, bound)
         assert bd.device_status(c.ws) == 0
+
+
+@pytest.mark.parametrize("prefix", [2, 12])
+def test_eviction_behind_a_prefix_keeps_the_heaviest(bd, prefix):
+    """Own keys that the mask's first tokens do not hold are kept by weight alone, and the windowed steps stay right."""
+    c, g = make(bd, [30, 0, 0, 0, prefix], window=5, sinks=4, weigh=True)
+    c.weights.copy_(torch.rand(c.weights.shape, generator=g, device=DEV))
+    c.weights[0, :, :4] = 0                               # the first own keys are the lightest
+    kept, before = max(0, 4 - prefix), c.k[0].clone()
+    c.evict(i32([0]), i32([2]), budget=15, recent=6, sinks=kept)
+    for h, rows_kept in enumerate(ref.evict(c.weights.cpu(), c.lens.cpu(), i32([0]).cpu(), 15, kept, 6)[0]):
+        assert rows_kept[kept] >= 4
+        assert torch.equal(c.k[2, :15, h], before[rows_kept, h])
+    q, k, v = rows(1, g)
+    out = c.decode(q, k, v, i32([2]), i32([0]), i32([4])).view(1, HQ, D)
+    keys, values = (torch.cat([t[4, :min(4, prefix)], t[0, :kept], t[0, 26:30], new.view(1, HK, D)])[None]
+                    for t, new in ((c.k, k), (c.v, v)))
+    want, bound, _ = ref.attention(q.view(1, HQ, D), keys, values, i32([9]), rounded=True)
+    ref.assert_close(out, want, bound)

@@ -163,3 +163,11 @@ def test_evict_under_a_window():
             with pytest.raises(ValueError, match="window"):
                 c.evict(i32([0]), i32([1]), 6, recent)
             assert c.bd.evicted is None
+
+
+def test_evict_behind_a_prefix():
+    """The mask's first tokens lie in the prefix as far as it reaches: the caller says how many are own keys."""
+    c = layer.CachedAttention(Recorder(), SLOTS, CAP, HQ, HK, D, tokens=4, batch=4, sinks=4, weigh=True, device="cpu")
+    for sinks, kept in ((None, 4), (0, 0), (1, 1)):
+        c.evict(i32([0]), i32([1]), 6, 2, sinks=sinks)
+        assert c.bd.evicted["sinks"] == kept
