@@ -45,6 +45,10 @@ constexpr int kRuns = 128;                // runs of requests that a block looks
 // bf16 terms, so that it keeps 16 significant bits and the result is rounded once,
 // at its end.  With up to 8 heads the second term costs nothing (it takes rows 8 to
 // 15 of the product), with more a second product, and the bytes still bound it.
+// An infinite value times the second term, which may be zero or of the other sign,
+// would make a NaN of an infinite result.  With 8 rows the second terms' sum stands
+// by itself and is added to a finite first one only; with 16 both go to one sum, so the first
+// term is rounded towards zero and the second takes 2^-23 of the probability more, so that it is never zero.
 // Two stages a warp: of the 64 KB that 8 warps then load ahead nothing is missed, and
 // a third makes the reads of large calls slower (284 -> 294 us on the 128 requests).
 // 16 rows for up to 8 heads: one request of 300 keys 7.9 -> 9.3 us.
@@ -439,17 +443,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
 #pragma unroll
                     for (int e = 0; e < 4; ++e) p[e] = exp2_approx(s[e / 2][2 * i + e % 2] - use);
                     l[i] += (p[0] + p[1]) + (p[2] + p[3]);
-                    const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
                     if constexpr (R == 8) {
+                        const uint32_t h0 = pack_bf16(p[0], p[1]), h1 = pack_bf16(p[2], p[3]);
                         pf[0] = h0;
                         pf[1] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
                         pf[2] = h1;
                         pf[3] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
                     } else {
+                        const uint32_t h0 = pack_bf16_down(p[0], p[1]), h1 = pack_bf16_down(p[2], p[3]);
+                        constexpr float more = 1.f + 1.f / (1 << 23);
                         pf[i] = h0;
                         pf[2 + i] = h1;
-                        pl[i] = pack_bf16(p[0] - bf16_lo(h0), p[1] - bf16_hi(h0));
-                        pl[2 + i] = pack_bf16(p[2] - bf16_lo(h1), p[3] - bf16_hi(h1));
+                        pl[i] = pack_bf16(fmaf(p[0], more, -bf16_lo(h0)), fmaf(p[1], more, -bf16_hi(h0)));
+                        pl[2 + i] = pack_bf16(fmaf(p[2], more, -bf16_lo(h1)), fmaf(p[3], more, -bf16_hi(h1)));
                     }
                 }
 #pragma unroll
@@ -475,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
             if constexpr (R == 8) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    o[i][0] += o[i][2];
-                    o[i][1] += o[i][3];
+                    o[i][0] += isfinite(o[i][0]) ? o[i][2] : 0.f;
+                    o[i][1] += isfinite(o[i][1]) ? o[i][3] : 0.f;
                 }
             }
             const bool open_start = seg_tile > 0, open_end = c.end < c.tiles;

@@ -61,6 +61,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
+// The same, rounded towards zero.
+__device__ __forceinline__ uint32_t pack_bf16_down(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // What a row's sum divides by: a row that saw nothing gives zeros, a NaN stays.
 __device__ __forceinline__ float inverse(float l) { return l > 0.f ? 1.f / l : l; }
 
