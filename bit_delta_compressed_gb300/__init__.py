@@ -365,6 +365,12 @@ def _weights_ptr(weights, dev, S, H, C):
     return weights.data_ptr()
 
 
+def _mask_args(window, sinks):
+    """As the C ABI's int32 has them: a number beyond it means no more than the largest
+    (no position reaches it), and one below zero stays one."""
+    return max(-1, min(window, 0x7FFFFFFF)), max(-1, min(sinks, 0x7FFFFFFF))
+
+
 def _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B):
     if prefix_ids is None and prefix_slots is None and prefix_lens is None:
         return None, None, None, 0
@@ -405,7 +411,7 @@ def attn_decode_prefix(q, k_cache, v_cache, lens, prefix_ids, prefix_slots, pref
     ``bitdelta_attn_decode_prefix``)."""
     (S, C, Hk, D), dev, desc = _desc_of(k_cache, v_cache)
     B, H, stride, out = _attn_args(q, D, out, dev)
-    rest = (window, sinks, D ** -0.5 if scale is None else scale, _weights_ptr(weights, dev, S, Hk, C), out.data_ptr(),
+    rest = (*_mask_args(window, sinks), D ** -0.5 if scale is None else scale, _weights_ptr(weights, dev, S, Hk, C), out.data_ptr(),
             *_workspace(workspace, dev), _stream(stream))
     ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B)
     lib = get_lib()
@@ -432,7 +438,7 @@ def attn_prefill(q, k_cache, v_cache, cu_q, lens, workspace, slots=None, window:
     ids, pslots, plens, P = _prefix_args(prefix_ids, prefix_slots, prefix_lens, dev, B)
     check(get_lib().bitdelta_attn_prefill(q.data_ptr(), stride, T, B, H, desc, _int32("slots", slots, dev, B),
                                           _int32("cu_q", cu_q, dev, B + 1), _int32("lens", lens, dev, B), ids, pslots, plens, P,
-                                          window, sinks, D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                          *_mask_args(window, sinks), D ** -0.5 if scale is None else scale, out.data_ptr(),
                                           *_workspace(workspace, dev), _stream(stream)),
           "bitdelta_attn_prefill")
     return out

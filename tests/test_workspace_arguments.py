@@ -41,6 +41,7 @@ class Library:
     def __getattr__(self, name):
         def call(*args):
             self.called.append(name)
+            self.args = args
             return bd.BD_OK
         return call
 
@@ -91,6 +92,21 @@ def test_attention_calls(lib, call):
         with pytest.raises(ValueError):
             run({**operands(), "ws": ws})
     assert len(lib.called) == 1
+
+
+@pytest.mark.parametrize("given,passed", [(0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1),
+                                          (10 ** 30, 2 ** 31 - 1), (-1, -1), (-2 ** 32, -1), (-2 ** 32 + 5, -1)])
+def test_masks_beyond_32_bits(lib, given, passed):
+    """A window or a number of first tokens that the C ABI's int32 does not hold is not cut down to its low bits."""
+    o = operands()
+    for mask in (dict(window=given, sinks=3), dict(window=3, sinks=given)):
+        want = [passed if x == given else x for x in mask.values()]
+        bd.attn_decode(o["q"], o["k"], o["v"], o["lens"], o["ws"], out=o["out"], **mask)
+        assert list(lib.args[7:9]) == want
+        bd.attn_decode_prefix(o["q"], o["k"], o["v"], o["lens"], o["ids"], o["pslots"], o["plens"], o["ws"], out=o["out"], **mask)
+        assert list(lib.args[11:13]) == want
+        bd.attn_prefill(o["q"], o["k"], o["v"], o["cu"], o["lens"], o["ws"], out=o["out"], **mask)
+        assert list(lib.args[13:15]) == want
 
 
 M, N, K = 4, 32, 64
