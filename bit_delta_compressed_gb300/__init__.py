@@ -407,8 +407,8 @@ def attn_decode_prefix(q, k_cache, v_cache, lens, prefix_ids, prefix_slots, pref
                        window: int = 0, sinks: int = 0, scale=None, weights=None, out=None, stream=None):
     """``attn_decode`` for requests that share prefixes: request b's keys follow
     the ``prefix_lens[p]`` keys in slot ``prefix_slots[p]``, p = ``prefix_ids[b]``
-    (-1: none), which are read once for all requests that name them (see
-    ``bitdelta_attn_decode_prefix``)."""
+    (-1: none), which are read once for up to 256 rows, requests times heads of a
+    group (see ``bitdelta_attn_decode_prefix``)."""
     (S, C, Hk, D), dev, desc = _desc_of(k_cache, v_cache)
     B, H, stride, out = _attn_args(q, D, out, dev)
     rest = (*_mask_args(window, sinks), D ** -0.5 if scale is None else scale, _weights_ptr(weights, dev, S, Hk, C), out.data_ptr(),

@@ -17,17 +17,18 @@
 // since the last time (with every growth 750 us where this took 737 on 8192 tokens); P is then at most
 // 2^8 and rounds no worse.  Its rounding to bf16 is the one that the products ask for;
 // scores, maxima, sums and outputs stay f32.
-// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 670 us for the
-// first calls after a pause = 1.64 PFLOP/s, 86% of the measured bf16 burst rate, and 705-730 us
-// call after call = 1.53 PFLOP/s, 90% of the measured sustained rate (1360 W, the power cap
-// holds the clock at 1.8 GHz); 8 prompts of 333 to 2048 tokens behind up to 700, seeing
+// Measured (64 query heads on 8 of 128): a prompt of 8192 tokens 705-730 us call after
+// call = 1.51-1.56 PFLOP/s, 79-82% of the measured bf16 burst rate and 88-91% of the sustained
+// one (1360 W, the power cap holds the clock at 1.8 GHz), and 670 us in a short burst after a
+// pause; 8 prompts of 333 to 2048 tokens behind up to 700, seeing
 // 4 + 1024 keys, 267 us (their visible pairs alone 133).  The tensor pipe is active 73% of
 // an SM's busy cycles; what is left are the hand-overs of S -- product to softmax and back,
 // ~600 cycles each of ~1500 that a group's turn takes.  Blocks of 80 keys, for which both
 // groups' S have room, took 896 us where 128 took 768: a softmax step costs ~600 cycles
 // whatever its width.  With two or three warps a scheduler, an instruction on the way from
 // one wait to the next costs 5 to 10 cycles: hence no divisions between units, no votes in
-// the waits, and a step without spilled registers.
+// the waits.  (The kernel is compiled with 152 bytes of spill stores and 172 of loads a
+// thread: a softmax thread keeps a row's 128 scores beside the walk over the units.)
 //
 // With enough units each block takes whole ones and writes the result.  Else the
 // blocks of keys of all units form one line that is cut into equal parts for the
@@ -51,7 +52,7 @@ constexpr int kKeys = 128;                 // of a block
 constexpr int kThreads = 384;
 constexpr uint32_t kLimit = 1u << 20;      // tries of a wait, of 1 us at most each
 // Blocks that joining the parts costs about as much as.  Split / whole: 64 new tokens on
-// 16,000 keys 42 / 197 us, on 2,000 25 / 36; but 700 tokens of a new prompt 48 / 24.
+// 16,000 keys 46 / 182 us, on 2,000 29 / 34; but 700 tokens of a new prompt 54 / 23.
 constexpr int kSplitPrice = 8;
 constexpr float kGrow = 8.f;               // powers of two that a maximum may grow before a rescale
 

@@ -68,7 +68,7 @@ class CachedAttention:
 
     k, v : bf16 [slots, capacity, kv_heads, head_dim]; lens : int32 [slots], the
     keys of every slot; weights : f32 [slots, kv_heads, capacity], what decode
-    steps gave each key (None unless ``weigh``).  All on the device: a decode
+    steps gave each key (None unless ``weigh``; a prompt's own queries give none).  All on the device: a decode
     step can be captured in a CUDA graph.  A shared prefix lies in a slot of its
     own, filled by ``prefill`` like any other.
 

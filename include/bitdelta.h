@@ -292,6 +292,10 @@ typedef struct {
  *     Cached values that no query of the call sees never reach a result, NaN and
  *     infinities included.  (A non-finite value that some query of a prefill or
  *     prefix call sees may reach others that are computed with it.)
+ *   Precision.  Decode multiplies its own keys' values by probabilities of 16
+ *     significant bits; prefill, and the prefixes' keys in decode, by ones rounded
+ *     to bf16 (relative error of the result 1.7e-3 and 2.1e-3 to 2.3e-3, 1.7e-3
+ *     being its own rounding).
  *   Requests.  slots: device int32 [B], the slot of each request (NULL: request
  *     b owns slot b).  lens: device int32 [B], its own keys in the cache,
  *     0 <= lens[b] <= capacity.  A request with a slot, length or prefix id
@@ -327,7 +331,7 @@ bd_status bitdelta_attn_decode(const void *q, int64_t q_stride, int64_t B, int32
                                void *workspace, size_t ws_bytes, void *stream);
 
 /* The same for requests that share prefixes: a prefix's keys are read once
- * for all requests that name it.  (Requests of one variant share its prompt;
+ * for 256 rows (requests that name it x query heads of a group).  (Requests of one variant share its prompt;
  * the keys of different variants differ.)  The weights count own keys only. */
 bd_status bitdelta_attn_decode_prefix(const void *q, int64_t q_stride, int64_t B, int32_t q_heads,
                                       const bd_kv_cache *cache, const int32_t *slots, const int32_t *lens,
@@ -340,7 +344,8 @@ bd_status bitdelta_attn_decode_prefix(const void *q, int64_t q_stride, int64_t B
  * int32 [B + 1], ascending from 0 to T) are request b's newest tokens, the last
  * of them at its last position; their keys are already in the cache.  With a
  * prefix, the queries see it as decode does.  Rows outside every request's
- * range are left as they are.  From the first request on whose offsets do not
+ * range are left as they are.  (Each request's tiles read its prefix for
+ * themselves.)  From the first request on whose offsets do not
  * ascend within [0, T], rows become zeros, and BD_ERR_SLOT is set. */
 bd_status bitdelta_attn_prefill(const void *q, int64_t q_stride, int64_t T, int64_t B, int32_t q_heads,
                                 const bd_kv_cache *cache, const int32_t *slots, const int32_t *cu_q,
@@ -357,7 +362,8 @@ size_t bitdelta_evict_workspace(int64_t n, int32_t kv_heads, int64_t capacity);
  * `sinks`, the last `recent`, and of the others the heaviest by `weights`
  * (equal weights: the earlier key; a NaN counts as the heaviest).  The kept
  * keys stay in order.
- *   weights  : device f32 [slots, kv_heads, capacity].
+ *   weights  : device f32 [slots, kv_heads, capacity].  Decode steps add to them,
+ *              prompts do not: of keys that no step has weighed the earliest stay.
  *   lens     : device int32 [slots] (here a length for every SLOT): lens[dst]
  *              becomes min(lens[src], budget).
  *   src, dst : device int32 [n].  No slot may be in both, nor twice in dst: such a
