@@ -63,6 +63,11 @@ def chained_layer(bd, lin: dict, h, V: int, ws, bufs: dict, path: str = "auto", 
                 "gate": (h1, g), "up": (h1, u), "down": (a, d)}
 
 
+def _held(name: str):
+    """A tensor that stays in its place: what is assigned to it is copied into it."""
+    return property(lambda self: getattr(self, name), lambda self, t: getattr(self, name).copy_(t))
+
+
 class CachedAttention:
     """One layer's key/value cache and the attention on it.
 
@@ -76,6 +81,8 @@ class CachedAttention:
     left as it is: nothing is appended, its rows come out as zeros, and the status
     word of ``ws`` holds ``BD_ERR_SLOT``."""
 
+    k, v, lens, weights = _held("_k"), _held("_v"), _held("_lens"), _held("_weights")
+
     def __init__(self, bd, slots: int, capacity: int, q_heads: int, kv_heads: int, head_dim: int, tokens: int,
                  batch: int, window: int = 0, sinks: int = 0, weigh: bool = False, device="cuda"):
         import torch
@@ -88,14 +95,14 @@ class CachedAttention:
         shape = (slots, capacity, kv_heads, head_dim)
         self.rows_k = torch.zeros(slots * capacity + 1, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
         self.rows_v = torch.zeros_like(self.rows_k)
-        self.k, self.v = self.rows_k[:-1].view(shape), self.rows_v[:-1].view(shape)
+        self._k, self._v = self.rows_k[:-1].view(shape), self.rows_v[:-1].view(shape)
         self.slot_lens = torch.zeros(slots + 1, dtype=torch.int32, device=device)
         self.slot_lens[-1] = capacity
-        self.lens = self.slot_lens[:-1]
-        self.weights = None
+        self._lens = self.slot_lens[:-1]
+        self._weights = None
         if weigh:
             self.slot_weights = torch.zeros(slots + 1, kv_heads, capacity, device=device)
-            self.weights = self.slot_weights[:-1]
+            self._weights = self.slot_weights[:-1]
             self.zero = torch.zeros((), device=device)
         self.ws = bd.attn_workspace(tokens, batch, q_heads, kv_heads, head_dim, capacity if weigh else 0, device)
         self.evict_ws = bd.evict_workspace(batch, kv_heads, capacity, device)

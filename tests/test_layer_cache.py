@@ -171,3 +171,18 @@ def test_evict_behind_a_prefix():
     for sinks, kept in ((None, 4), (0, 0), (1, 1)):
         c.evict(i32([0]), i32([1]), 6, 2, sinks=sinks)
         assert c.bd.evicted["sinks"] == kept
+
+
+def test_assigned_tensors_reach_the_steps():
+    """A cache that is put back from a copy goes on from there."""
+    c, want = make([0, 3, 1, 2])
+    c.decode(*rows(2), i32([0, 1]))
+    for name, t in want.items():
+        setattr(c, name, t)
+    c.lens += 1
+    want["lens"] += 1
+    q, k, v = rows(1)
+    c.decode(q, k, v, i32([3]))
+    put(want, k, v, 0, 3, 3)
+    want["lens"] = i32([1, 4, 2, 4])
+    same(c, want)
