@@ -25,6 +25,8 @@ q and k by position, where a model does, is its caller's.
 """
 from __future__ import annotations
 
+import contextlib
+
 NAMES = ("q", "k", "v", "o", "gate", "up", "down")
 
 
@@ -121,6 +123,15 @@ class CachedAttention:
             # (a number would be copied from the host, which the capture of a graph refuses)
             self.slot_weights[place // capacity, :, place % capacity] = self.zero
 
+    @contextlib.contextmanager
+    def _given_back(self, to, have):
+        """The lengths before the step, if its attention call is refused."""
+        try:
+            yield
+        except Exception:
+            self.slot_lens[to] = have
+            raise
+
     def _prefix_lens(self, prefix_slots):
         return None if prefix_slots is None else self.slot_lens[self._slots(prefix_slots)]
 
@@ -134,9 +145,10 @@ class CachedAttention:
         self._append(k, v, torch.where(have < capacity, torch.add(have, to, alpha=capacity), -1))
         lens = have + 1                           # beyond a full slot's capacity: the call below reports it
         self.slot_lens[to] = lens.clamp_max(capacity)
-        out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots,
-                                         self._prefix_lens(prefix_slots), self.ws, slots=slots, weights=self.weights,
-                                         **self.mask)
+        with self._given_back(to, have):
+            out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots,
+                                             self._prefix_lens(prefix_slots), self.ws, slots=slots, weights=self.weights,
+                                             **self.mask)
         return out.view(-1, hq * d)
 
     def prefill(self, q, k, v, slots, cu_q, prefix_ids=None, prefix_slots=None):
@@ -159,9 +171,10 @@ class CachedAttention:
         row = torch.arange(T, dtype=torch.int32, device=q.device)
         self._append(k, v, (start[torch.searchsorted(steady, row, right=True)] + row).clamp_min_(-1))
         self.slot_lens[to] = torch.where(fits, lens, have)
-        out = self.bd.attn_prefill(q.view(-1, hq, d), self.k, self.v, cu_q, lens, self.ws, slots=slots,
-                                   prefix_ids=prefix_ids, prefix_slots=prefix_slots,
-                                   prefix_lens=self._prefix_lens(prefix_slots), **self.mask)
+        with self._given_back(to, have):
+            out = self.bd.attn_prefill(q.view(-1, hq, d), self.k, self.v, cu_q, lens, self.ws, slots=slots,
+                                       prefix_ids=prefix_ids, prefix_slots=prefix_slots,
+                                       prefix_lens=self._prefix_lens(prefix_slots), **self.mask)
         return out.view(-1, hq * d)
 
     def evict(self, src, dst, budget: int, recent: int, sinks: int | None = None) -> None:

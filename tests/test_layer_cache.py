@@ -186,3 +186,19 @@ def test_assigned_tensors_reach_the_steps():
     put(want, k, v, 0, 3, 3)
     want["lens"] = i32([1, 4, 2, 4])
     same(c, want)
+
+
+def test_refused_calls_append_nothing():
+    """A step whose attention call is refused leaves the lengths as they were, so it can be made again."""
+    c, want = make([0, 3, CAP, 2])
+
+    def refuse(*args, **how):
+        raise ValueError("refused")
+    c.bd.attn_decode_prefix = c.bd.attn_prefill = refuse
+    for step in (lambda: c.decode(*rows(3), i32([0, 2, 3])), lambda: c.decode(*rows(2), i32([-1, SLOTS])),
+                 lambda: c.prefill(*rows(6), i32([3, 0, 2, 9]), i32([0, 2, 3, 5, 6]))):
+        with pytest.raises(ValueError, match="refused"):
+            step()
+        assert torch.equal(c.lens, want["lens"])
+        for b, n in enumerate(want["lens"].tolist()):
+            assert torch.equal(c.k[b, :n], want["k"][b, :n]) and torch.equal(c.weights[b, :, :n], want["weights"][b, :, :n])
