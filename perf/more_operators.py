@@ -1,0 +1,395 @@
+"""A key/value cache held in 4 bits, as one decoder layer of the multi-variant server keeps it: new tokens quantised as they are
+written, tokens read back, and attention over the cache, for single tokens and for prompts.
+
+A cache is uint8 [slots, kv_heads, capacity / 16, 17 * head_dim]: blocks of 16 tokens of one head, a request owns a slot.
+32 values of a head of a token share a scale s, an unsigned float of 5 exponent and 3 mantissa bits (bias 15) nearest (ties to
+even) to their largest magnitude / 7, at most 240; a value is n s with n = x / s rounded to nearest (ties to even) in [-7, 7].
+Stored is n + 8.  With D = head_dim, the bytes of a block are
+  [0, 8 D)             K, 16-bit units [token][D / 8][2]: unit (w, half) holds dims 8 w + 2 f + half
+  [8 D, 16 D)          V, 16-bit units [token / 2][D / 4][token % 2]: unit w holds dims 4 w + f
+  [16 D, 16.5 D)       scales of K [token][D / 32]
+  [16.5 D, 17 D)       scales of V [D / 32][token]
+where field f = 0, 1 of a unit lies at bits 9-6 and 5-2, and f = 2, 3 lies there once the unit's bytes are swapped.
+
+A query at position t sees key p of its request if p <= t and (p < sinks or window == 0 or p > t - window).  A query that sees
+nothing gives zeros."""
+import math
+
+import torch
+
+own = False
+
+# ---------------------------------------------------------------------------------------------------------------------
+# The cases.  64 query heads, 8 key/value heads, head_dim 128 and 128 requests a decode step are this repository's
+# decoder-layer workload; the other head layouts are generic ones.
+# ---------------------------------------------------------------------------------------------------------------------
+
+
+def listed():
+    wide = {"q_heads": 64, "kv_heads": 8, "head_dim": 128}
+    return [
+        # append: new tokens are quantised and written, and what the cache now holds of them is read back.
+        # one user's next token: the smallest call, latency counts
+        {"name": "append_one", "op": "append", "batch": 1, "shortest": 1, "longest": 1, "before": 300, **wide},
+        # the new keys of a whole decode step
+        {"name": "append_step", "op": "append", "batch": 128, "shortest": 1, "longest": 1, "before": 4500, **wide},
+        # later chunks of ragged prompts, which begin at odd places
+        {"name": "append_prompts", "op": "append", "batch": 8, "shortest": 333, "longest": 2048, "before": 700, **wide},
+        # read: requests that leave the 4-bit cache, whole.  One short one of a smaller model,
+        {"name": "read_one", "op": "read", "batch": 1, "shortest": 1001, "longest": 1001, "q_heads": 32, "kv_heads": 8, "head_dim": 64},
+        # and a batch of long ragged ones
+        {"name": "read_batch", "op": "read", "batch": 16, "shortest": 1, "longest": 16384, **wide},
+        # decode: one new token a request.  One user, a short chat; latency counts
+        {"name": "decode_one", "op": "decode", "batch": 1, "shortest": 300, "longest": 300, "window": 0, "sinks": 0, **wide},
+        # the stack's decode batch with ragged lengths and a windowed layer
+        {"name": "decode_window", "op": "decode", "batch": 128, "shortest": 1, "longest": 16384, "window": 4096, "sinks": 4, **wide},
+        # a few very long documents, everything visible: what 4 bits are for
+        {"name": "decode_long", "op": "decode", "batch": 4, "shortest": 90001, "longest": 131072, "window": 0, "sinks": 0, **wide},
+        # an ordinary step of a smaller model, four heads of 64 on a key/value head
+        {"name": "decode_small", "op": "decode", "batch": 16, "shortest": 391, "longest": 7777, "window": 0, "sinks": 0, "q_heads": 32, "kv_heads": 8, "head_dim": 64},
+        # prefill: several new tokens a request.  Short prompts that start a chat, one of a single token
+        {"name": "prefill_short", "op": "prefill", "batch": 3, "shortest": 1, "longest": 131, "before": 0, "window": 0, "sinks": 0, **wide},
+        # ragged prompts of a windowed layer, the later chunks of longer ones
+        {"name": "prefill_window", "op": "prefill", "batch": 8, "shortest": 333, "longest": 2048, "before": 700, "window": 1024, "sinks": 4, **wide},
+        # the last chunk of a long document, everything visible: the largest call
+        {"name": "prefill_chunk", "op": "prefill", "batch": 1, "shortest": 2048, "longest": 2048, "before": 14336, "window": 0, "sinks": 0, **wide},
+    ]
+
+
+def draw(rng):
+    def log(lo, hi):
+        return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+    q_heads, kv_heads, head_dim = rng.choice([(64, 8, 128), (64, 8, 128), (32, 8, 128), (32, 8, 64), (16, 16, 64), (48, 4, 128), (20, 4, 128), (16, 1, 128)])
+    case = {"op": rng.choice(["append", "read", "decode", "decode", "decode", "prefill", "prefill"]), "q_heads": q_heads, "kv_heads": kv_heads, "head_dim": head_dim}
+    window, sinks = rng.choice([(0, 0), (log(16, 4096), rng.choice([0, 1, 4, 64]))])
+    if case["op"] == "append":
+        if rng.random() < 0.5:
+            return {**case, "batch": log(1, 128), "shortest": 1, "longest": 1, "before": log(1, 4500)}
+        longest = log(1, 2048)
+        return {**case, "batch": log(1, 8), "shortest": log(1, longest), "longest": longest, "before": rng.choice([0, log(1, 2000)])}
+    if case["op"] == "read":
+        longest = log(1, 16384)
+        return {**case, "batch": log(1, 16), "shortest": log(1, longest), "longest": longest}
+    if case["op"] == "decode":
+        batch = log(1, 128)
+        longest = log(1, min(131072, 128 * 8192 // batch))
+        return {**case, "batch": batch, "shortest": log(1, longest), "longest": longest, "window": window, "sinks": sinks}
+    batch = log(1, 8)
+    longest = log(1, 2048 if batch < 3 else 1024)
+    return {**case, "batch": batch, "shortest": log(1, longest), "longest": longest, "before": rng.choice([0, log(1, 4000)]), "window": window, "sinks": sinks}
+
+
+def spread(lo, hi, n):
+    """n lengths from lo to hi, the longest first."""
+    return [hi - (hi - lo) * i // max(1, n - 1) for i in range(n)]
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# The format
+# ---------------------------------------------------------------------------------------------------------------------
+
+
+def quantised(x):
+    """Values [.., D] as whole numbers n + 8 (int16) and scales' bytes [.., D / 32]."""
+    x = x.float().unflatten(-1, (-1, 32))
+    want = x.abs().amax(-1) / torch.full((), 7.0, device=x.device)  # (a number would be multiplied as its reciprocal)
+    unit = ((torch.frexp(want).exponent - 4).clamp_min(-17) + 127 << 23).view(torch.float32)  # 2 to that power
+    s = ((want / unit).round() * unit).clamp_max(240.0)
+    n = (x / s.clamp_min(2.0 ** -17)[..., None]).round().clamp(-7, 7)
+    return n.flatten(-2).to(torch.int16) + 8, (s.to(torch.float16).view(torch.int16) >> 7).to(torch.uint8)
+
+
+def swapped(h):
+    return ((h & 255) << 8) | ((h >> 8) & 255)
+
+
+def units_of(n):
+    """Whole numbers [.., 4] of a unit, as int16 [..]."""
+    return (n[..., 0] << 6) | (n[..., 1] << 2) | swapped((n[..., 2] << 6) | (n[..., 3] << 2))
+
+
+def numbers_of(h):
+    """A unit's whole numbers less 8, [.., 4]."""
+    b = swapped(h)
+    return torch.stack([(h >> 6) & 15, (h >> 2) & 15, (b >> 6) & 15, (b >> 2) & 15], -1) - 8
+
+
+def k_units(n):
+    """[.., D] as 16-bit units [.., D / 8, 2]"""
+    return units_of(n.unflatten(-1, (-1, 4, 2)).transpose(-1, -2))
+
+
+def v_units(n):
+    """[.., D] as 16-bit units [.., D / 4]"""
+    return units_of(n.unflatten(-1, (-1, 4)))
+
+
+def packed(k, v):
+    """Keys and values [.., tokens, D], tokens a multiple of 16, as blocks [.., tokens / 16, 17 D]."""
+    def of16(t):
+        return t.unflatten(-2, (-1, 16))
+
+    (nk, sk), (nv, sv) = quantised(k), quantised(v)
+    ku, vu = k_units(of16(nk)), v_units(of16(nv))
+    vu = vu.unflatten(-2, (8, 2)).transpose(-1, -2)
+    parts = [ku.flatten(-3).contiguous().view(torch.uint8), vu.flatten(-3).contiguous().view(torch.uint8), of16(sk).flatten(-2), of16(sv).transpose(-1, -2).flatten(-2)]
+    return torch.cat(parts, -1)
+
+
+def scales_of(b):
+    return (b.to(torch.int16) << 7).view(torch.float16).float()
+
+
+def unpacked(blocks):
+    """Blocks [.., n, 17 D] as keys and values [.., 16 n, D] in 32 bits."""
+    d = blocks.shape[-1] // 17
+    k = numbers_of(blocks[..., : 8 * d].contiguous().view(torch.int16).unflatten(-1, (16, d // 8, 2)))
+    k = k.transpose(-1, -2).flatten(-3).float()
+    v = numbers_of(blocks[..., 8 * d: 16 * d].contiguous().view(torch.int16).unflatten(-1, (8, d // 4, 2)))
+    v = v.transpose(-2, -3).flatten(-2).flatten(-3, -2).float()
+    sk = scales_of(blocks[..., 16 * d: 16 * d + d // 2]).unflatten(-1, (16, d // 32))
+    sv = scales_of(blocks[..., 16 * d + d // 2:]).unflatten(-1, (d // 32, 16)).transpose(-1, -2)
+    k, v = [(x.unflatten(-1, (-1, 32)) * s[..., None]).flatten(-2) for x, s in ((k, sk), (v, sv))]
+    return k.flatten(-3, -2), v.flatten(-3, -2)
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# Inputs
+# ---------------------------------------------------------------------------------------------------------------------
+
+
+def prepare(case, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    hq, hk, d, n = case["q_heads"], case["kv_heads"], case["head_dim"], case["batch"]
+    op, new, before = case["op"], spread(case["shortest"], case["longest"], case["batch"]), case.get("before", 0)
+    capacity = -(-(case["longest"] + before) // 16) * 16
+    # keys have a few dims of large values; values have none
+    loud = 1 + 4 * (torch.rand(hk, d, generator=g, device="cuda") < 0.04)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    def whole(values):
+        return torch.tensor(values, dtype=torch.int32, device="cuda")
+
+    s = {"case": case, "scale": d ** -0.5}
+    s["cache"] = torch.empty(n, hk, capacity // 16, 17 * d, dtype=torch.uint8, device="cuda")
+    for slot in range(n):
+        s["cache"][slot] = packed(normal(hk, capacity, d) * loud[:, None], normal(hk, capacity, d))
+    order = torch.randperm(n, generator=g, device="cuda")
+    s["slots"] = order.to(torch.int32)
+    news = whole(new)[torch.randperm(n, generator=g, device="cuda")]
+    if op in ("append", "prefill"):
+        # how much of a request is in the cache before this chunk differs from request to request
+        s["lens"] = whole([before * (i + 1) // n for i in range(n)]) + news
+    else:
+        s["lens"] = news
+    if op != "decode":
+        s["cu_q"] = torch.cat([whole([0]), news.cumsum(0, dtype=torch.int32)])
+    tokens = n if op == "decode" else sum(new)
+    if op in ("append", "read"):
+        s["k"], s["v"] = torch.empty(2, tokens, hk, d, dtype=torch.bfloat16, device="cuda")
+        if op == "append":
+            s["new_k"], s["new_v"] = (normal(tokens, hk, d) * loud).to(torch.bfloat16), normal(tokens, hk, d)
+    else:
+        s["q"] = normal(tokens, hq, d) * 1.5
+        s["out"] = torch.empty(tokens, hq, d, dtype=torch.bfloat16, device="cuda")
+    s["longest"], s["rows"] = case["longest"] + before, tokens
+    if own:
+        import bit_delta_compressed_gb300 as bd
+
+        s["bd"] = bd
+        s["workspace"] = bd.attn4_workspace(tokens, n, hq, hk, d, longest=s["longest"] if op == "prefill" else 0, device="cuda")
+    return s
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# The plain form and the framework's calls
+# ---------------------------------------------------------------------------------------------------------------------
+
+
+def places(s):
+    """Of each row: its request, its slot and its place there."""
+    row = torch.arange(s["rows"], device="cuda")
+    of = torch.searchsorted(s["cu_q"][1:].contiguous(), row.to(torch.int32), right=True)
+    return of, s["slots"].long()[of], (s["lens"] - s["cu_q"][1:])[of].long() + row
+
+
+def plain_write(s, c):
+    d, hk = c["head_dim"], c["kv_heads"]
+    _, slot, at = places(s)
+    block, j = at // 16, at % 16
+    units, data = s["cache"].view(torch.int16), s["cache"]
+    head = torch.arange(hk, device="cuda")[:, None]
+    where = [t[:, None, None] for t in (slot, block)]
+    (nk, sk), (nv, sv) = quantised(s["new_k"]), quantised(s["new_v"])
+    i, w, g = (torch.arange(m, device="cuda") for m in (d // 4, d // 4, d // 32))
+    units[where[0], head, where[1], j[:, None, None] * (d // 4) + i] = k_units(nk).flatten(-2)
+    units[where[0], head, where[1], 4 * d + (j // 2)[:, None, None] * (d // 2) + 2 * w + (j % 2)[:, None, None]] = v_units(nv)
+    data[where[0], head, where[1], 16 * d + j[:, None, None] * (d // 32) + g] = sk
+    data[where[0], head, where[1], 16 * d + d // 2 + 16 * g + j[:, None, None]] = sv
+
+
+def plain_read(s, c):
+    d, hk = c["head_dim"], c["kv_heads"]
+    _, slot, at = places(s)
+    block, j = at // 16, at % 16
+    units, data = s["cache"].view(torch.int16), s["cache"]
+    head = torch.arange(hk, device="cuda")[:, None]
+    where = [t[:, None, None] for t in (slot, block)]
+    i, w, g = (torch.arange(m, device="cuda") for m in (d // 4, d // 4, d // 32))
+    k = numbers_of(units[where[0], head, where[1], j[:, None, None] * (d // 4) + i].unflatten(-1, (-1, 2))).transpose(-1, -2)
+    v = numbers_of(units[where[0], head, where[1], 4 * d + (j // 2)[:, None, None] * (d // 2) + 2 * w + (j % 2)[:, None, None]])
+    sk = scales_of(data[where[0], head, where[1], 16 * d + j[:, None, None] * (d // 32) + g])
+    sv = scales_of(data[where[0], head, where[1], 16 * d + d // 2 + 16 * g + j[:, None, None]])
+    return [(x.reshape(-1, hk, d // 32, 32) * y[..., None]).flatten(-2).to(torch.bfloat16) for x, y in ((k, sk), (v, sv))]
+
+
+def softmax_product(q, k, v, mask, scale):
+    """Softmax over the masked last axis and the product with the values, 32 bits; rows that see nothing are zero."""
+    s = (q @ k.transpose(-1, -2)).mul_(scale)
+    s.masked_fill_(~mask, -math.inf)
+    top = s.amax(-1, keepdim=True)
+    p = s.sub_(top.masked_fill_(top == -math.inf, 0.0)).exp_()
+    p.div_(p.sum(-1, keepdim=True).clamp_min_(1e-30))
+    return p @ v
+
+
+def sees(at, pos, window, sinks):
+    """Whether a query at position `at` sees position `pos`."""
+    seen = pos <= at
+    return seen & ((pos < sinks) | (pos > at - window)) if window else seen
+
+
+def plain_attention(s, c):
+    n, hk, d, group, longest = c["batch"], c["kv_heads"], c["head_dim"], c["q_heads"] // c["kv_heads"], s["longest"]
+    k, v = unpacked(s["cache"][s["slots"].long()])
+    k, v = k[:, :, :longest], v[:, :, :longest]
+    pos = torch.arange(longest, device="cuda")
+    if c["op"] == "decode":
+        mask = sees(s["lens"][:, None] - 1, pos, c["window"], c["sinks"])
+        return softmax_product(s["q"].float().view(n, hk, group, d), k, v, mask[:, None, None], s["scale"]).reshape(n, hk * group, d).to(torch.bfloat16)
+    of, _, at = places(s)
+    new = c["longest"]
+    i = torch.arange(s["rows"], device="cuda") - s["cu_q"].long()[of]
+    q = torch.zeros(n, new, hk * group, d, device="cuda")
+    q[of, i] = s["q"].float()
+    q = q.view(n, new, hk, group, d).permute(0, 2, 3, 1, 4)
+    t = (s["lens"] - (s["cu_q"][1:] - s["cu_q"][:-1]))[:, None] + torch.arange(new, device="cuda")
+    mask = sees(t[:, None, None, :, None], pos, c["window"], c["sinks"])
+    o = softmax_product(q, k[:, :, None], v[:, :, None], mask, s["scale"])
+    return o.permute(0, 3, 1, 2, 4).reshape(n, new, hk * group, d)[of, i].to(torch.bfloat16)
+
+
+def run(state):
+    s, c = state, state["case"]
+    op = c["op"]
+    if own:
+        bd, rest = s["bd"], {"slots": s["slots"]}
+        if op in ("append", "read"):
+            if op == "append":
+                bd.cache4_write(s["new_k"], s["new_v"], s["cache"], s["lens"], s["workspace"], cu_q=s["cu_q"], **rest)
+            bd.cache4_read(s["k"], s["v"], s["cache"], s["lens"], s["workspace"], cu_q=s["cu_q"], **rest)
+            return s["k"], s["v"]
+        rest.update(window=c["window"], sinks=c["sinks"], scale=s["scale"], out=s["out"])
+        if op == "decode":
+            return bd.attn4_decode(s["q"], s["cache"], s["lens"], s["workspace"], **rest)
+        return bd.attn4_prefill(s["q"], s["cache"], s["cu_q"], s["lens"], s["workspace"], s["longest"], **rest)
+    if op == "append":
+        plain_write(s, c)
+    return tuple(plain_read(s, c)) if op in ("append", "read") else plain_attention(s, c)
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# What a pass cannot do without, and its results in 64 bits
+# ---------------------------------------------------------------------------------------------------------------------
+
+
+def work(case):
+    hq, hk, d, n = case["q_heads"], case["kv_heads"], case["head_dim"], case["batch"]
+    lengths, window, before = spread(case["shortest"], case["longest"], n), case.get("window", 0), case.get("before", 0)
+    wide, narrow = 4 * hk * d, hk * d + hk * d // 16  # bytes of one key and its value, in bf16 and in 4 bits
+
+    def visible(t):  # positions that a query at position t sees
+        return t + 1 if not window else min(t + 1, window + min(case["sinks"], max(0, t + 1 - window)))
+
+    if case["op"] == "append":  # rows in, the cache's bytes, rows out
+        return {"bytes": sum(lengths) * (2 * wide + narrow), "flops": 0}
+    if case["op"] == "read":
+        return {"bytes": sum(lengths) * (wide + narrow), "flops": 0}
+    if case["op"] == "decode":
+        keys = sum(visible(x - 1) for x in lengths)
+        return {"bytes": keys * narrow + 4 * n * hq * d, "flops": 4 * d * hq * keys}
+    pairs = keys = 0
+    # which length meets which part before it differs by the seed: taken here in the order of prepare's own list
+    for i, x in enumerate(lengths):
+        first = before * (i + 1) // n
+        pairs += sum(visible(t) for t in range(first, first + x))
+        keys += min(first + x, x - 1 + visible(first))
+    return {"bytes": keys * narrow + 4 * sum(lengths) * hq * d, "flops": 4 * d * hq * pairs}
+
+
+def held(s, c, slot, h, size, which):
+    """The first keys (which = 0) or values (1) of a slot's head, from the places of their bits, in 64 bits."""
+    d = c["head_dim"]
+    j, e = torch.arange(size, device="cuda")[:, None], torch.arange(d, device="cuda")
+    block, t = j // 16, j % 16
+    data = s["cache"][slot, h].long()
+    if which == 0:
+        byte, field = t * (d // 2) + e // 8 * 4 + e % 2 * 2, e % 8 // 2
+        code = data[block, 16 * d + t * (d // 32) + e // 32]
+    else:
+        byte, field = 8 * d + t // 2 * d + e // 4 * 4 + t % 2 * 2, e % 4
+        code = data[block, 16 * d + d // 2 + e // 32 * 16 + t]
+    low, high = data[block, byte], data[block, byte + 1]
+    unit = torch.where(field < 2, low + 256 * high, high + 256 * low)
+    n = torch.where(field % 2 == 0, unit // 64, unit // 4) % 16 - 8
+    exponent, mantissa = code // 8, (code % 8).double()
+    s = torch.where(exponent == 0, mantissa / 8 * 2.0 ** -14, (1 + mantissa / 8) * torch.pow(2.0, exponent.double() - 15))
+    return n * s
+
+
+def as_held(x):
+    """What a cache stands for of values [.., D], by trying every scale and every number, in 64 bits."""
+    x = x.double().unflatten(-1, (-1, 32))
+    code = torch.arange(184, device=x.device)  # up to 240
+    table = torch.where(code < 8, code / 8 * 2.0 ** -14, (1 + code % 8 / 8) * torch.pow(2.0, (code // 8).double() - 15))
+    want = (x.abs().amax(-1) / 7).clamp_max(240.0)
+    above = torch.searchsorted(table, want).clamp(0, 183)
+    below = (above - 1).clamp_min(0)
+    up, down = table[above] - want, want - table[below]
+    s = table[torch.where((up < down) | ((up == down) & (above % 2 == 0)), above, below)][..., None]
+    numbers = torch.tensor([*range(-6, 8, 2), *range(-7, 8, 2)], dtype=torch.float64, device=x.device)  # the even ones win ties
+    best = numbers[(x[..., None] - numbers * s[..., None]).abs().argmin(-1)]
+    return (best * s).flatten(-2)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    n, hq, hk, d = case["batch"], case["q_heads"], case["kv_heads"], case["head_dim"]
+    if case["op"] == "append":
+        return as_held(s["new_k"]), as_held(s["new_v"])
+    lens, slots = s["lens"].tolist(), s["slots"].tolist()
+    ends = s["cu_q"].tolist() if case["op"] != "decode" else list(range(n + 1))
+    if case["op"] == "read":
+        result = torch.empty(2, ends[-1], hk, d, dtype=torch.float64, device="cuda")
+        for b, slot in enumerate(slots):
+            for h in range(hk):
+                for which in (0, 1):
+                    result[which, ends[b]: ends[b + 1], h] = held(s, case, slot, h, lens[b], which)[lens[b] - (ends[b + 1] - ends[b]):]
+        return result[0], result[1]
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
+    for b, slot in enumerate(slots):
+        size = lens[b]
+        at = torch.arange(size - (ends[b + 1] - ends[b]), size, device="cuda")[:, None]
+        pos = torch.arange(size, device="cuda")
+        hidden = pos > at
+        if case["window"]:
+            hidden = hidden | ((pos <= at - case["window"]) & (pos >= case["sinks"]))
+        for h in range(hk):
+            keys, values = held(s, case, slot, h, size, 0), held(s, case, slot, h, size, 1)
+            for j in range(h * hq // hk, (h + 1) * hq // hk):
+                score = s["q"][ends[b]: ends[b + 1], j].double() @ keys.T * s["scale"]
+                out[ends[b]: ends[b + 1], j] = torch.softmax(score.masked_fill_(hidden, -math.inf), -1) @ values
+    return out
