@@ -330,6 +330,11 @@ def work(case):
     return {"bytes": keys * narrow + 4 * sum(lengths) * hq * d, "flops": 4 * d * hq * pairs}
 
 
+def scale_table(device):
+    """The scales of the bytes up to that of 240, exactly."""
+    return torch.tensor([c / 8 * 2.0 ** -14 if c < 8 else (1 + c % 8 / 8) * 2.0 ** (c // 8 - 15) for c in range(184)], dtype=torch.float64, device=device)
+
+
 def held(s, c, slot, h, size, which):
     """The first keys (which = 0) or values (1) of a slot's head, from the places of their bits, in 64 bits."""
     d = c["head_dim"]
@@ -345,16 +350,13 @@ def held(s, c, slot, h, size, which):
     low, high = data[block, byte], data[block, byte + 1]
     unit = torch.where(field < 2, low + 256 * high, high + 256 * low)
     n = torch.where(field % 2 == 0, unit // 64, unit // 4) % 16 - 8
-    exponent, mantissa = code // 8, (code % 8).double()
-    s = torch.where(exponent == 0, mantissa / 8 * 2.0 ** -14, (1 + mantissa / 8) * torch.pow(2.0, exponent.double() - 15))
-    return n * s
+    return n * scale_table("cuda")[code]
 
 
 def as_held(x):
     """What a cache stands for of values [.., D], by trying every scale and every number, in 64 bits."""
     x = x.double().unflatten(-1, (-1, 32))
-    code = torch.arange(184, device=x.device)  # up to 240
-    table = torch.where(code < 8, code / 8 * 2.0 ** -14, (1 + code % 8 / 8) * torch.pow(2.0, (code // 8).double() - 15))
+    table = scale_table(x.device)
     want = (x.abs().amax(-1) / 7).clamp_max(240.0)
     above = torch.searchsorted(table, want).clamp(0, 183)
     below = (above - 1).clamp_min(0)
