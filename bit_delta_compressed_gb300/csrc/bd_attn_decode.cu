@@ -24,8 +24,7 @@
 // 8 requests of 32,000 keys on one head 72 us for 64 query heads and 113 for 128, 19 for the bytes.
 #include <math.h>
 
-#include "bd_attn.cuh"
-#include "bd_attn_math.cuh"
+#include "bd_attn_line.cuh"
 #include "bd_tc_common.cuh"
 
 namespace bd {
@@ -35,16 +34,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                 // keys of a tile
-// Measured on both sides: kUnitCost 0 / 3 / 8 on 128 requests over 14 prefixes (own
-// parts of 1 to 700 keys) 108 / 99 / 99 us, one request of 8000 keys 17.5 / 17.4 /
-// 16.8; kLeast 16 / 64 on the latter 17.4 / 18.3; a block for each short unit, with /
-// without, one request of 300 keys 7.8 / 10.3 us, 16 of 200 to 900 12.5 / 15.6.
-constexpr int kUnitCost = 3;              // places of a unit besides its tiles
-constexpr int kLeast = 16;                // places of a block
-constexpr int kShort = 64;                // tiles up to which a unit may have a block of its own
-constexpr int kKept = 1024;               // requests that a block keeps on chip
-constexpr int kRuns = 128;                // runs of requests that a block looks its place up in
-
 // R: rows of a unit (8 or 16 query heads).  A probability is multiplied as two
 // bf16 terms, so that it keeps 16 significant bits and the result is rounded once,
 // at its end.  With up to 8 heads the second term costs nothing (it takes rows 8 to
@@ -68,93 +57,27 @@ struct Shape {
 
 // Where the visible own keys of a request lie: the first `head` and, behind a
 // gap, the window.  Key x of the n visible ones is key x + (x >= head ? gap : 0).
+// Measured on both sides: kUnitCost 0 / 3 / 8 on 128 requests over 14 prefixes (own
+// parts of 1 to 700 keys) 108 / 99 / 99 us, one request of 8000 keys 17.5 / 17.4 /
+// 16.8; kLeast 16 / 64 on the latter 17.4 / 18.3; a block for each short unit, with /
+// without, one request of 300 keys 7.8 / 10.3 us, 16 of 200 to 900 12.5 / 15.6.
 struct Keys {
+    static constexpr int kUnitCost = 3, kLeast = 16, kShort = 64;
     int n, head, gap;
-};
-
-__device__ __forceinline__ Keys visible_keys(const Args& a, const Request& r) {
-    Keys k;
-    const int lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);
-    const int sinks = min(max(a.sinks - r.plen, 0), r.len);
-    k.gap = max(lo - sinks, 0);
-    k.head = k.gap ? sinks : r.len;
-    k.n = r.len - k.gap;
-    return k;
-}
-
-__device__ __forceinline__ int tiles_of(const Args& a, const Request& r) {
-    return max(1, (visible_keys(a, r).n + kTile - 1) / kTile);
-}
-
-// The line: every unit takes kUnitCost places (what a unit costs besides its tiles:
-// its query, its result) and one for each tile.  If all units are short and no more
-// than the blocks, each has a block of its own instead: `each` places.
-struct Line {
-    int64_t lo, hi;                        // this warp's places
-    int32_t each;                          // 0: units follow one another
-    __device__ __forceinline__ int length(int tiles) const { return each ? each : kUnitCost + tiles; }
-    __device__ __forceinline__ int lead() const { return each ? 0 : kUnitCost; }
-};
-
-// A unit on the line and its tiles [tile, end) that lie in the warp's part.
-struct Cursor {
-    int b, u, tiles, tile, end;
-    int64_t start;                         // the unit's first place
-    Request r;
-    Keys k;
-};
-
-// What a block keeps of the first requests: read once, at its beginning.  Later the
-// same loads would queue behind the keys' (2 to 4 thousand cycles each).
-struct Kept {
-    int32_t slot, len, plen;
-};
-
-__device__ __forceinline__ void load_request(const Args& a, const Kept* kept, Cursor& c) {
-    if (c.b < kKept) {
-        c.r.slot = kept[c.b].slot;
-        c.r.len = kept[c.b].len;
-        c.r.plen = kept[c.b].plen;
-    } else {
-        c.r = read_request(a, c.b);
+    static __device__ __forceinline__ Keys of(const Args& a, const Request& r) {
+        Keys k;
+        const int lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);
+        const int sinks = min(max(a.sinks - r.plen, 0), r.len);
+        k.gap = max(lo - sinks, 0);
+        k.head = k.gap ? sinks : r.len;
+        k.n = r.len - k.gap;
+        return k;
     }
-    c.k = visible_keys(a, c.r);
-    c.tiles = max(1, (c.k.n + kTile - 1) / kTile);
-}
-
-// Goes on to the first unit from c on with tiles in the part; false if there is none.
-__device__ __forceinline__ bool seek(const Args& a, const Kept* kept, const Line& line, Cursor& c, int units) {
-    while (c.start < line.hi) {
-        const int64_t first = c.start + line.lead();
-        c.tile = (int)min(max(line.lo - first, (int64_t)0), (int64_t)c.tiles);
-        c.end = (int)min(max(line.hi - first, (int64_t)0), (int64_t)c.tiles);
-        if (c.tile < c.end) return true;
-        c.start += line.length(c.tiles);
-        if (++c.u == units) {
-            c.u = 0;
-            if (++c.b >= a.B) return false;
-            load_request(a, kept, c);
-        }
-    }
-    return false;
-}
-__device__ __forceinline__ bool next_unit(const Args& a, const Kept* kept, const Line& line, Cursor& c, int units) {
-    c.start += line.length(c.tiles);
-    if (++c.u == units) {
-        c.u = 0;
-        if (++c.b >= a.B) return false;
-        load_request(a, kept, c);
-    }
-    return seek(a, kept, line, c, units);
-}
-
-struct Record {                            // an open unit of a warp
-    int valid, b, u, tiles, open_start, open_end;
-    int64_t start;
+    __device__ __forceinline__ int tiles() const { return max(1, (n + kTile - 1) / kTile); }
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int chunks, uint32_t stage, int lane) {
+__device__ __forceinline__ void load_tile(const Args& a, const Cursor<Keys>& c, int chunks, uint32_t stage, int lane) {
     constexpr int L = D / 8;               // lanes of a row
     constexpr int rows = 32 / L;           // rows of one step
     const int h = c.u / chunks, x0 = c.tile * kTile, row = lane / L;
@@ -183,161 +106,31 @@ __device__ __forceinline__ void load_tile(const Args& a, const Cursor& c, int ch
     }
 }
 
-// Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
-// gives a part's base, O [R][D] then (m, l) [R].  Four at a time, so that their
-// loads are under way together.
-template <int D, int R, typename F>
-__device__ __forceinline__ void join(int row, int col, int count, F part, float& m, float& l, float4& o) {
-    for (int s0 = 0; s0 < count; s0 += 4) {
-        float2 ml[4];
-        float4 v[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const float* p = part(min(s0 + s, count - 1));
-            ml[s] = *reinterpret_cast<const float2*>(p + R * D + 2 * row);
-            v[s] = *reinterpret_cast<const float4*>(p + row * D + col);
-        }
-        float top = m;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s0 + s >= count) ml[s] = make_float2(-INFINITY, 0.f);
-            top = fmaxf(top, ml[s].x);
-        }
-        const float use = top == -INFINITY ? 0.f : top;
-        float f = exp2_approx(m - use);
-        l *= f;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (s0 + s >= count) break;
-            f = exp2_approx(ml[s].x - use);
-            l += f * ml[s].y;
-            o.x += f * v[s].x;
-            o.y += f * v[s].y;
-            o.z += f * v[s].z;
-            o.w += f * v[s].w;
-        }
-        m = top;
-    }
-}
-
-// A row's joined sums become its result, or wait for the prefix's: row r of the
-// group, four values.
-template <int D>
-__device__ __forceinline__ void finish(const Args& a, const DecodeBuffers& buf, int b, int hk, int r, int col, float m,
-                                       float l, float4 o) {
-    const int64_t at = (int64_t)b * a.Hq + hk * a.G + r;
-    if (buf.with_prefix) {
-        *reinterpret_cast<float4*>(buf.own + at * D + col) = o;
-        if (col == 0) buf.own_ml[at] = make_float2(m, l);
-        return;
-    }
-    const float inv = inverse(l);
-    *reinterpret_cast<uint2*>(a.out + at * D + col) =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (a.weights && col == 0) buf.lse[at] = log_sum(m, l);
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const DecodeBuffers buf, const TilePlan plan) {
     using S = Shape<D, R>;
     constexpr int NT = D / 8;              // 8-wide column tiles of the output
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t sums[kRuns + 1];
-    __shared__ int longest[kRuns / 32];
-    __shared__ Kept kept[kKept];
-    __shared__ Record records[2 * kWarps];
-    __shared__ int chain[2 * kWarps];
-    __shared__ int last_block;
+    __shared__ LineBlock<kWarps> sh;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
     const int units = a.Hk * chunks;
 
     grid_go_on();
-    // the line: places of the requests before each of kRuns runs of requests
-    const int run = (a.B + kRuns - 1) / kRuns;
-    {
-        int64_t mine = 0;
-        int most = 0;
-        for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) {
-            const Request r = read_request(a, b);
-            if (b < kKept) kept[b] = Kept{r.slot, r.len, r.plen};
-            const int n = tiles_of(a, r);
-            mine += kUnitCost + n;
-            most = max(most, n);
-        }
-        int64_t incl = mine;
-        for (int x = 1; x < 32; x <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
-            if (lane >= x) incl += o;
-        }
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 31 && tid < kRuns) {
-            sums[warp] = incl;
-            longest[warp] = most;
-        }
-        if (tid < 2 * kWarps) records[tid].valid = 0;
-        __syncthreads();
-        int64_t before = 0;
-        for (int w = 0; w < warp && tid < kRuns; ++w) before += sums[w];
-        __syncthreads();
-        if (tid < kRuns) sums[tid + 1] = before + incl;
-        if (tid == 0) sums[0] = 0;
-        __syncthreads();
-    }
-    Line line;
-    line.each = 0;
-    if ((int64_t)a.B * units <= gridDim.x) {
-        int most = 0;
-        for (int w = 0; w < kRuns / 32; ++w) most = max(most, longest[w]);
-        if (most <= kShort) line.each = most;
-    }
-    const int64_t total = line.each ? (int64_t)a.B * units * line.each : sums[kRuns] * units;
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (line.each) per = line.each;
-    else per = per < kLeast ? kLeast : per;
-    const int64_t block_lo = min(total, per * blockIdx.x), block_hi = min(total, block_lo + per);
-    line.lo = block_lo + (block_hi - block_lo) * warp / kWarps;
-    line.hi = block_lo + (block_hi - block_lo) * (warp + 1) / kWarps;
-
+    const Line<Keys> line = lay_line<Keys>(a, sh, units);
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
     float* const head_part = reinterpret_cast<float*>(smem + kWarps * S::kRing + warp * S::kPart);
 
-    Cursor c;
-    bool has = line.lo < line.hi;
-    if (has) {
-        if (line.each) {
-            const int unit = (int)(line.lo / line.each);
-            c.b = unit / units;
-            c.u = unit % units;
-            c.start = (int64_t)unit * line.each;
-            load_request(a, kept, c);
-        } else {
-            int s = 0;                     // the run that holds place lo
-            for (int step = kRuns / 2; step; step /= 2)
-                if (sums[s + step] * units <= line.lo) s += step;
-            c.start = sums[s] * units;
-            c.b = s * run;
-            load_request(a, kept, c);
-            while (line.lo - c.start >= (int64_t)line.length(c.tiles) * units && c.b + 1 < a.B) {
-                c.start += (int64_t)line.length(c.tiles) * units;
-                ++c.b;
-                load_request(a, kept, c);
-            }
-            c.u = min((int)((line.lo - c.start) / line.length(c.tiles)), units - 1);
-            c.start += (int64_t)c.u * line.length(c.tiles);
-        }
-        has = seek(a, kept, line, c, units);
-    }
-    if (has) {
-        Cursor ahead = c;
+    Cursor<Keys> c;
+    if (first_unit(a, sh, line, c, units)) {
+        Cursor<Keys> ahead = c;
         bool more = true;
         int put = 0;
         auto prefetch = [&]() {
             if (more) {
                 load_tile<D>(a, ahead, chunks, ring + put * S::kStage, lane);
-                if (++ahead.tile == ahead.end) more = next_unit(a, kept, line, ahead, units);
+                if (++ahead.tile == ahead.end) more = next_unit(a, sh.kept, line, ahead, units);
             }
             cp_async_commit();
             if (++put == S::kStages) put = 0;
@@ -504,16 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                         *reinterpret_cast<float2*>(part + r * D + t * 8 + col) = make_float2(o[t][2 * i], o[t][2 * i + 1]);
                     if (lane % 4 == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m[i], l[i]);
                 }
-                if (lane == 0) {
-                    Record& rec = records[2 * warp + (open_start ? 0 : 1)];
-                    rec.valid = 1;
-                    rec.b = c.b;
-                    rec.u = c.u;
-                    rec.tiles = c.tiles;
-                    rec.open_start = open_start;
-                    rec.open_end = open_end;
-                    rec.start = c.start + line.lead();
-                }
+                if (lane == 0) note_open(sh, line, c, open_start, open_end);
             } else {
                 const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
 #pragma unroll
@@ -537,68 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
                     if (a.weights && lane % 4 == 0) buf.lse[row_at] = log_sum(m[i], l[i]);
                 }
             }
-        } while (next_unit(a, kept, line, c, units));
+        } while (next_unit(a, sh.kept, line, c, units));
         cp_async_wait<0>();
     }
     __syncthreads();
 
-    // join the open units of this block's warps, one after the other: `chain` lists the
-    // records in their order, a unit's follow one another
-    unsigned valid = __ballot_sync(0xffffffffu, lane < 2 * kWarps && records[lane % (2 * kWarps)].valid);
-    if (warp == 0 && (valid >> lane & 1)) chain[__popc(valid & ((1u << lane) - 1))] = lane;
-    const int listed = __popc(valid);
-    __syncthreads();
-    for (int first = 0, next; first < listed; first = next) {
-        next = first + 1;
-        while (records[chain[next - 1]].open_end && next < listed) ++next;
-        const Record& rec = records[chain[first]];
-        const bool before = rec.open_start, after = records[chain[next - 1]].open_end;
-        const int hk = rec.u / chunks, g0 = (rec.u - hk * chunks) * R;
-        for (int i = tid; i < R * D / 4; i += kThreads) {
-            const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-            float m = -INFINITY, l = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            join<D, R>(r, col, next - first,
-                       [&](int j) {
-                           const int k = chain[first + j];
-                           return reinterpret_cast<const float*>(
-                               smem + (k % 2 ? k / 2 * S::kRing : kWarps * S::kRing + k / 2 * S::kPart));
-                       },
-                       m, l, o);
-            if (before || after) {
-                float* part = buf.parts + (int64_t)(2 * blockIdx.x + (before ? 0 : 1)) * (R * D + 2 * R);
-                *reinterpret_cast<float4*>(part + r * D + col) = o;
-                if (col == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m, l);
-            } else if (g0 + r < a.G) {
-                finish<D>(a, buf, rec.b, hk, g0 + r, col, m, l, o);
-            }
-        }
-        if (before || after) {
-            // the block that brings a unit's last part joins them all
-            const int c0 = (int)(rec.start / per), c1 = (int)((rec.start + rec.tiles - 1) / per);
-            __syncthreads();
-            if (tid == 0) {
-                __threadfence();
-                unsigned* ticket = buf.tickets + c0 / 4;
-                const int at = 8 * (c0 % 4), n = atomicAdd(ticket, 1u << at) >> at & 255u;
-                last_block = n == c1 - c0;
-                if (last_block) atomicAnd(ticket, ~(255u << at));
-                __threadfence();
-            }
-            __syncthreads();
-            if (last_block) {
-                for (int i = tid; i < R * D / 4; i += kThreads) {
-                    const int r = i / (D / 4), col = (i % (D / 4)) * 4;
-                    float m = -INFINITY, l = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    join<D, R>(r, col, c1 - c0 + 1,
-                               [&](int s) { return buf.parts + (int64_t)(2 * (c0 + s) + (s ? 0 : 1)) * (R * D + 2 * R); }, m, l, o);
-                    if (g0 + r < a.G) finish<D>(a, buf, rec.b, hk, g0 + r, col, m, l, o);
-                }
-            }
-            __syncthreads();
-        }
-    }
+    join_open<D, R>(a, buf, sh, line, chunks, [&](int k) {
+        return reinterpret_cast<const float*>(smem + (k % 2 ? k / 2 * S::kRing : kWarps * S::kRing + k / 2 * S::kPart));
+    });
     if (buf.with_prefix) {
         // the plan is there: the queries in the order of the prefixes, for the tiles
         grid_wait();
@@ -622,7 +352,7 @@ __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBu
     const int b = blockIdx.z, hk = blockIdx.y;
     grid_wait();
     const Request r = read_request(a, b);
-    const Keys k = visible_keys(a, r);
+    const Keys k = Keys::of(a, r);
     const int64_t row = (int64_t)b * a.Hq + (int64_t)hk * a.G;
     float* w = a.weights + ((int64_t)r.slot * a.Hk + hk) * a.capacity;
     // four keys a thread (rows of scores have room for whole tiles)
