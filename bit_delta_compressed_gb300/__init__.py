@@ -50,6 +50,12 @@ class KVCacheDesc(ctypes.Structure):
                 ("stride_slot", _I64), ("stride_token", _I64), ("stride_head", _I64)]
 
 
+class KVCache4Desc(ctypes.Structure):
+    """``bd_kv_cache4``: one layer's 4-bit cache as the C ABI takes it."""
+    _fields_ = [("data", _P), ("slots", _I64), ("capacity", _I64), ("kv_heads", _I32), ("head_dim", _I32),
+                ("stride_slot", _I64), ("stride_head", _I64)]
+
+
 SIGNATURES = {
     "bitdelta_compress_workspace": (_SZ, [_I64, _I64]),
     "bitdelta_compress": (_ST, [_P, _P, _ST, _I64, _I64, _P, _P, _P, _SZ, _P]),
@@ -73,6 +79,12 @@ SIGNATURES = {
                                     _F32, _P, _P, _SZ, _P]),
     "bitdelta_evict_workspace": (_SZ, [_I64, _I32, _I64]),
     "bitdelta_cache_evict": (_ST, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _SZ, _P]),
+    "bitdelta_cache4_bytes": (_SZ, [_I64, _I64, _I32, _I32]),
+    "bitdelta_cache4_write": (_ST, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bitdelta_cache4_read": (_ST, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bitdelta_attn4_workspace": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I64]),
+    "bitdelta_attn4_decode": (_ST, [_P, _I64, _I64, _I32, _P, _P, _P, _I32, _I32, _F32, _P, _P, _SZ, _P]),
+    "bitdelta_attn4_prefill": (_ST, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _I64, _I32, _I32, _F32, _P, _P, _SZ, _P]),
     "bitdelta_device_status": (_ST, [_P, _P]),
     "bitdelta_check_bounded_wait": (_ST, [_P, ctypes.c_uint32, ctypes.c_int, _P]),
     "bitdelta_launch_count": (ctypes.c_uint64, []),
@@ -467,6 +479,115 @@ def cache_evict(k_cache, v_cache, weights, lens, src, dst, budget: int, workspac
                                          _int32("src", src, dev, n), _int32("dst", dst, dev, n), n, budget, sinks, recent,
                                          _int32("kept", kept, dev, n, H, budget), *_workspace(workspace, dev),
                                          _stream(stream)), "bitdelta_cache_evict")
+
+
+# -- a key/value cache held in 4 bits ------------------------------------------------
+
+_DESC4 = struct.Struct("@Pqqiiqq")         # KVCache4Desc's layout
+
+
+def cache4(slots: int, capacity: int, kv_heads: int, head_dim: int, device=None):
+    """An empty 4-bit cache, uint8 [slots, kv_heads, capacity / 16, 17 * head_dim]
+    (see ``bd_kv_cache4``): blocks of 16 tokens of one head; ``capacity`` a multiple of 16."""
+    torch = _torch()
+    if int(get_lib().bitdelta_cache4_bytes(slots, capacity, kv_heads, head_dim)) == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "bitdelta_cache4_bytes")
+    return torch.zeros((slots, kv_heads, capacity // 16, 17 * head_dim), dtype=torch.uint8, device=device)
+
+
+def _desc4_of(cache):
+    shape, strides = cache.shape, cache.stride()
+    if len(shape) != 4 or shape[3] not in (17 * 64, 17 * 128):
+        raise ValueError("the cache must be 4-D [slots, kv_heads, capacity / 16, 17 * head_dim], head_dim 64 or 128")
+    if cache.dtype is not _torch().uint8:
+        raise TypeError("the cache must be uint8")
+    S, H, N, W = shape
+    ss, sh, sn, sb = strides
+    dev = cache.get_device()
+    if dev < 0 or sb != 1 or (N > 1 and sn != W):
+        raise ValueError("the cache must be a CUDA tensor whose blocks of a head follow one another")
+    # the stride of a dimension of one entry is never used, and torch leaves it open
+    return (H, W // 17), dev, _DESC4.pack(cache.data_ptr(), S, 16 * N, H, W // 17, ss if S > 1 else W, sh if H > 1 else W)
+
+
+def _rows4(name, t, H, D, dev):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or t.dtype is not _torch().bfloat16 or t.get_device() != dev:
+        raise ValueError("%s must be a bf16 tensor [rows, kv_heads, head_dim] on the cache's device" % name)
+    if strides[2] != 1 or (H > 1 and strides[1] != D):
+        raise ValueError("the heads of a row of %s must be contiguous" % name)
+    return shape[0], t.data_ptr(), strides[0] if shape[0] > 1 else H * D
+
+
+def _move4(entry, k, v, cache, lens, workspace, slots, cu_q, stream):
+    (H, D), dev, desc = _desc4_of(cache)
+    T, k_ptr, k_stride = _rows4("k", k, H, D, dev)
+    rows, v_ptr, v_stride = _rows4("v", v, H, D, dev)
+    B = lens.numel()
+    if rows != T or (cu_q is None and T != B):
+        raise ValueError("k and v must have one number of rows, without cu_q one for each request")
+    code = getattr(get_lib(), entry)(k_ptr, k_stride, v_ptr, v_stride, T, B, desc, _int32("slots", slots, dev, B),
+                                     _int32("cu_q", cu_q, dev, B + 1), _int32("lens", lens, dev, B),
+                                     *_workspace(workspace, dev), _stream(stream))
+    if code != BD_OK:
+        check(code, entry)
+
+
+def cache4_write(k, v, cache, lens, workspace, slots=None, cu_q=None, stream=None) -> None:
+    """Quantise new tokens into a 4-bit cache: rows ``cu_q[b]`` to ``cu_q[b+1]``
+    of k and v [T, kv_heads, head_dim] bf16 become the last of request b's ``lens[b]`` keys
+    (without ``cu_q`` one row a request; see ``bitdelta_cache4_write``)."""
+    _move4("bitdelta_cache4_write", k, v, cache, lens, workspace, slots, cu_q, stream)
+
+
+def cache4_read(k, v, cache, lens, workspace, slots=None, cu_q=None, stream=None):
+    """Read keys and values back into rows of k and v: what ``cache4_write`` of the
+    same arguments would have written, as the cache holds it (see ``bitdelta_cache4_read``).  Returns k, v."""
+    _move4("bitdelta_cache4_read", k, v, cache, lens, workspace, slots, cu_q, stream)
+    return k, v
+
+
+def _longest(n):
+    """As the C ABI's int64 has it: a number beyond what it takes stays one."""
+    return max(-1, min(n, 1 << 40))
+
+
+def attn4_workspace(tokens: int, batch: int, q_heads: int, kv_heads: int, head_dim: int, longest: int = 0, device=None):
+    """Zeroed workspace for attention calls on a 4-bit cache of at most ``tokens`` query
+    rows and ``batch`` requests; ``longest``: the most keys of a request that
+    ``attn4_prefill`` serves (0: decode only)."""
+    torch = _torch()
+    n = int(get_lib().bitdelta_attn4_workspace(tokens, batch, q_heads, kv_heads, head_dim, _longest(longest)))
+    if n == 0:
+        raise BitDeltaError(BD_ERR_SHAPE, "bitdelta_attn4_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def attn4_decode(q, cache, lens, workspace, slots=None, window: int = 0, sinks: int = 0, scale=None, out=None, stream=None):
+    """``attn_decode`` on a 4-bit cache (see ``bitdelta_attn4_decode``)."""
+    (_, D), dev, desc = _desc4_of(cache)
+    B, H, stride, out = _attn_args(q, D, out, dev)
+    code = get_lib().bitdelta_attn4_decode(q.data_ptr(), stride, B, H, desc, _int32("slots", slots, dev, B),
+                                           _int32("lens", lens, dev, B), *_mask_args(window, sinks),
+                                           D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                           *_workspace(workspace, dev), _stream(stream))
+    if code != BD_OK:
+        check(code, "bitdelta_attn4_decode")
+    return out
+
+
+def attn4_prefill(q, cache, cu_q, lens, workspace, longest: int, slots=None, window: int = 0, sinks: int = 0, scale=None,
+                  out=None, stream=None):
+    """``attn_prefill`` on a 4-bit cache, for requests of at most ``longest`` keys, what the
+    workspace was made for or less (see ``bitdelta_attn4_prefill``)."""
+    (_, D), dev, desc = _desc4_of(cache)
+    T, H, stride, out = _attn_args(q, D, out, dev)
+    B = lens.numel()
+    check(get_lib().bitdelta_attn4_prefill(q.data_ptr(), stride, T, B, H, desc, _int32("slots", slots, dev, B),
+                                           _int32("cu_q", cu_q, dev, B + 1), _int32("lens", lens, dev, B), _longest(longest),
+                                           *_mask_args(window, sinks), D ** -0.5 if scale is None else scale, out.data_ptr(),
+                                           *_workspace(workspace, dev), _stream(stream)), "bitdelta_attn4_prefill")
+    return out
 
 
 def device_status(workspace, stream=None) -> int:

@@ -22,21 +22,11 @@ bool bad_cache(const bd_kv_cache* c, bd_status* st) {
     return false;
 }
 
-namespace {
-
 bool sizes_ok(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     return tokens >= 0 && tokens <= (int64_t)1 << 30 && batch >= 0 && batch <= 65535 && kv_heads >= 1 &&
            q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads / kv_heads <= kMaxGroup && q_heads <= 65535 &&
            (head_dim == 64 || head_dim == 128);
 }
-
-// The workspace of one call: the header, which holds the tickets, lies where every
-// call expects it, the rest is scratch.
-struct Workspace {
-    DecodeBuffers decode;
-    TilePlan plan;
-    size_t total;
-};
 
 Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                  int64_t weigh_len) {
@@ -75,6 +65,8 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
     w.total = at;
     return w;
 }
+
+namespace {
 
 bd_status attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int32_t q_heads, const bd_kv_cache* c,
                     const int32_t* slots, const int32_t* cu_q, const int32_t* lens, const int32_t* prefix_ids,

@@ -1,0 +1,365 @@
+// bd_attn4_decode.cu -- attention of one query row a request on its own keys in the
+// 4-bit cache.
+//
+// o = sum_j p_j v_j with p the softmax of q.k_j, k and v what the cache stands for:
+// 4 head_dim flops a head and key for 17/16 head_dim bytes, so the cache's bytes bound
+// it, and next to them the instructions that make f16 of 4 bits.  The line of units,
+// the blocks' and warps' parts of it and their joining are those of the bf16 cache's
+// decode kernel; tiles are two cache blocks, 32 keys, and begin where a block
+// begins.  A warp streams its tiles, bytes as they lie, through a ring of its own (cp.async) and
+// multiplies the transposed way, S^T = K Q^T and O^T = V^T P^T, with mma.m16n8k16 in f16:
+// keys and dims are the 16 rows and a group's heads the 8 columns, so a group of 8 wastes nothing.  Which
+// dims meet in a product's step is free, so the cache's words are laid out for the
+// lanes: 16 bytes a lane are its part of a key, and a word is two steps' operand after
+// nine operations (bd_cache4.cuh).  Numbers times scales are exact in f16; only the
+// query (16-bit already, brought to f16's range by a power of two of its own) and the
+// probabilities (11 significant bits) are rounded, both below the result's bf16.
+// P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
+#include <math.h>
+
+#include "bd_attn_line.cuh"
+#include "bd_attn4.cuh"
+#include "bd_cache4.cuh"
+#include "bd_tc_common.cuh"
+
+namespace bd {
+namespace attn {
+namespace {
+
+using cache4::Cache;
+using cache4::kBlock;
+using cache4::Layout;
+using cache4::Scales;
+
+constexpr int kBlocks = 2;                // cache blocks of a tile
+constexpr int kTile = kBlocks * kBlock;   // its keys
+// The running maximum is kept this many powers of two below the scores' (probabilities
+// then reach down to 2^-30 of the largest before they lose bits of f16) and lags
+// behind by up to 2^kLag / 2^kLift: 2^14 is within f16.
+constexpr float kLift = 6.f, kLag = 14.f;
+
+// Where the visible keys of a request lie: tiles from the first key on (`head` of them)
+// and, behind a gap, those from tile `from` on.
+struct Keys4 {
+    static constexpr int kUnitCost = 2, kLeast = 16, kShort = 64;
+    int len, lo, sinks, head, from, n;
+    static __device__ __forceinline__ Keys4 of(const Args& a, const Request& r) {
+        Keys4 k;
+        k.len = r.len;
+        k.lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);
+        k.sinks = min(max(a.sinks - r.plen, 0), r.len);
+        k.head = (k.sinks + kTile - 1) / kTile;
+        k.from = k.lo / kTile;
+        if (k.from <= k.head) k.head = k.from = 0;
+        k.n = k.head + (r.len + kTile - 1) / kTile - k.from;
+        return k;
+    }
+    __device__ __forceinline__ int tiles() const { return max(1, n); }
+    // first key of a tile
+    __device__ __forceinline__ int base(int tile) const { return (tile < head ? tile : tile - head + from) * kTile; }
+    __device__ __forceinline__ bool sees(int key) const { return key < len && (key >= lo || key < sinks); }
+    __device__ __forceinline__ bool whole(int base) const { return base + kTile <= len && (base >= lo || base + kTile <= sinks); }
+};
+
+template <int D, int R>
+struct Shape4 {
+    static constexpr int kWarps = R == 8 ? 16 : 8;
+    static constexpr int kStage = kBlocks * Layout<D>::kBytes;
+    static constexpr int kStages = 2 * (128 / D);
+    static constexpr int kRing = kStage * kStages;                          // of one warp
+    static constexpr int kPart = R * D * 4 + R * 8;                         // an open unit: O, then (m, l)
+    static constexpr int kSmem = kWarps * (kRing + kPart);
+    static_assert(kRing >= kPart, "a warp's last open unit reuses its ring");
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values across the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// W words at a time from shared memory.
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&w)[W], uint32_t at) {
+    if constexpr (W == 4)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t load_byte(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t load_two(uint32_t at) {
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at) : "memory");
+    return r;
+}
+
+// A tile's bytes as they lie; of the last one only blocks that hold keys.
+template <int D>
+__device__ __forceinline__ void load_tile4(const Cache& cache, const Cursor<Keys4>& c, int chunks, uint32_t stage, int lane) {
+    constexpr int kChunks = kBlocks * Layout<D>::kBytes / 16;
+    const int base = c.k.base(c.tile);
+    const int blocks = (c.k.len - base + kBlock - 1) / kBlock;
+    const int n = blocks >= kBlocks ? kChunks : max(blocks, 0) * (Layout<D>::kBytes / 16);
+    const uint8_t* from = cache.data + c.r.slot * cache.ss + c.u / chunks * cache.sh + (int64_t)(base / kBlock) * Layout<D>::kBytes + lane * 16;
+    const uint32_t to = stage + lane * 16;
+#pragma unroll
+    for (int i = 0; i < (kChunks + 31) / 32; ++i)
+        if (lane + i * 32 < n)
+            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512) : "memory");
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
+    decode4_kernel(const Args a, const Cache cache, const DecodeBuffers buf) {
+    using S = Shape4<D, R>;
+    using Lay = Layout<D>;
+    constexpr int NT = R / 8;              // columns of eight heads
+    constexpr int W = D / 32;              // words of a lane's part of a key, or of two values
+    constexpr int MT = D / 16;             // sixteens of dims
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ LineBlock<S::kWarps> sh;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
+    const int units = a.Hk * chunks;
+
+    const Line<Keys4> line = lay_line<Keys4>(a, sh, units);
+    const uint32_t ring = smem_addr(smem) + warp * S::kRing;
+    float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
+    float* const head_part = reinterpret_cast<float*>(smem + S::kWarps * S::kRing + warp * S::kPart);
+
+    Cursor<Keys4> c;
+    if (first_unit(a, sh, line, c, units)) {
+        Cursor<Keys4> ahead = c;
+        bool more = true;
+        int put = 0;
+        auto prefetch = [&]() {
+            if (more) {
+                load_tile4<D>(cache, ahead, chunks, ring + put * S::kStage, lane);
+                if (++ahead.tile == ahead.end) more = next_unit(a, sh.kept, line, ahead, units);
+            }
+            cp_async_commit();
+            if (++put == S::kStages) put = 0;
+        };
+#pragma unroll 1
+        for (int i = 0; i < S::kStages - 1; ++i) prefetch();
+
+        int got = 0;
+        const int g = lane / 4, t = lane % 4;
+        uint32_t qf[NT][2 * W][2];         // of head 8 n + g: the lane's dims of each step
+        float factor[NT][2];               // scores in powers of two: of heads 8 n + 2 t, + 1
+        float o[NT][MT][4], l[NT][4], m[NT][2];
+        do {
+            const int seg_tile = c.tile;
+            const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
+            {
+                const __nv_bfloat16* qp = a.q + (int64_t)c.b * a.q_stride + (int64_t)(hk * a.G + g0) * D + t * (D / 4);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint32_t w[4 * W];
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        const uint4 x = 8 * n + g < a.G - g0 ? *reinterpret_cast<const uint4*>(qp + (8 * n + g) * D + i * 8) : make_uint4(0u, 0u, 0u, 0u);
+                        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+                    }
+                    // the largest magnitude's power of two goes to 2^13; a row that is not finite stays as it is
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < 4 * W; ++i) top = max(top, max(w[i] & 0x7FFFu, w[i] >> 16 & 0x7FFFu));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t e = top >= 0x7F80u ? 140u : max(top >> 7, 14u);
+                    const float by = __uint_as_float((267u - e) << 23), back = __uint_as_float((e - 13u) << 23);
+#pragma unroll
+                    for (int i = 0; i < 4 * W; ++i) qf[n][i / 2][i % 2] = pack_f16(bf16_lo(w[i]) * by, bf16_hi(w[i]) * by);
+                    factor[n][0] = a.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
+                    factor[n][1] = a.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+                    l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.f;
+                    m[n][0] = m[n][1] = -INFINITY;
+                }
+            }
+#pragma unroll 1
+            for (; c.tile < c.end; ++c.tile) {
+                prefetch();
+                cp_async_wait<S::kStages - 1>();
+                __syncwarp();
+                const uint32_t stage = ring + got * S::kStage;
+                if (++got == S::kStages) got = 0;
+                const int base = c.k.base(c.tile);
+                const bool whole = c.k.whole(base);
+                float s[kBlocks][NT][4];
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x) {
+                    const uint32_t at = stage + x * Lay::kBytes;
+                    uint32_t ka[W], kb[W];                 // keys g and g + 8
+                    load_words(ka, at + g * (D / 2) + t * (4 * W));
+                    load_words(kb, at + (g + 8) * (D / 2) + t * (4 * W));
+                    const uint32_t code = at + Lay::kScaleK + g * (D / 32) + t * (D / 32) / 4;
+                    const Scales sa = cache4::scale_of(load_byte(code)), sb = cache4::scale_of(load_byte(code + 8 * (D / 32)));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) s[x][n][0] = s[x][n][1] = s[x][n][2] = s[x][n][3] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2 * W; ++i) {
+                        const uint32_t wa = i % 2 ? cache4::swap_bytes(ka[i / 2]) : ka[i / 2], wb = i % 2 ? cache4::swap_bytes(kb[i / 2]) : kb[i / 2];
+                        const uint32_t a0 = cache4::field0(wa, sa), a1 = cache4::field0(wb, sb), a2 = cache4::field1(wa, sa), a3 = cache4::field1(wb, sb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(s[x][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
+                    }
+                }
+                bool grows = false;
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = whole || c.k.sees(base + x * kBlock + g + i / 2 * 8);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            s[x][n][i] = in ? s[x][n][i] * factor[n][i % 2] : -INFINITY;
+                            grows = grows || s[x][n][i] > m[n][i % 2] + kLag;
+                        }
+                    }
+                if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float f[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float top = -INFINITY;
+#pragma unroll
+                            for (int x = 0; x < kBlocks; ++x) top = fmaxf(top, fmaxf(s[x][n][i], s[x][n][2 + i]));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) - kLift;
+                            f[i] = top > m[n][i] ? exp2_approx(m[n][i] - top) : 1.f;
+                            m[n][i] = fmaxf(m[n][i], top);
+                        }
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            o[n][i][0] *= f[0];
+                            o[n][i][1] *= f[1];
+                            o[n][i][2] *= f[0];
+                            o[n][i][3] *= f[1];
+                        }
+                        l[n][0] *= f[0];
+                        l[n][1] *= f[1];
+                        l[n][2] *= f[0];
+                        l[n][3] *= f[1];
+                    }
+                }
+                uint32_t p[kBlocks][NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float use0 = m[n][0] == -INFINITY ? 0.f : m[n][0], use1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+                    for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            p[x][n][i] = transpose8(pack_f16(exp2_approx(s[x][n][2 * i] - use0), exp2_approx(s[x][n][2 * i + 1] - use1)));
+                }
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x) {
+                    const uint32_t at = stage + x * Lay::kBytes;
+                    uint32_t va[W], vb[W];                 // of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                    load_words(va, at + Lay::kV + t * D + g * (4 * W));
+                    load_words(vb, at + Lay::kV + (t + 4) * D + g * (4 * W));
+                    const uint32_t code = at + Lay::kScaleV + g * (D / 32) / 8 * kBlock + 2 * t;
+                    uint32_t pa = cache4::scale_pair(load_two(code)), pb = cache4::scale_pair(load_two(code + 8));
+                    if (!whole) {
+                        // values that are not seen become zeros, whatever they are
+                        const int key = base + x * kBlock + 2 * t;
+                        pa &= (c.k.sees(key) ? 0xFFFFu : 0u) | (c.k.sees(key + 1) ? 0xFFFF0000u : 0u);
+                        pb &= (c.k.sees(key + 8) ? 0xFFFFu : 0u) | (c.k.sees(key + 9) ? 0xFFFF0000u : 0u);
+                    }
+                    const Scales sa = cache4::scales(pa), sb = cache4::scales(pb);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const uint32_t wa = i % 2 ? cache4::swap_bytes(va[i / 2]) : va[i / 2], wb = i % 2 ? cache4::swap_bytes(vb[i / 2]) : vb[i / 2];
+                        const uint32_t a0 = cache4::field0(wa, sa), a1 = cache4::field1(wa, sa), a2 = cache4::field0(wb, sb), a3 = cache4::field1(wb, sb);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(o[n][i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[x][n][0], p[x][n][1]);
+                }
+                __syncwarp();
+            }
+            // the unit, or this warp's part of it, is done; the lane has dims D / 8 g ... of heads 8 n + 2 t, + 1
+            const bool open_start = seg_tile > 0, open_end = c.end < c.tiles;
+            if (open_start || open_end) {
+                // one that began before is kept beside the ring, the last one (no
+                // tile follows it) in the ring
+                if (!open_start) cp_async_wait<0>();
+                __syncwarp();
+                float* part = open_start ? head_part : tail_part;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = 8 * n + 2 * t + i;
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+                            *reinterpret_cast<float4*>(part + r * D + g * (D / 8) + 4 * w) =
+                                make_float4(o[n][2 * w][i], o[n][2 * w][2 + i], o[n][2 * w + 1][i], o[n][2 * w + 1][2 + i]);
+                        if (g == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m[n][i], l[n][i]);
+                    }
+                if (lane == 0) note_open(sh, line, c, open_start, open_end);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = g0 + 8 * n + 2 * t + i;
+                        if (r >= a.G) continue;
+#pragma unroll
+                        for (int w = 0; w < W; ++w)
+                            finish<D>(a, buf, c.b, hk, r, g * (D / 8) + 4 * w, m[n][i], l[n][i],
+                                      make_float4(o[n][2 * w][i], o[n][2 * w][2 + i], o[n][2 * w + 1][i], o[n][2 * w + 1][2 + i]));
+                    }
+            }
+        } while (next_unit(a, sh.kept, line, c, units));
+        cp_async_wait<0>();
+    }
+    __syncthreads();
+
+    join_open<D, R>(a, buf, sh, line, chunks, [&](int k) {
+        return reinterpret_cast<const float*>(smem + (k % 2 ? k / 2 * S::kRing : S::kWarps * S::kRing + k / 2 * S::kPart));
+    });
+}
+
+template <int D, int R>
+bd_status launch_shape4(const Args& a, const Cache& cache, const DecodeBuffers& buf, cudaStream_t stream) {
+    using S = Shape4<D, R>;
+    const void* kernel = reinterpret_cast<const void*>(decode4_kernel<D, R>);
+    if (!set_smem_attr(kernel, S::kSmem, D == 128 ? (R == 8 ? 11 : 12) : (R == 8 ? 13 : 14))) return BD_ERR_CUDA;
+    decode4_kernel<D, R><<<decode_blocks(), S::kWarps * 32, S::kSmem, stream>>>(a, cache, buf);
+    return launch_status();
+}
+
+}  // namespace
+
+bd_status launch_decode4(const Args& a, const cache4::Cache& cache, int head_dim, const DecodeBuffers& buf, cudaStream_t stream) {
+    if (a.G <= 8) return head_dim == 128 ? launch_shape4<128, 8>(a, cache, buf, stream) : launch_shape4<64, 8>(a, cache, buf, stream);
+    return head_dim == 128 ? launch_shape4<128, 16>(a, cache, buf, stream) : launch_shape4<64, 16>(a, cache, buf, stream);
+}
+
+}  // namespace attn
+}  // namespace bd

@@ -170,6 +170,16 @@ __device__ __forceinline__ Parts parts_of(const RowTile& t, const PlanHead& head
     return p;
 }
 
+// The workspace of one call: the header, which holds the tickets, lies where every
+// call expects it, the rest is scratch.
+struct Workspace {
+    DecodeBuffers decode;
+    TilePlan plan;
+    size_t total;
+};
+bool sizes_ok(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t weigh_len);
+
 int tile_blocks();
 int64_t split_below();       // units from which on a prefill is not split
 int64_t most_tiles(int64_t tokens, int64_t batch, int G);

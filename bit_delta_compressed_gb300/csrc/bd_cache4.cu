@@ -1,0 +1,416 @@
+// bd_cache4.cu -- rows of keys and values into the 4-bit cache and out of it.
+//
+// Both directions move 4 bytes of bf16 for 17/16 of a byte of cache and do a few
+// operations a value, so the bytes bound them.  A warp takes a block (16 tokens of one
+// head, K and V) at a time: a row's D values lie on D / 8 lanes, 16 bytes each, so a
+// group's largest value is two shuffles away and a lane's eight numbers are one word of K.  A
+// word of V holds four dims of two tokens; the lanes of the two swap halves, so that
+// whole words are written wherever both tokens are.
+#include <math.h>
+
+#include "bd_attn_math.cuh"
+#include "bd_cache4.cuh"
+#include "bd_cache4_host.cuh"
+
+namespace bd {
+namespace cache4 {
+namespace {
+
+using attn::Args;
+using attn::Request;
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAtOnce = 4;                      // steps of a block whose loads are under way together
+
+// The rows' side: bf16, heads of a row one after the other.
+struct Rows {
+    __nv_bfloat16 *k, *v;
+    int64_t k_stride, v_stride;
+};
+
+// The attention's scratch for prompts: keys in their places, [B, kv_heads, length, D] bf16, and
+// the requests' lengths as the attention is to see them (-1: not a request).
+struct Scratch {
+    __nv_bfloat16 *k, *v;
+    int64_t length;
+    int32_t* lens;
+};
+
+// Which blocks of a request a call touches: `head` from the first on, and those from
+// block `from` to its end; of them the tokens [first, len).
+struct Span {
+    int first, len, row0, head, from, n;
+};
+
+__device__ __forceinline__ Span rows_span(const Args& a, const Request& r) {
+    Span s;
+    s.first = r.len - r.rows;
+    s.len = r.len;
+    s.row0 = r.row0;
+    s.head = 0;
+    s.from = s.first / kBlock;
+    s.n = (r.len + kBlock - 1) / kBlock - s.from;
+    return s;
+}
+
+// What the queries of a prompt see: all but what lies before the first one's window and
+// behind the first tokens.
+__device__ __forceinline__ Span seen_span(const Args& a, const Request& r) {
+    Span s;
+    const int lo = attn::window_lo(a, r.len - r.rows), sinks = min(a.sinks, r.len);
+    s.first = 0;
+    s.len = r.len;
+    s.row0 = 0;
+    s.head = (sinks + kBlock - 1) / kBlock;
+    s.from = lo / kBlock;
+    if (s.from <= s.head) s.head = s.from = 0;
+    s.n = s.head + (r.len + kBlock - 1) / kBlock - s.from;
+    return s;
+}
+
+// Blocks of the requests before each thread's run of requests.
+struct Items {
+    int64_t before[kThreads + 1];
+    int64_t warp[kWarps];
+    int served;
+};
+
+// Request b as this call sees it; false if nothing of it is touched.
+template <bool SCRATCH>
+__device__ __forceinline__ bool span_of(const Args& a, const Scratch& scratch, int b, int served, Span& s) {
+    if (b >= served) return false;
+    const Request r = attn::read_request(a, b);
+    if (r.rows == 0) return false;
+    if (r.len < r.rows || (SCRATCH && r.len > scratch.length)) {   // (one that is out of range has no length)
+        report(a.status, BD_ERR_SLOT);
+        return false;
+    }
+    s = SCRATCH ? seen_span(a, r) : rows_span(a, r);
+    return true;
+}
+
+template <bool SCRATCH>
+__device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scratch, Items& items) {
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int run = (a.B + kThreads - 1) / kThreads;
+    if (tid == 0) items.served = a.B;
+    __syncthreads();
+    if (a.cu_q) {
+        // requests from the first whose offsets do not ascend on are not served
+        for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
+            const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+            if (lo < 0 || hi < lo || hi > a.T) {
+                atomicMin(&items.served, b);
+                report(a.status, BD_ERR_SLOT);
+                break;
+            }
+        }
+        __syncthreads();
+    }
+    const int served = items.served;
+    int64_t mine = 0;
+    for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
+        Span s;
+        const bool in = span_of<SCRATCH>(a, scratch, b, served, s);
+        if (in) mine += s.n;
+        // (a request of no rows has nothing to say; one that is not served says so)
+        if (SCRATCH && blockIdx.x == 0) {
+            const bool ok = in || (b < served && a.cu_q[b] == a.cu_q[b + 1]);
+            scratch.lens[b] = ok ? min(max(a.lens[b], 0), (int)scratch.length) : -1;
+        }
+    }
+    int64_t incl = mine;
+    for (int x = 1; x < 32; x <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, x);
+        if (lane >= x) incl += o;
+    }
+    if (lane == 31) items.warp[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    for (int w = 0; w < warp; ++w) before += items.warp[w];
+    items.before[tid + 1] = before + incl;
+    if (tid == 0) items.before[0] = 0;
+    __syncthreads();
+    return items.before[kThreads];
+}
+
+// The request that holds block i of all, which becomes the block's number within it.
+template <bool SCRATCH>
+__device__ __forceinline__ int find(const Args& a, const Scratch& scratch, const Items& items, int64_t& i, Span& s) {
+    int t = 0;
+    for (int step = kThreads / 2; step; step /= 2)
+        if (items.before[t + step] <= i) t += step;
+    i -= items.before[t];
+    int b = t * ((a.B + kThreads - 1) / kThreads);
+    for (;; ++b) {
+        if (!span_of<SCRATCH>(a, scratch, b, items.served, s)) continue;
+        if (i < s.n) return b;
+        i -= s.n;
+    }
+}
+
+// ---- values into numbers ---------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t largest(uint32_t m, uint32_t w) { return max(m, max(w & 0x7FFFu, w >> 16 & 0x7FFFu)); }
+
+// A group's scale as its byte, from the bits of the largest |x| (bf16).
+__device__ __forceinline__ uint32_t scale_code(uint32_t top) {
+    if (top >= 0x7F80u) return kNanScale;
+    const float want = __fdiv_rn(__uint_as_float(top << 16), 7.f);
+    if (want < 6.103515625e-5f) return (uint32_t)__float2int_rn(want * 131072.f);   // below 2^-14: units of 2^-17
+    const uint32_t bits = __float_as_uint(want);
+    const uint32_t code = ((bits + 0x7FFFFu + (bits >> 20 & 1u)) >> 20) - (112u << 3);
+    return min(code, kTopScale);
+}
+
+// Eight values as n + 8.  x / s is taken as a product with 1 / s, off by 2^-23 of itself; then
+// to the nearest multiple of 2^-10 (that many of 1.5 2^13's last places), which
+// a tie x = (n + 1/2) s is itself, and to whole numbers.  Other x lie 2^-9 or more from a tie (8 bits of
+// x against 4 of s), so this is the exact quotient's rounding, ties to even.
+__device__ __forceinline__ void numbers(const uint4& x, uint32_t code, uint32_t (&n)[8]) {
+    const float s = __half2float(__ushort_as_half((unsigned short)(code << 7)));
+    const float inv = code ? __frcp_rn(s) : 0.f;
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+        const float y = fminf(fmaxf(v * inv, -7.f), 7.f) + 12288.f;
+        n[i] = __float_as_uint(y + 12570632.f) & 15u;      // 1.5 2^23 - 12288 + 8
+    }
+}
+
+// Four of them as a unit; a group that is not finite holds zeros beside its scale.
+__device__ __forceinline__ uint32_t unit(uint32_t code, uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3) {
+    return code == kNanScale ? 0x2222u : n0 << 6 | n1 << 2 | n2 >> 2 | (n2 & 3u) << 14 | n3 << 10;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) write_kernel(const Args a, const Cache c, const Rows rows) {
+    using Lay = Layout<D>;
+    constexpr int L = D / 8;                    // lanes of a row
+    constexpr int R = 32 / L;                   // rows of a step
+    __shared__ Items items;
+    const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
+    const Scratch none{};
+    const int64_t total = lay_items<false>(a, none, items) * a.Hk;
+    for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
+        int64_t i = at / a.Hk;
+        const int h = (int)(at - i * a.Hk);
+        Span s;
+        const int b = find<false>(a, none, items, i, s);
+        const int block = s.from + (int)i, t0 = block * kBlock;
+        const int slot = a.slots ? a.slots[b] : b;
+        uint8_t* const to = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
+        const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);      // tokens of the block
+        const int64_t row0 = (int64_t)s.row0 - s.first + t0;
+        for (int step = lo / R; step * R < hi; step += kAtOnce) {
+            uint4 k[kAtOnce], v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int j = (step + u) * R + lane / L;
+                k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (j < lo || j >= hi) continue;
+                k[u] = *reinterpret_cast<const uint4*>(rows.k + (row0 + j) * rows.k_stride + h * D + col * 8);
+                v[u] = *reinterpret_cast<const uint4*>(rows.v + (row0 + j) * rows.v_stride + h * D + col * 8);
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if ((step + u) * R >= hi) break;
+                const int j = (step + u) * R + lane / L;
+                uint32_t top = 0, codes[2], n[8];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint4& x = w ? v[u] : k[u];
+                    top = largest(largest(largest(largest(0u, x.x), x.y), x.z), x.w);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    codes[w] = scale_code(top);
+                }
+                const bool in = j >= lo && j < hi, other = (j ^ 1) >= lo && (j ^ 1) < hi;
+                numbers(k[u], codes[0], n);
+                if (in) {
+                    *reinterpret_cast<uint32_t*>(to + j * (D / 2) + col * 4) = unit(codes[0], n[0], n[2], n[4], n[6]) | unit(codes[0], n[1], n[3], n[5], n[7]) << 16;
+                    if (col % 4 == 0) {
+                        to[Lay::kScaleK + j * (D / 32) + col / 4] = (uint8_t)codes[0];
+                        to[Lay::kScaleV + col / 4 * kBlock + j] = (uint8_t)codes[1];
+                    }
+                }
+                numbers(v[u], codes[1], n);
+                const uint32_t first = unit(codes[1], n[0], n[1], n[2], n[3]), second = unit(codes[1], n[4], n[5], n[6], n[7]);
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, j % 2 ? first : second, L);
+                uint8_t* const pair = to + Lay::kV + j / 2 * D + col * 8;
+                if (in && other) {
+                    *reinterpret_cast<uint32_t*>(pair + j % 2 * 4) = j % 2 ? got | second << 16 : first | got << 16;
+                } else if (in) {
+                    *reinterpret_cast<uint16_t*>(pair + j % 2 * 2) = (uint16_t)first;
+                    *reinterpret_cast<uint16_t*>(pair + j % 2 * 2 + 4) = (uint16_t)second;
+                }
+            }
+        }
+    }
+}
+
+// ---- and out again ---------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t to_bf16(uint32_t h2) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+    return attn::pack_bf16(f.x, f.y);           // exact
+}
+
+template <int D, bool SCRATCH>
+__global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cache c, const Rows rows, const Scratch scratch) {
+    using Lay = Layout<D>;
+    constexpr int L = D / 8, R = 32 / L;
+    __shared__ Items items;
+    const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
+    const int64_t total = lay_items<SCRATCH>(a, scratch, items) * a.Hk;
+    for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
+        int64_t i = at / a.Hk;
+        const int h = (int)(at - i * a.Hk);
+        Span s;
+        const int b = find<SCRATCH>(a, scratch, items, i, s);
+        const int block = (i < s.head ? 0 : s.from - s.head) + (int)i, t0 = block * kBlock;
+        const int slot = a.slots ? a.slots[b] : b;
+        const uint8_t* const from = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
+        const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);
+        __nv_bfloat16 *k_to, *v_to;
+        int64_t k_next, v_next;                 // from token to token
+        if constexpr (SCRATCH) {
+            const int64_t first = (((int64_t)b * a.Hk + h) * scratch.length + t0) * D;
+            k_to = scratch.k + first;
+            v_to = scratch.v + first;
+            k_next = v_next = D;
+        } else {
+            const int64_t row0 = (int64_t)s.row0 - s.first + t0;
+            k_to = rows.k + row0 * rows.k_stride + h * D;
+            v_to = rows.v + row0 * rows.v_stride + h * D;
+            k_next = rows.k_stride;
+            v_next = rows.v_stride;
+        }
+        for (int step = lo / R; step * R < hi; step += kAtOnce) {
+            uint32_t k[kAtOnce], codes[kAtOnce];
+            uint2 v[kAtOnce];
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int j = (step + u) * R + lane / L;
+                if (j < lo || j >= hi) continue;
+                k[u] = *reinterpret_cast<const uint32_t*>(from + j * (D / 2) + col * 4);
+                v[u] = *reinterpret_cast<const uint2*>(from + Lay::kV + j / 2 * D + col * 8);
+                codes[u] = from[Lay::kScaleK + j * (D / 32) + col / 4] | from[Lay::kScaleV + col / 4 * kBlock + j] << 8;
+            }
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const int j = (step + u) * R + lane / L;
+                if (j < lo || j >= hi) continue;
+                const Scales sk = scale_of(codes[u] & 255u), sv = scale_of(codes[u] >> 8);
+                uint32_t w = k[u], x = swap_bytes(w);
+                *reinterpret_cast<uint4*>(k_to + j * k_next + col * 8) =
+                    make_uint4(to_bf16(field0(w, sk)), to_bf16(field1(w, sk)), to_bf16(field0(x, sk)), to_bf16(field1(x, sk)));
+                w = __byte_perm(v[u].x, v[u].y, j % 2 ? 0x7632 : 0x5410);       // this token's two units
+                x = swap_bytes(w);
+                const uint32_t f0 = to_bf16(field0(w, sv)), f1 = to_bf16(field1(w, sv)), f2 = to_bf16(field0(x, sv)), f3 = to_bf16(field1(x, sv));
+                *reinterpret_cast<uint4*>(v_to + j * v_next + col * 8) =
+                    make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
+            }
+        }
+    }
+}
+
+// Thread blocks for at most `blocks` cache blocks.
+unsigned grid_for(int64_t blocks, int heads) {
+    const int64_t want = (blocks * heads + kWarps - 1) / kWarps, most = 8 * (int64_t)sm_count();
+    return (unsigned)(want < most ? (want < 1 ? 1 : want) : most);
+}
+
+// A call's rows: checks, and the arguments as the kernels see them.
+bd_status rows_call(bool write, void* k, int64_t k_stride, void* v, int64_t v_stride, int64_t T, int64_t B, const bd_kv_cache4* cache,
+                    const int32_t* slots, const int32_t* cu_q, const int32_t* lens, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    bd_status st;
+    if (bad_cache4(cache, &st)) return st;
+    const int64_t row = (int64_t)cache->kv_heads * cache->head_dim;
+    if (T < 0 || T > (int64_t)1 << 30 || B < 0 || B > 65535 || (!cu_q && T != B) || k_stride < row || v_stride < row || k_stride > attn::kMaxStride ||
+        v_stride > attn::kMaxStride)
+        return BD_ERR_SHAPE;
+    if (T == 0 || B == 0) return BD_OK;
+    if (!k || !v || !lens) return BD_ERR_NULL;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8 || !aligned(slots, 4) || !aligned(cu_q, 4) || !aligned(lens, 4))
+        return BD_ERR_ALIGN;
+    if (!workspace || ws_bytes < kHeaderBytes) return BD_ERR_WORKSPACE;
+    if (!aligned(workspace, 16)) return BD_ERR_ALIGN;
+    const Args a = args_of(cache, T, B, slots, cu_q, lens, workspace);
+    const Cache c = kernel_cache(cache);
+    const Rows rows{static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride};
+    const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads);
+    const Scratch none{};
+    if (write) {
+        if (cache->head_dim == 128) write_kernel<128><<<grid, kThreads, 0, stream>>>(a, c, rows);
+        else write_kernel<64><<<grid, kThreads, 0, stream>>>(a, c, rows);
+    } else {
+        if (cache->head_dim == 128) read_kernel<128, false><<<grid, kThreads, 0, stream>>>(a, c, rows, none);
+        else read_kernel<64, false><<<grid, kThreads, 0, stream>>>(a, c, rows, none);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+bool bad_cache4(const bd_kv_cache4* c, bd_status* st) {
+    if (!c || !c->data) { *st = BD_ERR_NULL; return true; }
+    if (c->slots < 1 || c->slots > attn::kMaxTokens || c->capacity < 1 || c->capacity > attn::kMaxTokens || c->capacity % kBlock ||
+        c->kv_heads < 1 || (c->head_dim != 64 && c->head_dim != 128) || c->stride_slot < 1 || c->stride_head < 1 ||
+        c->stride_slot > 2 * attn::kMaxStride || c->stride_head > 2 * attn::kMaxStride) {
+        *st = BD_ERR_SHAPE;
+        return true;
+    }
+    if (!aligned(c->data, 16) || c->stride_slot % 16 || c->stride_head % 16) { *st = BD_ERR_ALIGN; return true; }
+    return false;
+}
+
+attn::Args args_of(const bd_kv_cache4* cache, int64_t T, int64_t B, const int32_t* slots, const int32_t* cu_q, const int32_t* lens, void* workspace) {
+    Args a{};
+    a.n_slots = (int32_t)cache->slots;
+    a.capacity = (int32_t)cache->capacity;
+    a.T = (int32_t)T;
+    a.B = (int32_t)B;
+    a.Hk = cache->kv_heads;
+    a.slots = slots;
+    a.cu_q = cu_q;
+    a.lens = lens;
+    a.status = static_cast<unsigned*>(workspace);
+    return a;
+}
+
+Cache kernel_cache(const bd_kv_cache4* c) { return Cache{static_cast<uint8_t*>(c->data), c->stride_slot, c->stride_head}; }
+
+bd_status launch_seen(const Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, int32_t* lens, cudaStream_t stream) {
+    const Scratch scratch{k, v, length, lens};
+    const unsigned grid = grid_for((int64_t)a.B * (length / kBlock + 1), a.Hk);
+    const Rows none{};
+    if (head_dim == 128) read_kernel<128, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
+    else read_kernel<64, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
+    return launch_status();
+}
+
+}  // namespace cache4
+}  // namespace bd
+
+extern "C" size_t bitdelta_cache4_bytes(int64_t slots, int64_t capacity, int32_t kv_heads, int32_t head_dim) {
+    bd_kv_cache4 c{reinterpret_cast<void*>(16), slots, capacity, kv_heads, head_dim, 16, 16};
+    bd_status st;
+    if (bd::cache4::bad_cache4(&c, &st)) return 0;
+    // (slots, capacity up to 2^24, heads up to 2^31: what does not fit 63 bits is no size)
+    const double bytes = (double)slots * (double)kv_heads * (double)(capacity / bd::cache4::kBlock) * (17.0 * head_dim);
+    return bytes < 9e18 ? (size_t)slots * (size_t)kv_heads * (size_t)(capacity / bd::cache4::kBlock) * (size_t)(17 * head_dim) : 0;
+}
+
+extern "C" bd_status bitdelta_cache4_write(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T, int64_t B, const bd_kv_cache4* cache,
+                                           const int32_t* slots, const int32_t* cu_q, const int32_t* lens, void* workspace, size_t ws_bytes, void* stream) {
+    return bd::cache4::rows_call(true, const_cast<void*>(k), k_stride, const_cast<void*>(v), v_stride, T, B, cache, slots, cu_q, lens, workspace, ws_bytes,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+extern "C" bd_status bitdelta_cache4_read(void* k, int64_t k_stride, void* v, int64_t v_stride, int64_t T, int64_t B, const bd_kv_cache4* cache,
+                                          const int32_t* slots, const int32_t* cu_q, const int32_t* lens, void* workspace, size_t ws_bytes, void* stream) {
+    return bd::cache4::rows_call(false, k, k_stride, v, v_stride, T, B, cache, slots, cu_q, lens, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}

@@ -20,8 +20,9 @@ grouped once (``bd.group``) and every projection runs through
 
 ``CachedAttention`` is an ``attend`` on a key/value cache: it appends the step's
 keys and values (plain torch) and runs the library's attention on them, decode
-or prefill, with shared prefixes, a window, and eviction to a budget.  Rotating
-q and k by position, where a model does, is its caller's.
+or prefill, with shared prefixes, a window, and eviction to a budget.  With
+``bits=4`` the cache is held in 4 bits: the library quantises new tokens as it writes them.
+Rotating q and k by position, where a model does, is its caller's.
 """
 from __future__ import annotations
 
@@ -66,7 +67,8 @@ def chained_layer(bd, lin: dict, h, V: int, ws, bufs: dict, path: str = "auto", 
 
 
 def _held(name: str):
-    """A tensor that stays in its place: what is assigned to it is copied into it."""
+    """A tensor that stays in its place: what is assigned to it is copied into it
+    (None where the cache has none)."""
     return property(lambda self: getattr(self, name), lambda self, t: getattr(self, name).copy_(t))
 
 
@@ -79,6 +81,12 @@ class CachedAttention:
     step can be captured in a CUDA graph.  A shared prefix lies in a slot of its
     own, filled by ``prefill`` like any other.
 
+    With ``bits=4`` the keys and values are ``cache``, a 4-bit cache (see ``bd.cache4``; k and v are
+    None), in 17/64 of the bytes; ``capacity`` is then a multiple of 16.  ``longest``: the most keys, new ones
+    included, of a request whose prompt is served (the capacity, unless given: prompts read
+    the keys they see back to bf16, and the workspace has room for `batch` requests of that many).  Shared
+    prefixes, weights and eviction are the bf16 cache's.
+
     A request whose slot is not there, or has no room for all its new tokens, is
     left as it is: nothing is appended, its rows come out as zeros, and the status
     word of ``ws`` holds ``BD_ERR_SLOT``."""
@@ -86,22 +94,37 @@ class CachedAttention:
     k, v, lens, weights = _held("_k"), _held("_v"), _held("_lens"), _held("_weights")
 
     def __init__(self, bd, slots: int, capacity: int, q_heads: int, kv_heads: int, head_dim: int, tokens: int,
-                 batch: int, window: int = 0, sinks: int = 0, weigh: bool = False, device="cuda"):
+                 batch: int, window: int = 0, sinks: int = 0, weigh: bool = False, device="cuda", bits: int = 16,
+                 longest: int | None = None):
         import torch
+        if bits not in (4, 16):
+            raise ValueError("a cache holds 4 or 16 bits a value")
+        if bits == 4 and weigh:
+            raise ValueError("a 4-bit cache does not accumulate weights")
+        if bits == 16 and longest is not None:
+            raise ValueError("only a 4-bit cache has prompts of a longest length")
         self.bd, self.torch = bd, torch
         self.heads = (q_heads, kv_heads, head_dim)
         self.mask = {"window": window, "sinks": sinks}
-        # Behind the cache's places lies one more key, and a slot that is always full: what
-        # has no place of its own goes there, so that no index leaves its tensor (on a GPU
-        # that ends the context) and no step waits for the host.
+        self.capacity, self.cache, self._weights = capacity, None, None
+        # behind the cache's slots lies one that is always full: its length is that of what has no slot
+        self.slot_lens = torch.zeros(slots + 1, dtype=torch.int32, device=device)
+        self.slot_lens[-1] = capacity
+        self._lens = self.slot_lens[:-1]
+        if bits == 4:
+            self._k = self._v = None
+            self.longest = capacity if longest is None else min(longest, capacity)
+            self.cache = bd.cache4(slots, capacity, kv_heads, head_dim, device)
+            self.ws = bd.attn4_workspace(tokens, batch, q_heads, kv_heads, head_dim, self.longest, device)
+            return
+        self.longest = capacity
+        # Behind the cache's places lies one more key: what has no place of its own goes
+        # there, so that no index leaves its tensor (on a GPU that ends the context) and no
+        # step waits for the host.
         shape = (slots, capacity, kv_heads, head_dim)
         self.rows_k = torch.zeros(slots * capacity + 1, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
         self.rows_v = torch.zeros_like(self.rows_k)
         self._k, self._v = self.rows_k[:-1].view(shape), self.rows_v[:-1].view(shape)
-        self.slot_lens = torch.zeros(slots + 1, dtype=torch.int32, device=device)
-        self.slot_lens[-1] = capacity
-        self._lens = self.slot_lens[:-1]
-        self._weights = None
         if weigh:
             self.slot_weights = torch.zeros(slots + 1, kv_heads, capacity, device=device)
             self._weights = self.slot_weights[:-1]
@@ -113,13 +136,18 @@ class CachedAttention:
         """Places in ``slot_lens``: those of no slot (-1 and ``slots``) are the one behind."""
         return slots.clamp(-1, self.lens.shape[0]).long()
 
+    def _write(self, k, v, lens, slots, cu_q=None):
+        """A 4-bit cache's append: rows of k and v become the last of the requests' keys."""
+        _, hk, d = self.heads
+        self.bd.cache4_write(k.view(-1, hk, d), v.view(-1, hk, d), self.cache, lens, self.ws, slots=slots, cu_q=cu_q)
+
     def _append(self, k, v, place):
         """Rows of k and v become the keys at ``place``, counted through all slots (-1: the one behind)."""
         _, hk, d = self.heads
         self.rows_k[place] = k.view(-1, hk, d)
         self.rows_v[place] = v.view(-1, hk, d)
         if self.weights is not None:
-            capacity = self.k.shape[1]
+            capacity = self.capacity
             # (a number would be copied from the host, which the capture of a graph refuses)
             self.slot_weights[place // capacity, :, place % capacity] = self.zero
 
@@ -132,31 +160,42 @@ class CachedAttention:
             self.slot_lens[to] = have
             raise
 
+    def _no_prefix4(self, *prefix):
+        if self.cache is not None and any(p is not None for p in prefix):
+            raise ValueError("a 4-bit cache has no shared prefixes")
+
     def _prefix_lens(self, prefix_slots):
         return None if prefix_slots is None else self.slot_lens[self._slots(prefix_slots)]
 
     def decode(self, q, k, v, slots, prefix_ids=None, prefix_slots=None):
         """One token for each request: its slot in ``slots`` (int32 [M], none twice); requests
         may name shared prefixes by their index in ``prefix_slots``."""
-        torch, capacity = self.torch, self.k.shape[1]
+        torch, capacity = self.torch, self.capacity
         hq, _, d = self.heads
+        self._no_prefix4(prefix_ids, prefix_slots)
         to = self._slots(slots)
         have = self.slot_lens[to]
-        self._append(k, v, torch.where(have < capacity, torch.add(have, to, alpha=capacity), -1))
+        if self.cache is None:
+            self._append(k, v, torch.where(have < capacity, torch.add(have, to, alpha=capacity), -1))
         lens = have + 1                           # beyond a full slot's capacity: the call below reports it
         self.slot_lens[to] = lens.clamp_max(capacity)
         with self._given_back(to, have):
-            out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots,
-                                             self._prefix_lens(prefix_slots), self.ws, slots=slots, weights=self.weights,
-                                             **self.mask)
+            if self.cache is not None:
+                self._write(k, v, lens, slots)
+                out = self.bd.attn4_decode(q.view(-1, hq, d), self.cache, lens, self.ws, slots=slots, **self.mask)
+            else:
+                out = self.bd.attn_decode_prefix(q.view(-1, hq, d), self.k, self.v, lens, prefix_ids, prefix_slots,
+                                                 self._prefix_lens(prefix_slots), self.ws, slots=slots, weights=self.weights,
+                                                 **self.mask)
         return out.view(-1, hq * d)
 
     def prefill(self, q, k, v, slots, cu_q, prefix_ids=None, prefix_slots=None):
         """The next tokens of some requests: rows ``cu_q[b]`` to ``cu_q[b + 1]`` are
         the request's in slot ``slots[b]``.  Rows of no request are not written."""
-        torch, capacity = self.torch, self.k.shape[1]
+        torch, capacity = self.torch, self.capacity
         hq, _, d = self.heads
         T = q.shape[0]
+        self._no_prefix4(prefix_ids, prefix_slots)
         to = self._slots(slots)
         have = self.slot_lens[to]
         # requests from the first whose offsets do not ascend on are not served (as the
@@ -164,7 +203,16 @@ class CachedAttention:
         steady = cu_q.clamp(0, T).cummax(0).values
         served = (steady == cu_q).cumprod(0, dtype=torch.int32)[1:]
         lens = have + (cu_q[1:] - cu_q[:-1]) * served
-        fits = (lens <= capacity) & (served > 0)
+        fits = (lens <= self.longest) & (served > 0)
+        if self.cache is not None:
+            fits |= (cu_q[1:] == cu_q[:-1]) & (served > 0)    # nothing new: nothing that could be too long
+            self.slot_lens[to] = torch.where(fits, lens, have)
+            with self._given_back(to, have):
+                lens = torch.where(fits, lens, -1)    # no length at all: the calls report it
+                self._write(k, v, lens, slots, cu_q)
+                out = self.bd.attn4_prefill(q.view(-1, hq, d), self.cache, cu_q, lens, self.ws, self.longest, slots=slots,
+                                            **self.mask)
+            return out.view(-1, hq * d)
         # a request's first place less its first row; far below zero for rows that are appended nowhere
         start = torch.where(fits, torch.add(have, to, alpha=capacity) - cu_q[:-1], -1 << 40)
         start = torch.nn.functional.pad(start, (1, 1), value=-1 << 40)
@@ -191,6 +239,8 @@ class CachedAttention:
         the keys that stay: ``recent`` >= window - 1 (the next query sees itself and
         as many before it)."""
         window = self.mask["window"]
+        if self.cache is not None:
+            raise ValueError("a 4-bit cache is not evicted from")
         if window > 0 and recent < window - 1:
             raise ValueError("recent must be at least window - 1 (%d): keys that left the window would come back into it"
                              % (window - 1))

@@ -382,6 +382,89 @@ bd_status bitdelta_cache_evict(const bd_kv_cache *cache, float *weights, int32_t
                                size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* A key/value cache held in 4 bits, and attention over it: 17/64 of the */
+/* bf16 cache's bytes.  (The page has no counterpart: the cache is the    */
+/* standard forward pass's, like the attention above.)                    */
+/* ------------------------------------------------------------------ */
+
+/* One layer's 4-bit cache, described on the HOST and read during the call only.
+ * 32 consecutive values of a head of a token share a scale s, an unsigned float
+ * of 5 exponent and 3 mantissa bits (bias 15): the one nearest (ties to even) to
+ * max|x| / 7, at most 240.  A value is kept as n s, n the whole number nearest
+ * (ties to even) to x / s in [-7, 7].  So |x - n s| <= s / 2 in a group whose
+ * largest magnitude lies in [7 2^-14, 1680]; larger values become 1680, smaller
+ * groups keep units of 2^-17.  A group that holds a NaN or an infinity becomes NaN.
+ *   data  : device, blocks of 16 tokens of one head, 17 * head_dim bytes each (K, V
+ *           and their scales; the order of the bytes is the library's own): token j of a
+ *           slot's head lies in block j / 16 of the capacity / 16 blocks that follow one another
+ *           at data + slot * stride_slot + head * stride_head.  16-byte aligned.
+ *           Zero bytes are a valid cache of zeros.
+ *   strides in bytes, multiples of 16 in [16, 2^39]; distinct heads of slots do not overlap.
+ *   slots, capacity, kv_heads >= 1; head_dim 64 or 128; capacity <= 2^24 and a multiple
+ *   of 16, slots <= 2^24. */
+typedef struct {
+    void *data;
+    int64_t slots, capacity;
+    int32_t kv_heads, head_dim;
+    int64_t stride_slot, stride_head;
+} bd_kv_cache4;
+
+/* Bytes of a cache without gaps, [slots, kv_heads, capacity / 16, 17 * head_dim].
+ * Returns 0 for invalid sizes. */
+size_t bitdelta_cache4_bytes(int64_t slots, int64_t capacity, int32_t kv_heads, int32_t head_dim);
+
+/* Quantise new tokens as they are written.  Requests, slots, lens and cu_q as in
+ * bitdelta_attn_prefill: rows cu_q[b] .. cu_q[b+1] - 1 of k and v become the last of
+ * the lens[b] keys of request b (cu_q NULL: one row a request, T == B).  So the arrays of the attention call that
+ * follows serve here too.
+ *   k, v      : device bf16, row t starts at k + t * k_stride (v + t * v_stride) elements
+ *               and holds kv_heads * head_dim contiguous values; 16-byte aligned, strides
+ *               multiples of 8.
+ *   workspace : device, any workspace of the library (256 bytes): its status word.
+ * Nothing but the places of the call's rows is written.  A request with a slot or
+ * length out of range, or with more rows than keys, is not written and sets BD_ERR_SLOT, and
+ * so is every request from the first on whose offsets do not ascend within [0, T].
+ * Two requests of one call may not share a slot (their rows would meet). */
+bd_status bitdelta_cache4_write(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                int64_t T, int64_t B, const bd_kv_cache4 *cache, const int32_t *slots,
+                                const int32_t *cu_q, const int32_t *lens, void *workspace,
+                                size_t ws_bytes, void *stream);
+
+/* Read keys and values back: the same rows the other way, rows cu_q[b] ..
+ * cu_q[b+1] - 1 of k and v (written here) become what the cache holds of the last of request b's
+ * lens[b] keys.  The values are exact in bf16.  Rows of no request, and of requests that
+ * bitdelta_cache4_write would not write, are left as they are; requests may
+ * share a slot. */
+bd_status bitdelta_cache4_read(void *k, int64_t k_stride, void *v, int64_t v_stride, int64_t T,
+                               int64_t B, const bd_kv_cache4 *cache, const int32_t *slots,
+                               const int32_t *cu_q, const int32_t *lens, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace for attention calls on a 4-bit cache of at most `tokens`
+ * query rows and `batch` requests.  `longest`: the most keys that a request of a
+ * bitdelta_attn4_prefill call has (0: decode only); prompts read the keys that they see back to
+ * bf16, into 4 * batch * kv_heads * longest * head_dim bytes.  Returns 0 for invalid sizes. */
+size_t bitdelta_attn4_workspace(int64_t tokens, int64_t batch, int32_t q_heads, int32_t kv_heads,
+                                int32_t head_dim, int64_t longest);
+
+/* bitdelta_attn_decode and bitdelta_attn_prefill (without prefixes and weights) on a 4-bit
+ * cache: attention on the values that the cache stands for, with the same heads, mask,
+ * requests, results, errors and workspace rules.  `longest` bounds the keys of every request: one
+ * with more gets zero rows and sets BD_ERR_SLOT.
+ * Precision: f32 statistics and sums, the result rounded once to bf16; decode
+ * multiplies probabilities of 11 significant bits, prefill ones rounded to bf16.
+ * A query that is not finite gives results that are not finite. */
+bd_status bitdelta_attn4_decode(const void *q, int64_t q_stride, int64_t B, int32_t q_heads,
+                                const bd_kv_cache4 *cache, const int32_t *slots, const int32_t *lens,
+                                int32_t window, int32_t sinks, float scale, void *out,
+                                void *workspace, size_t ws_bytes, void *stream);
+bd_status bitdelta_attn4_prefill(const void *q, int64_t q_stride, int64_t T, int64_t B,
+                                 int32_t q_heads, const bd_kv_cache4 *cache, const int32_t *slots,
+                                 const int32_t *cu_q, const int32_t *lens, int64_t longest,
+                                 int32_t window, int32_t sinks, float scale, void *out,
+                                 void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Status                                                               */
 /* ------------------------------------------------------------------ */
 
