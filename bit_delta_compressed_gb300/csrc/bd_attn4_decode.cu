@@ -17,6 +17,8 @@
 // P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
 #include <math.h>
 
+#include <type_traits>
+
 #include "bd_attn_line.cuh"
 #include "bd_attn4.cuh"
 #include "bd_cache4.cuh"
@@ -33,10 +35,9 @@ using cache4::Scales;
 
 constexpr int kBlocks = 2;                // cache blocks of a tile
 constexpr int kTile = kBlocks * kBlock;   // its keys
-// The running maximum is kept this many powers of two below the scores' (probabilities
-// then reach down to 2^-30 of the largest before they lose bits of f16) and lags
-// behind by up to 2^kLag / 2^kLift: 2^14 is within f16.
-constexpr float kLift = 6.f, kLag = 14.f;
+// The running maximum is kept this many powers of two below the scores' (so the largest probability is 2^6 at
+// least, and others keep f16's bits down to 2^-20 of it), and moves only once a probability exceeds 2^14.
+constexpr float kLift = 6.f;
 
 // Where the visible keys of a request lie: tiles from the first key on (`head` of them)
 // and, behind a gap, those from tile `from` on.
@@ -73,8 +74,7 @@ struct Shape4 {
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -82,7 +82,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 // An 8 x 8 matrix of 16-bit values across the warp, transposed.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
 
@@ -92,34 +92,40 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-// W words at a time from shared memory.
-template <int W>
-__device__ __forceinline__ void load_words(uint32_t (&w)[W], uint32_t at) {
-    if constexpr (W == 4)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
-    else
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ uint32_t load_byte(uint32_t at) {
+// The larger ones of two pairs (a NaN is never larger).
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
-    return r;
-}
-__device__ __forceinline__ uint32_t load_two(uint32_t at) {
-    uint16_t r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at) : "memory");
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// A tile's bytes as they lie; of the last one only blocks that hold keys.
+// Whether one of a pair exceeds 2^14.
+__device__ __forceinline__ bool over(uint32_t a) {
+    uint32_t r;
+    asm("set.gt.u32.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x74007400u));
+    return r != 0;
+}
+
+// W words at a time from shared memory.
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&w)[W], const uint8_t* at) {
+    if constexpr (W == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(at);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(at);
+        w[0] = x.x, w[1] = x.y;
+    }
+}
+
+// A tile's bytes as they lie, from its unit's first block; of the last one only blocks that hold keys.
 template <int D>
-__device__ __forceinline__ void load_tile4(const Cache& cache, const Cursor<Keys4>& c, int chunks, uint32_t stage, int lane) {
+__device__ __forceinline__ void load_tile4(const uint8_t* unit, const Keys4& k, int tile, uint32_t to) {
     constexpr int kChunks = kBlocks * Layout<D>::kBytes / 16;
-    const int base = c.k.base(c.tile);
-    const int blocks = (c.k.len - base + kBlock - 1) / kBlock;
-    const int n = blocks >= kBlocks ? kChunks : max(blocks, 0) * (Layout<D>::kBytes / 16);
-    const uint8_t* from = cache.data + c.r.slot * cache.ss + c.u / chunks * cache.sh + (int64_t)(base / kBlock) * Layout<D>::kBytes + lane * 16;
-    const uint32_t to = stage + lane * 16;
+    const int lane = threadIdx.x % 32, base = k.base(tile);
+    const uint8_t* from = unit + (int64_t)base * (Layout<D>::kBytes / kBlock);
+    // (lane * 16 is in both addresses)
+    const int n = base + kTile - kBlock < k.len ? kChunks : (k.len - base + kBlock - 1) / kBlock * (Layout<D>::kBytes / 16);
 #pragma unroll
     for (int i = 0; i < (kChunks + 31) / 32; ++i)
         if (lane + i * 32 < n)
@@ -141,19 +147,27 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     const int units = a.Hk * chunks;
 
     const Line<Keys4> line = lay_line<Keys4>(a, sh, units);
-    const uint32_t ring = smem_addr(smem) + warp * S::kRing;
-    float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
+    uint8_t* const ring = smem + warp * S::kRing;
+    float* const tail_part = reinterpret_cast<float*>(ring);
     float* const head_part = reinterpret_cast<float*>(smem + S::kWarps * S::kRing + warp * S::kPart);
+    const cache4::Ones ones;
 
     Cursor<Keys4> c;
     if (first_unit(a, sh, line, c, units)) {
         Cursor<Keys4> ahead = c;
         bool more = true;
         int put = 0;
+        const uint32_t ring_at = smem_addr(ring) + lane * 16;
+        const uint8_t* unit;
+        auto enter = [&]() { unit = cache.data + ahead.r.slot * cache.ss + ahead.u / chunks * cache.sh + lane * 16; };
+        enter();
         auto prefetch = [&]() {
             if (more) {
-                load_tile4<D>(cache, ahead, chunks, ring + put * S::kStage, lane);
-                if (++ahead.tile == ahead.end) more = next_unit(a, sh.kept, line, ahead, units);
+                load_tile4<D>(unit, ahead.k, ahead.tile, ring_at + put * S::kStage);
+                if (++ahead.tile == ahead.end) {
+                    more = next_unit(a, sh.kept, line, ahead, units);
+                    enter();
+                }
             }
             cp_async_commit();
             if (++put == S::kStages) put = 0;
@@ -166,6 +180,118 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
         uint32_t qf[NT][2 * W][2];         // of head 8 n + g: the lane's dims of each step
         float factor[NT][2];               // scores in powers of two: of heads 8 n + 2 t, + 1
         float o[NT][MT][4], l[NT][4], m[NT][2];
+        // One tile; of one that is not WHOLE some keys are not seen.
+        auto tile = [&](auto whole, const uint8_t* stage, int base) {
+            constexpr bool WHOLE = decltype(whole)::value;
+            float s[kBlocks][NT][4];
+#pragma unroll
+            for (int x = 0; x < kBlocks; ++x) {
+                const uint8_t* at = stage + x * Lay::kBytes;
+                uint32_t ka[W], kb[W];                 // keys g and g + 8
+                load_words(ka, at + g * (D / 2) + t * (4 * W));
+                load_words(kb, at + (g + 8) * (D / 2) + t * (4 * W));
+                const uint8_t* code = at + Lay::kScaleK + g * (D / 32) + t * (D / 32) / 4;
+                const Scales sa = cache4::scale_of(code[0]), sb = cache4::scale_of(code[8 * (D / 32)]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[x][n][0] = s[x][n][1] = s[x][n][2] = s[x][n][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2 * W; ++i) {
+                    const uint32_t wa = i % 2 ? cache4::swap_bytes(ka[i / 2]) : ka[i / 2], wb = i % 2 ? cache4::swap_bytes(kb[i / 2]) : kb[i / 2];
+                    const uint32_t a0 = cache4::field0(wa, sa, ones), a1 = cache4::field0(wb, sb, ones);
+                    const uint32_t a2 = cache4::field1(wa, sa, ones), a3 = cache4::field1(wb, sb, ones);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(s[x][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
+                }
+            }
+            bool seen[kBlocks][2], two[kBlocks][4];    // keys g, g + 8; keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+#pragma unroll
+            for (int x = 0; x < kBlocks; ++x) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) seen[x][i] = WHOLE || c.k.sees(base + x * kBlock + g + 8 * i);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) two[x][i] = WHOLE || c.k.sees(base + x * kBlock + 2 * t + i % 2 + i / 2 * 8);
+            }
+            uint32_t p[kBlocks][NT][2];
+            auto weigh = [&]() {
+                uint32_t top = 0;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float p0 = exp2_approx(fmaf(s[x][n][2 * i], factor[n][0], -m[n][0]));
+                            const float p1 = exp2_approx(fmaf(s[x][n][2 * i + 1], factor[n][1], -m[n][1]));
+                            p[x][n][i] = seen[x][i] ? pack_f16(p0, p1) : 0u;
+                            top = max2(top, p[x][n][i]);
+                        }
+                return __any_sync(0xffffffffu, over(top));
+            };
+            if (weigh()) {
+                // the maximum moves (from -inf, at first)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float f[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if (seen[x][y]) top = fmaxf(top, s[x][n][2 * y + i] * factor[n][i]);
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) - kLift;
+                        f[i] = top > m[n][i] ? exp2_approx(m[n][i] - top) : 1.f;
+                        m[n][i] = fmaxf(m[n][i], top);
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        o[n][i][0] *= f[0];
+                        o[n][i][1] *= f[1];
+                        o[n][i][2] *= f[0];
+                        o[n][i][3] *= f[1];
+                    }
+                    l[n][0] *= f[0];
+                    l[n][1] *= f[1];
+                    l[n][2] *= f[0];
+                    l[n][3] *= f[1];
+                }
+                weigh();
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) p[x][n][i] = transpose8(p[x][n][i]);
+#pragma unroll
+            for (int x = 0; x < kBlocks; ++x) {
+                const uint8_t* at = stage + x * Lay::kBytes;
+                uint32_t va[W], vb[W];                 // of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
+                load_words(va, at + Lay::kV + t * D + g * (4 * W));
+                load_words(vb, at + Lay::kV + (t + 4) * D + g * (4 * W));
+                const uint16_t* code = reinterpret_cast<const uint16_t*>(at + Lay::kScaleV + g * (D / 32) / 8 * kBlock + 2 * t);
+                uint32_t pa = cache4::scale_pair(code[0]), pb = cache4::scale_pair(code[4]);
+                if constexpr (!WHOLE) {
+                    // values that are not seen become zeros, whatever they are
+                    pa &= (two[x][0] ? 0xFFFFu : 0u) | (two[x][1] ? 0xFFFF0000u : 0u);
+                    pb &= (two[x][2] ? 0xFFFFu : 0u) | (two[x][3] ? 0xFFFF0000u : 0u);
+                }
+                const Scales sa = cache4::scales(pa), sb = cache4::scales(pb);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    const uint32_t wa = i % 2 ? cache4::swap_bytes(va[i / 2]) : va[i / 2], wb = i % 2 ? cache4::swap_bytes(vb[i / 2]) : vb[i / 2];
+                    const uint32_t a0 = cache4::field0(wa, sa, ones), a1 = cache4::field1(wa, sa, ones);
+                    const uint32_t a2 = cache4::field0(wb, sb, ones), a3 = cache4::field1(wb, sb, ones);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(o[n][i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[x][n][0], p[x][n][1]);
+            }
+        };
         do {
             const int seg_tile = c.tile;
             const int hk = c.u / chunks, g0 = (c.u % chunks) * R;
@@ -202,104 +328,11 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
                 prefetch();
                 cp_async_wait<S::kStages - 1>();
                 __syncwarp();
-                const uint32_t stage = ring + got * S::kStage;
+                const uint8_t* const stage = ring + got * S::kStage;
                 if (++got == S::kStages) got = 0;
                 const int base = c.k.base(c.tile);
-                const bool whole = c.k.whole(base);
-                float s[kBlocks][NT][4];
-#pragma unroll
-                for (int x = 0; x < kBlocks; ++x) {
-                    const uint32_t at = stage + x * Lay::kBytes;
-                    uint32_t ka[W], kb[W];                 // keys g and g + 8
-                    load_words(ka, at + g * (D / 2) + t * (4 * W));
-                    load_words(kb, at + (g + 8) * (D / 2) + t * (4 * W));
-                    const uint32_t code = at + Lay::kScaleK + g * (D / 32) + t * (D / 32) / 4;
-                    const Scales sa = cache4::scale_of(load_byte(code)), sb = cache4::scale_of(load_byte(code + 8 * (D / 32)));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) s[x][n][0] = s[x][n][1] = s[x][n][2] = s[x][n][3] = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 2 * W; ++i) {
-                        const uint32_t wa = i % 2 ? cache4::swap_bytes(ka[i / 2]) : ka[i / 2], wb = i % 2 ? cache4::swap_bytes(kb[i / 2]) : kb[i / 2];
-                        const uint32_t a0 = cache4::field0(wa, sa), a1 = cache4::field0(wb, sb), a2 = cache4::field1(wa, sa), a3 = cache4::field1(wb, sb);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(s[x][n], a0, a1, a2, a3, qf[n][i][0], qf[n][i][1]);
-                    }
-                }
-                bool grows = false;
-#pragma unroll
-                for (int x = 0; x < kBlocks; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool in = whole || c.k.sees(base + x * kBlock + g + i / 2 * 8);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            s[x][n][i] = in ? s[x][n][i] * factor[n][i % 2] : -INFINITY;
-                            grows = grows || s[x][n][i] > m[n][i % 2] + kLag;
-                        }
-                    }
-                if (__any_sync(0xffffffffu, grows)) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float f[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float top = -INFINITY;
-#pragma unroll
-                            for (int x = 0; x < kBlocks; ++x) top = fmaxf(top, fmaxf(s[x][n][i], s[x][n][2 + i]));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)) - kLift;
-                            f[i] = top > m[n][i] ? exp2_approx(m[n][i] - top) : 1.f;
-                            m[n][i] = fmaxf(m[n][i], top);
-                        }
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            o[n][i][0] *= f[0];
-                            o[n][i][1] *= f[1];
-                            o[n][i][2] *= f[0];
-                            o[n][i][3] *= f[1];
-                        }
-                        l[n][0] *= f[0];
-                        l[n][1] *= f[1];
-                        l[n][2] *= f[0];
-                        l[n][3] *= f[1];
-                    }
-                }
-                uint32_t p[kBlocks][NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float use0 = m[n][0] == -INFINITY ? 0.f : m[n][0], use1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-#pragma unroll
-                    for (int x = 0; x < kBlocks; ++x)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            p[x][n][i] = transpose8(pack_f16(exp2_approx(s[x][n][2 * i] - use0), exp2_approx(s[x][n][2 * i + 1] - use1)));
-                }
-#pragma unroll
-                for (int x = 0; x < kBlocks; ++x) {
-                    const uint32_t at = stage + x * Lay::kBytes;
-                    uint32_t va[W], vb[W];                 // of keys 2 t, 2 t + 1 and of 2 t + 8, 2 t + 9
-                    load_words(va, at + Lay::kV + t * D + g * (4 * W));
-                    load_words(vb, at + Lay::kV + (t + 4) * D + g * (4 * W));
-                    const uint32_t code = at + Lay::kScaleV + g * (D / 32) / 8 * kBlock + 2 * t;
-                    uint32_t pa = cache4::scale_pair(load_two(code)), pb = cache4::scale_pair(load_two(code + 8));
-                    if (!whole) {
-                        // values that are not seen become zeros, whatever they are
-                        const int key = base + x * kBlock + 2 * t;
-                        pa &= (c.k.sees(key) ? 0xFFFFu : 0u) | (c.k.sees(key + 1) ? 0xFFFF0000u : 0u);
-                        pb &= (c.k.sees(key + 8) ? 0xFFFFu : 0u) | (c.k.sees(key + 9) ? 0xFFFF0000u : 0u);
-                    }
-                    const Scales sa = cache4::scales(pa), sb = cache4::scales(pb);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        const uint32_t wa = i % 2 ? cache4::swap_bytes(va[i / 2]) : va[i / 2], wb = i % 2 ? cache4::swap_bytes(vb[i / 2]) : vb[i / 2];
-                        const uint32_t a0 = cache4::field0(wa, sa), a1 = cache4::field1(wa, sa), a2 = cache4::field0(wb, sb), a3 = cache4::field1(wb, sb);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(o[n][i], a0, a1, a2, a3, p[x][n][0], p[x][n][1]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16(l[n], 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u, p[x][n][0], p[x][n][1]);
-                }
+                if (c.k.whole(base)) tile(std::true_type(), stage, base);
+                else tile(std::false_type(), stage, base);
                 __syncwarp();
             }
             // the unit, or this warp's part of it, is done; the lane has dims D / 8 g ... of heads 8 n + 2 t, + 1

@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
     using Lay = Layout<D>;
     constexpr int L = D / 8, R = 32 / L;
     __shared__ Items items;
+    const Ones ones;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
     const int64_t total = lay_items<SCRATCH>(a, scratch, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
@@ -306,10 +307,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
                 const Scales sk = scale_of(codes[u] & 255u), sv = scale_of(codes[u] >> 8);
                 uint32_t w = k[u], x = swap_bytes(w);
                 *reinterpret_cast<uint4*>(k_to + j * k_next + col * 8) =
-                    make_uint4(to_bf16(field0(w, sk)), to_bf16(field1(w, sk)), to_bf16(field0(x, sk)), to_bf16(field1(x, sk)));
+                    make_uint4(to_bf16(field0(w, sk, ones)), to_bf16(field1(w, sk, ones)), to_bf16(field0(x, sk, ones)), to_bf16(field1(x, sk, ones)));
                 w = __byte_perm(v[u].x, v[u].y, j % 2 ? 0x7632 : 0x5410);       // this token's two units
                 x = swap_bytes(w);
-                const uint32_t f0 = to_bf16(field0(w, sv)), f1 = to_bf16(field1(w, sv)), f2 = to_bf16(field0(x, sv)), f3 = to_bf16(field1(x, sv));
+                const uint32_t f0 = to_bf16(field0(w, sv, ones)), f1 = to_bf16(field1(w, sv, ones)), f2 = to_bf16(field0(x, sv, ones)), f3 = to_bf16(field1(x, sv, ones));
                 *reinterpret_cast<uint4*>(v_to + j * v_next + col * 8) =
                     make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
             }

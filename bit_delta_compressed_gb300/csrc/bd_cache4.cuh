@@ -62,14 +62,28 @@ __device__ __forceinline__ Scales scales(uint32_t s) {
 __device__ __forceinline__ Scales scale_of(uint32_t byte) { return scales(byte * 0x00800080u); }   // one scale twice
 __device__ __forceinline__ uint32_t scale_pair(uint32_t two) { return __byte_perm(two, 0, 0x1404) >> 1; }
 
+// What the fields' masks are joined with: 16 and 256 twice.  A logical operation takes one
+// constant at most, so these two are registers.
+struct Ones {
+    uint32_t f0, f1;
+    __device__ __forceinline__ Ones() {
+        asm volatile("mov.u32 %0, 0x4C004C00;" : "=r"(f0));
+        asm volatile("mov.u32 %0, 0x5C005C00;" : "=r"(f1));
+    }
+};
+
+// (w & mask) | ones
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t cut(uint32_t w, uint32_t ones) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(MASK), "r"(ones));
+    return r;
+}
+
 // The first and second field of a word's two units as values, f16x2; with the word's
 // bytes swapped, the third and fourth.
-__device__ __forceinline__ uint32_t field0(uint32_t w, const Scales& s) {
-    return fma2((w & 0x03C003C0u) | 0x4C004C00u, s.s, s.c0);
-}
-__device__ __forceinline__ uint32_t field1(uint32_t w, const Scales& s) {
-    return fma2((w & 0x003C003Cu) | 0x5C005C00u, s.s, s.c1);
-}
+__device__ __forceinline__ uint32_t field0(uint32_t w, const Scales& s, const Ones& k) { return fma2(cut<0x03C003C0u>(w, k.f0), s.s, s.c0); }
+__device__ __forceinline__ uint32_t field1(uint32_t w, const Scales& s, const Ones& k) { return fma2(cut<0x003C003Cu>(w, k.f1), s.s, s.c1); }
 
 }  // namespace cache4
 }  // namespace bd
