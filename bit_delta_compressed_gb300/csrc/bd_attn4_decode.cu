@@ -5,7 +5,7 @@
 // 4 head_dim flops a head and key for 17/16 head_dim bytes, so the cache's bytes bound
 // it, and next to them the instructions that make f16 of 4 bits.  The line of units,
 // the blocks' and warps' parts of it and their joining are those of the bf16 cache's
-// decode kernel; tiles are two cache blocks, 32 keys, and begin where a block
+// decode kernel; tiles are three cache blocks, 48 keys, and begin where a block
 // begins.  A warp streams its tiles, bytes as they lie, through a ring of its own (cp.async) and
 // multiplies the transposed way, S^T = K Q^T and O^T = V^T P^T, with mma.m16n8k16 in f16:
 // keys and dims are the 16 rows and a group's heads the 8 columns, so a group of 8 wastes nothing.  Which
@@ -33,16 +33,16 @@ using cache4::kBlock;
 using cache4::Layout;
 using cache4::Scales;
 
-constexpr int kBlocks = 2;                // cache blocks of a tile
-constexpr int kTile = kBlocks * kBlock;   // its keys
 // The running maximum is kept this many powers of two below the scores' (so the largest probability is 2^6 at
 // least, and others keep f16's bits down to 2^-20 of it), and moves only once a probability exceeds 2^14.
 constexpr float kLift = 6.f;
 
 // Where the visible keys of a request lie: tiles from the first key on (`head` of them)
 // and, behind a gap, those from tile `from` on.
+template <int BLOCKS>
 struct Keys4 {
-    static constexpr int kUnitCost = 2, kLeast = 16, kShort = 64;
+    static constexpr int kTile = BLOCKS * kBlock;                           // keys of a tile
+    static constexpr int kUnitCost = 2, kLeast = 8, kShort = 30;
     int len, lo, sinks, head, from, n;
     static __device__ __forceinline__ Keys4 of(const Args& a, const Request& r) {
         Keys4 k;
@@ -64,7 +64,8 @@ struct Keys4 {
 
 template <int D, int R>
 struct Shape4 {
-    static constexpr int kWarps = R == 8 ? 16 : 8;
+    static constexpr int kWarps = R == 8 ? 12 : 8;
+    static constexpr int kBlocks = R == 8 ? 3 : 2;                          // cache blocks of a tile
     static constexpr int kStage = kBlocks * Layout<D>::kBytes;
     static constexpr int kStages = 2 * (128 / D);
     static constexpr int kRing = kStage * kStages;                          // of one warp
@@ -118,18 +119,23 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[W], const uint8_t* at) 
     }
 }
 
-// A tile's bytes as they lie, from its unit's first block; of the last one only blocks that hold keys.
-template <int D>
-__device__ __forceinline__ void load_tile4(const uint8_t* unit, const Keys4& k, int tile, uint32_t to) {
-    constexpr int kChunks = kBlocks * Layout<D>::kBytes / 16;
+// A tile's bytes as they lie, from its unit's first block; of a request's last one only blocks that
+// hold keys.  (lane * 16 is in both addresses.)
+template <int D, typename Keys>
+__device__ __forceinline__ void load_tile4(const uint8_t* unit, const Keys& k, int tile, uint32_t to) {
+    constexpr int kChunks = Keys::kTile / kBlock * Layout<D>::kBytes / 16;
     const int lane = threadIdx.x % 32, base = k.base(tile);
     const uint8_t* from = unit + (int64_t)base * (Layout<D>::kBytes / kBlock);
-    // (lane * 16 is in both addresses)
-    const int n = base + kTile - kBlock < k.len ? kChunks : (k.len - base + kBlock - 1) / kBlock * (Layout<D>::kBytes / 16);
+    auto copy = [&](int i) { asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512) : "memory"); };
+    if (base + Keys::kTile - kBlock < k.len) {
 #pragma unroll
-    for (int i = 0; i < (kChunks + 31) / 32; ++i)
-        if (lane + i * 32 < n)
-            asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(to + i * 512), "l"(from + i * 512) : "memory");
+        for (int i = 0; i < kChunks / 32; ++i) copy(i);
+        if (kChunks % 32 && lane < kChunks % 32) copy(kChunks / 32);
+    } else {
+        const int n = (k.len - base + kBlock - 1) / kBlock * (Layout<D>::kBytes / 16);
+#pragma unroll 1
+        for (int i = 0; lane + i * 32 < n; ++i) copy(i);
+    }
 }
 
 template <int D, int R>
@@ -138,6 +144,8 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     using S = Shape4<D, R>;
     using Lay = Layout<D>;
     constexpr int NT = R / 8;              // columns of eight heads
+    constexpr int kBlocks = S::kBlocks;
+    using Keys = Keys4<kBlocks>;
     constexpr int W = D / 32;              // words of a lane's part of a key, or of two values
     constexpr int MT = D / 16;             // sixteens of dims
     extern __shared__ __align__(128) uint8_t smem[];
@@ -146,15 +154,15 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
     const int units = a.Hk * chunks;
 
-    const Line<Keys4> line = lay_line<Keys4>(a, sh, units);
+    const Line<Keys> line = lay_line<Keys>(a, sh, units);
     uint8_t* const ring = smem + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(ring);
     float* const head_part = reinterpret_cast<float*>(smem + S::kWarps * S::kRing + warp * S::kPart);
     const cache4::Ones ones;
 
-    Cursor<Keys4> c;
+    Cursor<Keys> c;
     if (first_unit(a, sh, line, c, units)) {
-        Cursor<Keys4> ahead = c;
+        Cursor<Keys> ahead = c;
         bool more = true;
         int put = 0;
         const uint32_t ring_at = smem_addr(ring) + lane * 16;
