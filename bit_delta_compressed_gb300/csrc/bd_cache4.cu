@@ -21,7 +21,6 @@ using attn::Request;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAtOnce = 4;                      // steps of a block whose loads are under way together
 
 // The rows' side: bf16, heads of a row one after the other.
 struct Rows {
@@ -69,10 +68,13 @@ __device__ __forceinline__ Span seen_span(const Args& a, const Request& r) {
     return s;
 }
 
-// Blocks of the requests before each thread's run of requests.
+// Blocks of the requests before each thread's run of requests; of a call of no more requests
+// than threads the requests themselves.
 struct Items {
     int64_t before[kThreads + 1];
     int64_t warp[kWarps];
+    Span span[kThreads];
+    int slot[kThreads];
     int served;
 };
 
@@ -95,10 +97,12 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scrat
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int run = (a.B + kThreads - 1) / kThreads;
     if (tid == 0) items.served = a.B;
+    Span one;
+    bool in_one = false;                        // what a call of few requests reads in one go
     __syncthreads();
-    if (a.cu_q) {
-        // requests from the first whose offsets do not ascend on are not served
-        for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
+    for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
+        if (a.cu_q) {
+            // requests from the first whose offsets do not ascend on are not served
             const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
             if (lo < 0 || hi < lo || hi > a.T) {
                 atomicMin(&items.served, b);
@@ -106,14 +110,19 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scrat
                 break;
             }
         }
-        __syncthreads();
+        if (run == 1) in_one = span_of<SCRATCH>(a, scratch, b, a.B, one);
     }
+    __syncthreads();
     const int served = items.served;
     int64_t mine = 0;
     for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
-        Span s;
-        const bool in = span_of<SCRATCH>(a, scratch, b, served, s);
+        Span s = one;
+        const bool in = run == 1 ? in_one && b < served : span_of<SCRATCH>(a, scratch, b, served, s);
         if (in) mine += s.n;
+        if (run == 1) {
+            items.span[b] = s;
+            items.slot[b] = a.slots ? a.slots[b] : b;
+        }
         // (a request of no rows has nothing to say; one that is not served says so)
         if (SCRATCH && blockIdx.x == 0) {
             const bool ok = in || (b < served && a.cu_q[b] == a.cu_q[b + 1]);
@@ -135,61 +144,97 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scrat
     return items.before[kThreads];
 }
 
-// The request that holds block i of all, which becomes the block's number within it.
+// The request that holds block i of all, which becomes the block's number within it, and its slot.
 template <bool SCRATCH>
-__device__ __forceinline__ int find(const Args& a, const Scratch& scratch, const Items& items, int64_t& i, Span& s) {
+__device__ __forceinline__ int find(const Args& a, const Scratch& scratch, const Items& items, int64_t& i, Span& s, int& slot) {
     int t = 0;
     for (int step = kThreads / 2; step; step /= 2)
         if (items.before[t + step] <= i) t += step;
     i -= items.before[t];
-    int b = t * ((a.B + kThreads - 1) / kThreads);
-    for (;; ++b) {
+    const int run = (a.B + kThreads - 1) / kThreads;
+    if (run == 1) {
+        s = items.span[t];
+        slot = items.slot[t];
+        return t;
+    }
+    for (int b = t * run;; ++b) {
         if (!span_of<SCRATCH>(a, scratch, b, items.served, s)) continue;
-        if (i < s.n) return b;
+        if (i < s.n) {
+            slot = a.slots ? a.slots[b] : b;
+            return b;
+        }
         i -= s.n;
     }
 }
 
 // ---- values into numbers ---------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t largest(uint32_t m, uint32_t w) { return max(m, max(w & 0x7FFFu, w >> 16 & 0x7FFFu)); }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 
-// A group's scale as its byte, from the bits of the largest |x| (bf16).
+// The bits of the largest |x| (bf16) of a group, whose 32 values lie on four lanes.
+__device__ __forceinline__ uint32_t largest(const uint4& x) {
+    uint32_t m = max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+// A group's scale as its byte, from the bits of the largest |x| (bf16).  The quotient by 7 is a product with
+// 1 / 7, off by 2^-23 of itself, rounded to 12 bits, which a tie between two scales (5 bits; 7 times it has 8) is
+// itself and other quotients are 2^-9 or more from, and then to the scale's 4, ties to even.
 __device__ __forceinline__ uint32_t scale_code(uint32_t top) {
     if (top >= 0x7F80u) return kNanScale;
-    const float want = __fdiv_rn(__uint_as_float(top << 16), 7.f);
-    if (want < 6.103515625e-5f) return (uint32_t)__float2int_rn(want * 131072.f);   // below 2^-14: units of 2^-17
-    const uint32_t bits = __float_as_uint(want);
-    const uint32_t code = ((bits + 0x7FFFFu + (bits >> 20 & 1u)) >> 20) - (112u << 3);
-    return min(code, kTopScale);
+    const uint32_t bits = (__float_as_uint(__uint_as_float(top << 16) * (1.f / 7.f)) + 0x400u) & ~0x7FFu;
+    if (bits < 0x38800000u) return (uint32_t)__float2int_rn(__uint_as_float(bits) * 131072.f);      // below 2^-14: units of 2^-17
+    return min(((bits + 0x7FFFFu + (bits >> 20 & 1u)) >> 20) - (112u << 3), kTopScale);
 }
 
-// Eight values as n + 8.  x / s is taken as a product with 1 / s, off by 2^-23 of itself; then
-// to the nearest multiple of 2^-10 (that many of 1.5 2^13's last places), which
-// a tie x = (n + 1/2) s is itself, and to whole numbers.  Other x lie 2^-9 or more from a tie (8 bits of
-// x against 4 of s), so this is the exact quotient's rounding, ties to even.
-__device__ __forceinline__ void numbers(const uint4& x, uint32_t code, uint32_t (&n)[8]) {
-    const float s = __half2float(__ushort_as_half((unsigned short)(code << 7)));
-    const float inv = code ? __frcp_rn(s) : 0.f;
+__device__ __forceinline__ float scale_value(uint32_t code) { return __half2float(__ushort_as_half((unsigned short)(code << 7))); }
+
+// 1 / s, off by 2^-23 of itself; 0 for 0.
+__device__ __forceinline__ float inverse_scale(uint32_t code) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale_value(code)));
+    return code ? r : 0.f;
+}
+
+// Eight values as n + 8, two fields of a unit each: (n0 + 8) 2^6 + (n1 + 8) 2^2 in the low bits.  x / s is a product with 1 /
+// s, off by 2^-23 of itself, to the nearest multiple of 2^-10 (that many of 1.5 2^13's last places), which
+// a tie x = (n + 1/2) s is itself, and then to whole numbers.  Other x lie 2^-9 or more from a tie (8 bits of
+// x against 4 of s), so this is the exact quotient's rounding, ties to even.  Only quotients by the largest scale, and by
+// those below 2^-14, which have fewer bits, can lie outside [-7.5, 7.5].
+// (All in f32, at twice the rate of shifts and of minima; prompts of 9,525 tokens 21.4 -> 18.2 us, with the scales found once.)
+__device__ __forceinline__ void fields(const uint4& x, uint32_t code, float inv, uint32_t (&pairs)[4], const int (&order)[8]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float v = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
-        const float y = fminf(fmaxf(v * inv, -7.f), 7.f) + 12288.f;
-        n[i] = __float_as_uint(y + 12570632.f) & 15u;      // 1.5 2^23 - 12288 + 8
+    for (int i = 0; i < 8; ++i) y[i] = i % 2 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    if (code >= kTopScale || code < 8) {
+        const float s = scale_value(code);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = fminf(fmaxf(y[i], -7.f * s), 7.f * s);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = (fmaf(y[i], inv, 12288.f) + 12570632.f) - 12582912.f;     // 1.5 2^23 - 12288 + 8
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pairs[i] = __float_as_uint(fmaf(y[order[2 * i]], 64.f, fmaf(y[order[2 * i + 1]], 4.f, 8388608.f)));
 }
 
-// Four of them as a unit; a group that is not finite holds zeros beside its scale.
-__device__ __forceinline__ uint32_t unit(uint32_t code, uint32_t n0, uint32_t n1, uint32_t n2, uint32_t n3) {
-    return code == kNanScale ? 0x2222u : n0 << 6 | n1 << 2 | n2 >> 2 | (n2 & 3u) << 14 | n3 << 10;
+// A word of two units: their first two fields, and the other two with swapped bytes.
+__device__ __forceinline__ uint32_t word_of(uint32_t first0, uint32_t last0, uint32_t first1, uint32_t last1) {
+    return __byte_perm(first0, first1, 0x5410) | __byte_perm(last0, last1, 0x4501);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) write_kernel(const Args a, const Cache c, const Rows rows) {
+__global__ void __launch_bounds__(kThreads, 2) write_kernel(const Args a, const Cache c, const Rows rows) {
     using Lay = Layout<D>;
     constexpr int L = D / 8;                    // lanes of a row
     constexpr int R = 32 / L;                   // rows of a step
+    constexpr int kSteps = kBlock / R;
     __shared__ Items items;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
     const Scratch none{};
@@ -198,54 +243,53 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const Args a, const Cac
         int64_t i = at / a.Hk;
         const int h = (int)(at - i * a.Hk);
         Span s;
-        const int b = find<false>(a, none, items, i, s);
+        int slot;
+        find<false>(a, none, items, i, s, slot);
         const int block = s.from + (int)i, t0 = block * kBlock;
-        const int slot = a.slots ? a.slots[b] : b;
         uint8_t* const to = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);      // tokens of the block
         const int64_t row0 = (int64_t)s.row0 - s.first + t0;
-        for (int step = lo / R; step * R < hi; step += kAtOnce) {
-            uint4 k[kAtOnce], v[kAtOnce];
+        uint4 k[kSteps], v[kSteps];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int j = (step + u) * R + lane / L;
-                k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (j < lo || j >= hi) continue;
-                k[u] = *reinterpret_cast<const uint4*>(rows.k + (row0 + j) * rows.k_stride + h * D + col * 8);
-                v[u] = *reinterpret_cast<const uint4*>(rows.v + (row0 + j) * rows.v_stride + h * D + col * 8);
+        for (int u = 0; u < kSteps; ++u) {
+            const int j = u * R + lane / L;
+            k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (j < lo || j >= hi) continue;
+            k[u] = *reinterpret_cast<const uint4*>(rows.k + (row0 + j) * rows.k_stride + h * D + col * 8);
+            v[u] = *reinterpret_cast<const uint4*>(rows.v + (row0 + j) * rows.v_stride + h * D + col * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            if ((u + 1) * R <= lo || u * R >= hi) continue;
+            const int j = u * R + lane / L;
+            // a group's even lanes find the keys' scale, its odd ones the values'
+            const uint32_t top_k = largest(k[u]), top_v = largest(v[u]);
+            const uint32_t code = scale_code(lane % 2 ? top_v : top_k);
+            const float inv = inverse_scale(code);
+            const uint32_t code_k = __shfl_sync(0xffffffffu, code, lane & ~1), code_v = __shfl_sync(0xffffffffu, code, lane | 1);
+            const float inv_k = __shfl_sync(0xffffffffu, inv, lane & ~1), inv_v = __shfl_sync(0xffffffffu, inv, lane | 1);
+            const bool in = j >= lo && j < hi, other = (j ^ 1) >= lo && (j ^ 1) < hi;
+            uint32_t n[4];
+            constexpr int by_twos[8] = {0, 2, 4, 6, 1, 3, 5, 7}, in_order[8] = {0, 1, 2, 3, 4, 5, 6, 7};
+            fields(k[u], code_k, inv_k, n, by_twos);
+            if (in) {
+                // a group that is not finite holds zeros beside its scale
+                *reinterpret_cast<uint32_t*>(to + j * (D / 2) + col * 4) = code_k == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
+                if (col % 4 == 0) {
+                    to[Lay::kScaleK + j * (D / 32) + col / 4] = (uint8_t)code_k;
+                    to[Lay::kScaleV + col / 4 * kBlock + j] = (uint8_t)code_v;
+                }
             }
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                if ((step + u) * R >= hi) break;
-                const int j = (step + u) * R + lane / L;
-                uint32_t top = 0, codes[2], n[8];
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const uint4& x = w ? v[u] : k[u];
-                    top = largest(largest(largest(largest(0u, x.x), x.y), x.z), x.w);
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    codes[w] = scale_code(top);
-                }
-                const bool in = j >= lo && j < hi, other = (j ^ 1) >= lo && (j ^ 1) < hi;
-                numbers(k[u], codes[0], n);
-                if (in) {
-                    *reinterpret_cast<uint32_t*>(to + j * (D / 2) + col * 4) = unit(codes[0], n[0], n[2], n[4], n[6]) | unit(codes[0], n[1], n[3], n[5], n[7]) << 16;
-                    if (col % 4 == 0) {
-                        to[Lay::kScaleK + j * (D / 32) + col / 4] = (uint8_t)codes[0];
-                        to[Lay::kScaleV + col / 4 * kBlock + j] = (uint8_t)codes[1];
-                    }
-                }
-                numbers(v[u], codes[1], n);
-                const uint32_t first = unit(codes[1], n[0], n[1], n[2], n[3]), second = unit(codes[1], n[4], n[5], n[6], n[7]);
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, j % 2 ? first : second, L);
-                uint8_t* const pair = to + Lay::kV + j / 2 * D + col * 8;
-                if (in && other) {
-                    *reinterpret_cast<uint32_t*>(pair + j % 2 * 4) = j % 2 ? got | second << 16 : first | got << 16;
-                } else if (in) {
-                    *reinterpret_cast<uint16_t*>(pair + j % 2 * 2) = (uint16_t)first;
-                    *reinterpret_cast<uint16_t*>(pair + j % 2 * 2 + 4) = (uint16_t)second;
-                }
+            fields(v[u], code_v, inv_v, n, in_order);
+            // this token's two units, the first in the low half; of the word that both tokens share the other lane has one
+            const uint32_t both = code_v == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, both, L);
+            uint8_t* const pair = to + Lay::kV + j / 2 * D + col * 8;
+            if (in && other) {
+                *reinterpret_cast<uint32_t*>(pair + j % 2 * 4) = j % 2 ? __byte_perm(got, both, 0x7632) : __byte_perm(both, got, 0x5410);
+            } else if (in) {
+                *reinterpret_cast<uint16_t*>(pair + j % 2 * 2) = (uint16_t)both;
+                *reinterpret_cast<uint16_t*>(pair + j % 2 * 2 + 4) = (uint16_t)(both >> 16);
             }
         }
     }
@@ -261,7 +305,7 @@ __device__ __forceinline__ uint32_t to_bf16(uint32_t h2) {
 template <int D, bool SCRATCH>
 __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cache c, const Rows rows, const Scratch scratch) {
     using Lay = Layout<D>;
-    constexpr int L = D / 8, R = 32 / L;
+    constexpr int L = D / 8, R = 32 / L, kSteps = kBlock / R;
     __shared__ Items items;
     const Ones ones;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
@@ -270,9 +314,9 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
         int64_t i = at / a.Hk;
         const int h = (int)(at - i * a.Hk);
         Span s;
-        const int b = find<SCRATCH>(a, scratch, items, i, s);
+        int slot;
+        const int b = find<SCRATCH>(a, scratch, items, i, s, slot);
         const int block = (i < s.head ? 0 : s.from - s.head) + (int)i, t0 = block * kBlock;
-        const int slot = a.slots ? a.slots[b] : b;
         const uint8_t* const from = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);
         __nv_bfloat16 *k_to, *v_to;
@@ -289,38 +333,36 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
             k_next = rows.k_stride;
             v_next = rows.v_stride;
         }
-        for (int step = lo / R; step * R < hi; step += kAtOnce) {
-            uint32_t k[kAtOnce], codes[kAtOnce];
-            uint2 v[kAtOnce];
+        uint32_t k[kSteps], codes[kSteps];
+        uint2 v[kSteps];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int j = (step + u) * R + lane / L;
-                if (j < lo || j >= hi) continue;
-                k[u] = *reinterpret_cast<const uint32_t*>(from + j * (D / 2) + col * 4);
-                v[u] = *reinterpret_cast<const uint2*>(from + Lay::kV + j / 2 * D + col * 8);
-                codes[u] = from[Lay::kScaleK + j * (D / 32) + col / 4] | from[Lay::kScaleV + col / 4 * kBlock + j] << 8;
-            }
+        for (int u = 0; u < kSteps; ++u) {
+            const int j = u * R + lane / L;
+            if (j < lo || j >= hi) continue;
+            k[u] = *reinterpret_cast<const uint32_t*>(from + j * (D / 2) + col * 4);
+            v[u] = *reinterpret_cast<const uint2*>(from + Lay::kV + j / 2 * D + col * 8);
+            codes[u] = from[Lay::kScaleK + j * (D / 32) + col / 4] | from[Lay::kScaleV + col / 4 * kBlock + j] << 8;
+        }
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                const int j = (step + u) * R + lane / L;
-                if (j < lo || j >= hi) continue;
-                const Scales sk = scale_of(codes[u] & 255u), sv = scale_of(codes[u] >> 8);
-                uint32_t w = k[u], x = swap_bytes(w);
-                *reinterpret_cast<uint4*>(k_to + j * k_next + col * 8) =
-                    make_uint4(to_bf16(field0(w, sk, ones)), to_bf16(field1(w, sk, ones)), to_bf16(field0(x, sk, ones)), to_bf16(field1(x, sk, ones)));
-                w = __byte_perm(v[u].x, v[u].y, j % 2 ? 0x7632 : 0x5410);       // this token's two units
-                x = swap_bytes(w);
-                const uint32_t f0 = to_bf16(field0(w, sv, ones)), f1 = to_bf16(field1(w, sv, ones)), f2 = to_bf16(field0(x, sv, ones)), f3 = to_bf16(field1(x, sv, ones));
-                *reinterpret_cast<uint4*>(v_to + j * v_next + col * 8) =
-                    make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
-            }
+        for (int u = 0; u < kSteps; ++u) {
+            const int j = u * R + lane / L;
+            if (j < lo || j >= hi) continue;
+            const Scales sk = scale_of(codes[u] & 255u), sv = scale_of(codes[u] >> 8);
+            uint32_t w = k[u], x = swap_bytes(w);
+            *reinterpret_cast<uint4*>(k_to + j * k_next + col * 8) =
+                make_uint4(to_bf16(field0(w, sk, ones)), to_bf16(field1(w, sk, ones)), to_bf16(field0(x, sk, ones)), to_bf16(field1(x, sk, ones)));
+            w = __byte_perm(v[u].x, v[u].y, j % 2 ? 0x7632 : 0x5410);       // this token's two units
+            x = swap_bytes(w);
+            const uint32_t f0 = to_bf16(field0(w, sv, ones)), f1 = to_bf16(field1(w, sv, ones)), f2 = to_bf16(field0(x, sv, ones)), f3 = to_bf16(field1(x, sv, ones));
+            *reinterpret_cast<uint4*>(v_to + j * v_next + col * 8) =
+                make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
         }
     }
 }
 
-// Thread blocks for at most `blocks` cache blocks.
-unsigned grid_for(int64_t blocks, int heads) {
-    const int64_t want = (blocks * heads + kWarps - 1) / kWarps, most = 8 * (int64_t)sm_count();
+// Thread blocks for at most `blocks` cache blocks, up to `each` a SM.
+unsigned grid_for(int64_t blocks, int heads, int each) {
+    const int64_t want = (blocks * heads + kWarps - 1) / kWarps, most = each * (int64_t)sm_count();
     return (unsigned)(want < most ? (want < 1 ? 1 : want) : most);
 }
 
@@ -342,7 +384,7 @@ bd_status rows_call(bool write, void* k, int64_t k_stride, void* v, int64_t v_st
     const Args a = args_of(cache, T, B, slots, cu_q, lens, workspace);
     const Cache c = kernel_cache(cache);
     const Rows rows{static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride};
-    const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads);
+    const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads, write ? 2 : 8);
     const Scratch none{};
     if (write) {
         if (cache->head_dim == 128) write_kernel<128><<<grid, kThreads, 0, stream>>>(a, c, rows);
@@ -386,7 +428,7 @@ Cache kernel_cache(const bd_kv_cache4* c) { return Cache{static_cast<uint8_t*>(c
 
 bd_status launch_seen(const Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, int32_t* lens, cudaStream_t stream) {
     const Scratch scratch{k, v, length, lens};
-    const unsigned grid = grid_for((int64_t)a.B * (length / kBlock + 1), a.Hk);
+    const unsigned grid = grid_for((int64_t)a.B * (length / kBlock + 1), a.Hk, 8);
     const Rows none{};
     if (head_dim == 128) read_kernel<128, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
     else read_kernel<64, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
