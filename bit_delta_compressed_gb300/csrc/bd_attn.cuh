@@ -24,6 +24,7 @@ struct Args {
     const int32_t *slots, *lens, *cu_q; // cu_q NULL: one row a request
     const int32_t *prefix_ids, *prefix_slots, *prefix_lens;
     int32_t P;
+    int32_t stands_in;                  // whether k, v hold request b's keys in slot b, in the cache's stead
     int32_t window, sinks;
     float scale_log2;                   // scale * log2(e): scores are kept as powers of two
     float* weights;
@@ -67,6 +68,7 @@ __device__ __forceinline__ Request read_request(const Args& a, int b) {
         r.slot = r.pslot = 0;
         r.len = r.plen = 0;
     }
+    if (a.stands_in) r.slot = b;
     return r;
 }
 

@@ -18,7 +18,6 @@ namespace {
 struct Workspace4 {
     Workspace w;
     __nv_bfloat16 *k, *v;
-    int32_t* lens;
     int64_t length;                        // keys of a request that there is room for
     size_t total;
 };
@@ -38,7 +37,6 @@ Workspace4 layout4(void* base, int64_t tokens, int64_t batch, int32_t q_heads, i
         const size_t bytes = (size_t)batch * (size_t)kv_heads * (size_t)r.length * (size_t)head_dim * sizeof(__nv_bfloat16);
         r.k = reinterpret_cast<__nv_bfloat16*>(take(bytes));
         r.v = reinterpret_cast<__nv_bfloat16*>(take(bytes));
-        r.lens = reinterpret_cast<int32_t*>(take((size_t)batch * sizeof(int32_t)));
     }
     r.total = at;
     return r;
@@ -71,9 +69,14 @@ bd_status attention4(const void* q, int64_t q_stride, int64_t T, int64_t B, int3
     const cache4::Cache cache = cache4::kernel_cache(c);
     const Workspace4 w = layout4(workspace, T, B, q_heads, c->kv_heads, c->head_dim, longest);
     if (!cu_q) return launch_decode4(a, cache, c->head_dim, w.w.decode, stream);
-    st = cache4::launch_seen(a, cache, c->head_dim, w.k, w.v, w.length, w.lens, stream);
+    // the plan (one block) and the reading beside it go by the cache's slots and lengths, the
+    // tiles by the plan: request b's keys lie in slot b of what was read back
+    a.stands_in = 1;
+    if (longest < a.capacity) a.capacity = (int32_t)longest;
+    st = launch_plan(a, w.w.plan, stream);
     if (st != BD_OK) return st;
-    // from here on the cache is what was read back: request b in slot b
+    st = cache4::launch_seen(a, cache, c->head_dim, w.k, w.v, w.length, stream);
+    if (st != BD_OK) return st;
     a.k = w.k;
     a.v = w.v;
     a.st = c->head_dim;
@@ -81,9 +84,7 @@ bd_status attention4(const void* q, int64_t q_stride, int64_t T, int64_t B, int3
     a.ss = a.Hk * a.sh;
     a.n_slots = a.B;
     a.capacity = (int32_t)w.length;
-    a.slots = nullptr;
-    a.lens = w.lens;
-    return launch_prefill(a, c->head_dim, w.w.plan, stream);
+    return launch_tiles(a, c->head_dim, w.w.plan, stream);
 }
 
 }  // namespace

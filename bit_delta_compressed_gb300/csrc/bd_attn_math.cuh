@@ -183,7 +183,8 @@ Workspace layout(void* base, int64_t tokens, int64_t batch, int32_t q_heads, int
 int tile_blocks();
 int64_t split_below();       // units from which on a prefill is not split
 int64_t most_tiles(int64_t tokens, int64_t batch, int G);
-bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
+bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);   // plan and tiles
+bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream);
 bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream);
 bd_status launch_prefixes(const Args& a, int head_dim, const TilePlan& plan, const DecodeBuffers& buf, cudaStream_t stream);
 

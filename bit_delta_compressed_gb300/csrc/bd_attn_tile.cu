@@ -1107,9 +1107,12 @@ bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream) 
 }
 
 bd_status launch_prefill(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
-    bd_status st = launch_plan(a, plan, stream);
-    if (st != BD_OK) return st;
-    st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
+    const bd_status st = launch_plan(a, plan, stream);
+    return st == BD_OK ? launch_tiles(a, head_dim, plan, stream) : st;
+}
+
+bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaStream_t stream) {
+    const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
     if (st != BD_OK || !may_split(a)) return st;
     // (few units are joined by many blocks each)
     const int64_t units = most_tiles(a.T, a.B, a.G) * a.Hk, each = 8 * (int64_t)tile_blocks() / units;

@@ -28,12 +28,10 @@ struct Rows {
     int64_t k_stride, v_stride;
 };
 
-// The attention's scratch for prompts: keys in their places, [B, kv_heads, length, D] bf16, and
-// the requests' lengths as the attention is to see them (-1: not a request).
+// The attention's scratch for prompts: keys in their places, [B, kv_heads, length, D] bf16.
 struct Scratch {
     __nv_bfloat16 *k, *v;
     int64_t length;
-    int32_t* lens;
 };
 
 // Which blocks of a request a call touches: `head` from the first on, and those from
@@ -80,11 +78,11 @@ struct Items {
 
 // Request b as this call sees it; false if nothing of it is touched.
 template <bool SCRATCH>
-__device__ __forceinline__ bool span_of(const Args& a, const Scratch& scratch, int b, int served, Span& s) {
+__device__ __forceinline__ bool span_of(const Args& a, int b, int served, Span& s) {
     if (b >= served) return false;
     const Request r = attn::read_request(a, b);
     if (r.rows == 0) return false;
-    if (r.len < r.rows || (SCRATCH && r.len > scratch.length)) {   // (one that is out of range has no length)
+    if (r.len < r.rows) {   // (one that is out of range has no length)
         report(a.status, BD_ERR_SLOT);
         return false;
     }
@@ -93,7 +91,7 @@ __device__ __forceinline__ bool span_of(const Args& a, const Scratch& scratch, i
 }
 
 template <bool SCRATCH>
-__device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scratch, Items& items) {
+__device__ __forceinline__ int64_t lay_items(const Args& a, Items& items) {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int run = (a.B + kThreads - 1) / kThreads;
     if (tid == 0) items.served = a.B;
@@ -110,23 +108,18 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scrat
                 break;
             }
         }
-        if (run == 1) in_one = span_of<SCRATCH>(a, scratch, b, a.B, one);
+        if (run == 1) in_one = span_of<SCRATCH>(a, b, a.B, one);
     }
     __syncthreads();
     const int served = items.served;
     int64_t mine = 0;
     for (int b = tid * run; b < min(a.B, (tid + 1) * run); ++b) {
         Span s = one;
-        const bool in = run == 1 ? in_one && b < served : span_of<SCRATCH>(a, scratch, b, served, s);
+        const bool in = run == 1 ? in_one && b < served : span_of<SCRATCH>(a, b, served, s);
         if (in) mine += s.n;
         if (run == 1) {
             items.span[b] = s;
             items.slot[b] = a.slots ? a.slots[b] : b;
-        }
-        // (a request of no rows has nothing to say; one that is not served says so)
-        if (SCRATCH && blockIdx.x == 0) {
-            const bool ok = in || (b < served && a.cu_q[b] == a.cu_q[b + 1]);
-            scratch.lens[b] = ok ? min(max(a.lens[b], 0), (int)scratch.length) : -1;
         }
     }
     int64_t incl = mine;
@@ -146,7 +139,7 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, const Scratch& scrat
 
 // The request that holds block i of all, which becomes the block's number within it, and its slot.
 template <bool SCRATCH>
-__device__ __forceinline__ int find(const Args& a, const Scratch& scratch, const Items& items, int64_t& i, Span& s, int& slot) {
+__device__ __forceinline__ int find(const Args& a, const Items& items, int64_t& i, Span& s, int& slot) {
     int t = 0;
     for (int step = kThreads / 2; step; step /= 2)
         if (items.before[t + step] <= i) t += step;
@@ -158,7 +151,7 @@ __device__ __forceinline__ int find(const Args& a, const Scratch& scratch, const
         return t;
     }
     for (int b = t * run;; ++b) {
-        if (!span_of<SCRATCH>(a, scratch, b, items.served, s)) continue;
+        if (!span_of<SCRATCH>(a, b, items.served, s)) continue;
         if (i < s.n) {
             slot = a.slots ? a.slots[b] : b;
             return b;
@@ -237,14 +230,13 @@ __global__ void __launch_bounds__(kThreads, 2) write_kernel(const Args a, const 
     constexpr int kSteps = kBlock / R;
     __shared__ Items items;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
-    const Scratch none{};
-    const int64_t total = lay_items<false>(a, none, items) * a.Hk;
+    const int64_t total = lay_items<false>(a, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
         int64_t i = at / a.Hk;
         const int h = (int)(at - i * a.Hk);
         Span s;
         int slot;
-        find<false>(a, none, items, i, s, slot);
+        find<false>(a, items, i, s, slot);
         const int block = s.from + (int)i, t0 = block * kBlock;
         uint8_t* const to = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);      // tokens of the block
@@ -307,15 +299,16 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
     using Lay = Layout<D>;
     constexpr int L = D / 8, R = 32 / L, kSteps = kBlock / R;
     __shared__ Items items;
+    if (SCRATCH) attn::grid_go_on();
     const Ones ones;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
-    const int64_t total = lay_items<SCRATCH>(a, scratch, items) * a.Hk;
+    const int64_t total = lay_items<SCRATCH>(a, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
         int64_t i = at / a.Hk;
         const int h = (int)(at - i * a.Hk);
         Span s;
         int slot;
-        const int b = find<SCRATCH>(a, scratch, items, i, s, slot);
+        const int b = find<SCRATCH>(a, items, i, s, slot);
         const int block = (i < s.head ? 0 : s.from - s.head) + (int)i, t0 = block * kBlock;
         const uint8_t* const from = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);
@@ -358,6 +351,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
                 make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
         }
     }
+    if (SCRATCH) attn::grid_wait();                // the plan, for those that wait for this
 }
 
 // Thread blocks for at most `blocks` cache blocks, up to `each` a SM.
@@ -426,13 +420,12 @@ attn::Args args_of(const bd_kv_cache4* cache, int64_t T, int64_t B, const int32_
 
 Cache kernel_cache(const bd_kv_cache4* c) { return Cache{static_cast<uint8_t*>(c->data), c->stride_slot, c->stride_head}; }
 
-bd_status launch_seen(const Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, int32_t* lens, cudaStream_t stream) {
-    const Scratch scratch{k, v, length, lens};
+bd_status launch_seen(const Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, cudaStream_t stream) {
+    const Scratch scratch{k, v, length};
     const unsigned grid = grid_for((int64_t)a.B * (length / kBlock + 1), a.Hk, 8);
     const Rows none{};
-    if (head_dim == 128) read_kernel<128, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
-    else read_kernel<64, true><<<grid, kThreads, 0, stream>>>(a, c, none, scratch);
-    return launch_status();
+    return head_dim == 128 ? attn::launch_close(read_kernel<128, true>, grid, kThreads, 0, stream, a, c, none, scratch)
+                           : attn::launch_close(read_kernel<64, true>, grid, kThreads, 0, stream, a, c, none, scratch);
 }
 
 }  // namespace cache4

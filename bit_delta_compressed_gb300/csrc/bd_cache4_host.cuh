@@ -16,9 +16,8 @@ attn::Args args_of(const bd_kv_cache4* cache, int64_t T, int64_t B, const int32_
 Cache kernel_cache(const bd_kv_cache4* c);
 
 // Reads what the queries of a prompt call see back to bf16, [B, Hk, length, head_dim], keys in
-// their places, and writes the requests' lengths (-1: no request, or longer than `length`).
-bd_status launch_seen(const attn::Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, int32_t* lens,
-                      cudaStream_t stream);
+// their places.  It runs beside the launch before it, and ends after that.
+bd_status launch_seen(const attn::Args& a, const Cache& c, int head_dim, __nv_bfloat16* k, __nv_bfloat16* v, int64_t length, cudaStream_t stream);
 
 }  // namespace cache4
 }  // namespace bd
