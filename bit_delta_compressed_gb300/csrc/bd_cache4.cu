@@ -8,6 +8,8 @@
 // whole words are written wherever both tokens are.
 #include <math.h>
 
+#include <type_traits>
+
 #include "bd_attn_math.cuh"
 #include "bd_cache4.cuh"
 #include "bd_cache4_host.cuh"
@@ -168,12 +170,16 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// The bits of the largest |x| (bf16) of a group, whose 32 values lie on four lanes.
-__device__ __forceinline__ uint32_t largest(const uint4& x) {
-    uint32_t m = max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+// The bits of the largest |x| (bf16) of a group of keys, and of values in the upper half; a
+// group's 32 values lie on four lanes.
+__device__ __forceinline__ uint32_t largest(const uint4& k, const uint4& v) {
+    auto four = [](const uint4& x) {
+        return max_u16x2(max_u16x2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), max_u16x2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+    };
+    const uint32_t a = four(k), b = four(v);
+    uint32_t m = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    return max(m & 0xFFFFu, m >> 16);
+    return max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
 }
 
 // A group's scale as its byte, from the bits of the largest |x| (bf16).  The quotient by 7 is a product with
@@ -223,12 +229,13 @@ __device__ __forceinline__ uint32_t word_of(uint32_t first0, uint32_t last0, uin
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2) write_kernel(const Args a, const Cache c, const Rows rows) {
+__global__ void __launch_bounds__(kThreads, 4) write_kernel(const Args a, const Cache c, const Rows rows) {
     using Lay = Layout<D>;
     constexpr int L = D / 8;                    // lanes of a row
     constexpr int R = 32 / L;                   // rows of a step
-    constexpr int kSteps = kBlock / R;
+    constexpr int kHalf = kBlock / R / 2;       // steps of half a block
     __shared__ Items items;
+    __shared__ __align__(4) uint8_t codes[kWarps][D];
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
     const int64_t total = lay_items<false>(a, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
@@ -241,49 +248,82 @@ __global__ void __launch_bounds__(kThreads, 2) write_kernel(const Args a, const 
         uint8_t* const to = c.data + slot * c.ss + h * c.sh + (int64_t)block * Lay::kBytes;
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);      // tokens of the block
         const int64_t row0 = (int64_t)s.row0 - s.first + t0;
-        uint4 k[kSteps], v[kSteps];
+        const int row = lane / L;
+        const __nv_bfloat16 *k_from = rows.k + (row0 + row) * rows.k_stride + h * D + col * 8, *v_from = rows.v + (row0 + row) * rows.v_stride + h * D + col * 8;
+        uint8_t* const k_to = to + row * (D / 2) + col * 4;
+        uint8_t* const v_to = to + Lay::kV + row / 2 * D + col * 8;
+        uint8_t* const code_to = codes[tid / 32] + (col % 4 ? 0 : row * (D / 32) + col / 4);
+        // half a block from step u0 on; of one that is not WHOLE some tokens are none of the call's
+        auto half = [&](auto all, int u0) {
+            constexpr bool WHOLE = decltype(all)::value;
+            uint4 k[kHalf], v[kHalf];
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            const int j = u * R + lane / L;
-            k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (j < lo || j >= hi) continue;
-            k[u] = *reinterpret_cast<const uint4*>(rows.k + (row0 + j) * rows.k_stride + h * D + col * 8);
-            v[u] = *reinterpret_cast<const uint4*>(rows.v + (row0 + j) * rows.v_stride + h * D + col * 8);
-        }
+            for (int u = 0; u < kHalf; ++u) {
+                const int j = (u0 + u) * R + row;
+                if (!WHOLE) k[u] = v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (!WHOLE && (j < lo || j >= hi)) continue;
+                k[u] = *reinterpret_cast<const uint4*>(k_from + (u0 + u) * R * rows.k_stride);
+                v[u] = *reinterpret_cast<const uint4*>(v_from + (u0 + u) * R * rows.v_stride);
+            }
 #pragma unroll
-        for (int u = 0; u < kSteps; ++u) {
-            if ((u + 1) * R <= lo || u * R >= hi) continue;
-            const int j = u * R + lane / L;
-            // a group's even lanes find the keys' scale, its odd ones the values'
-            const uint32_t top_k = largest(k[u]), top_v = largest(v[u]);
-            const uint32_t code = scale_code(lane % 2 ? top_v : top_k);
-            const float inv = inverse_scale(code);
-            const uint32_t code_k = __shfl_sync(0xffffffffu, code, lane & ~1), code_v = __shfl_sync(0xffffffffu, code, lane | 1);
-            const float inv_k = __shfl_sync(0xffffffffu, inv, lane & ~1), inv_v = __shfl_sync(0xffffffffu, inv, lane | 1);
-            const bool in = j >= lo && j < hi, other = (j ^ 1) >= lo && (j ^ 1) < hi;
-            uint32_t n[4];
-            constexpr int by_twos[8] = {0, 2, 4, 6, 1, 3, 5, 7}, in_order[8] = {0, 1, 2, 3, 4, 5, 6, 7};
-            fields(k[u], code_k, inv_k, n, by_twos);
-            if (in) {
-                // a group that is not finite holds zeros beside its scale
-                *reinterpret_cast<uint32_t*>(to + j * (D / 2) + col * 4) = code_k == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
-                if (col % 4 == 0) {
-                    to[Lay::kScaleK + j * (D / 32) + col / 4] = (uint8_t)code_k;
-                    to[Lay::kScaleV + col / 4 * kBlock + j] = (uint8_t)code_v;
+            for (int u = 0; u < kHalf; ++u) {
+                if (!WHOLE && ((u0 + u + 1) * R <= lo || (u0 + u) * R >= hi)) continue;
+                const int j = (u0 + u) * R + row;
+                // a group's even lanes find the keys' scale, its odd ones the values'
+                const uint32_t top = largest(k[u], v[u]), code = scale_code(lane % 2 ? top >> 16 : top & 0xFFFFu);
+                const float inv = inverse_scale(code);
+                const uint32_t code_k = __shfl_sync(0xffffffffu, code, lane & ~1), code_v = __shfl_sync(0xffffffffu, code, lane | 1);
+                const float inv_k = __shfl_sync(0xffffffffu, inv, lane & ~1), inv_v = __shfl_sync(0xffffffffu, inv, lane | 1);
+                const bool in = WHOLE || (j >= lo && j < hi), other = WHOLE || ((j ^ 1) >= lo && (j ^ 1) < hi);
+                uint32_t n[4];
+                constexpr int by_twos[8] = {0, 2, 4, 6, 1, 3, 5, 7}, in_order[8] = {0, 1, 2, 3, 4, 5, 6, 7};
+                fields(k[u], code_k, inv_k, n, by_twos);
+                if (in) {
+                    // a group that is not finite holds zeros beside its scale
+                    *reinterpret_cast<uint32_t*>(k_to + (u0 + u) * (R * D / 2)) = code_k == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
+                    if (col % 4 == 0) {
+                        code_to[(u0 + u) * (R * D / 32)] = (uint8_t)code_k;
+                        codes[tid / 32][D / 2 + col / 4 * kBlock + j] = (uint8_t)code_v;
+                    }
+                }
+                fields(v[u], code_v, inv_v, n, in_order);
+                // this token's two units, the first in the low half; of the word that both tokens share the other lane has one
+                const uint32_t both = code_v == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, both, L);
+                uint8_t* const pair = v_to + (u0 + u) * (R * D / 2);
+                if (in && other) {
+                    *reinterpret_cast<uint32_t*>(pair + row % 2 * 4) = __byte_perm(both, got, row % 2 ? 0x3276 : 0x5410);
+                } else if (in) {
+                    *reinterpret_cast<uint16_t*>(pair + row % 2 * 2) = (uint16_t)both;
+                    *reinterpret_cast<uint16_t*>(pair + row % 2 * 2 + 4) = (uint16_t)(both >> 16);
                 }
             }
-            fields(v[u], code_v, inv_v, n, in_order);
-            // this token's two units, the first in the low half; of the word that both tokens share the other lane has one
-            const uint32_t both = code_v == kNanScale ? 0x22222222u : word_of(n[0], n[1], n[2], n[3]);
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, both, L);
-            uint8_t* const pair = to + Lay::kV + j / 2 * D + col * 8;
-            if (in && other) {
-                *reinterpret_cast<uint32_t*>(pair + j % 2 * 4) = j % 2 ? __byte_perm(got, both, 0x7632) : __byte_perm(both, got, 0x5410);
-            } else if (in) {
-                *reinterpret_cast<uint16_t*>(pair + j % 2 * 2) = (uint16_t)both;
-                *reinterpret_cast<uint16_t*>(pair + j % 2 * 2 + 4) = (uint16_t)(both >> 16);
+        };
+#pragma unroll 1
+        for (int u0 = lo / R / kHalf * kHalf; u0 * R < hi; u0 += kHalf) {
+            if (u0 * R >= lo && (u0 + kHalf) * R <= hi) half(std::true_type(), u0);
+            else half(std::false_type(), u0);
+        }
+        // the scales as they lie, four bytes a lane
+        __syncwarp();
+        if (lane * 4 < D) {
+            bool all = true, seen[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int at = lane * 4 + y, j = at < D / 2 ? at / (D / 32) : at % kBlock;
+                seen[y] = j >= lo && j < hi;
+                all = all && seen[y];
+            }
+            uint8_t* const scales = to + Lay::kScaleK + lane * 4;
+            if (all) {
+                *reinterpret_cast<uint32_t*>(scales) = *reinterpret_cast<const uint32_t*>(&codes[tid / 32][lane * 4]);
+            } else {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (seen[y]) scales[y] = codes[tid / 32][lane * 4 + y];
             }
         }
+        __syncwarp();
     }
 }
 
@@ -378,7 +418,7 @@ bd_status rows_call(bool write, void* k, int64_t k_stride, void* v, int64_t v_st
     const Args a = args_of(cache, T, B, slots, cu_q, lens, workspace);
     const Cache c = kernel_cache(cache);
     const Rows rows{static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride};
-    const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads, write ? 2 : 8);
+    const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads, write ? 4 : 8);
     const Scratch none{};
     if (write) {
         if (cache->head_dim == 128) write_kernel<128><<<grid, kThreads, 0, stream>>>(a, c, rows);
