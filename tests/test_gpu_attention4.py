@@ -315,3 +315,82 @@ def test_far_places(bd):
     out = bd.attn4_decode(q, cache, lens, ws, slots=i32([slots - 1]))
     want, bound = ref.attention(q, cache[-1:], lens)
     attention_ref.assert_close(out, want, bound)
+
+
+def test_requests_that_share_a_slot(bd):
+    """Several requests may read one slot (at lengths of their own), in each kind of call."""
+    g, hq, hk, d = gen(27), 16, 2, 128
+    cache = make_cache(2, 208, hk, d, g)
+    lens, slots = i32([200, 77, 200, 3, 131]), i32([1, 1, 1, 0, 1])
+    ws = bd.attn4_workspace(10, 5, hq, hk, d, longest=208, device=DEV)
+    q = queries(5, hq, d, g)
+    want, bound = ref.attention(q, cache, lens, slots=slots)
+    attention_ref.assert_close(bd.attn4_decode(q, cache, lens, ws, slots=slots), want, bound)
+    q, cu = queries(10, hq, d, g), i32([0, 2, 4, 7, 8, 10])
+    want, bound = ref.attention(q, cache, lens, slots=slots, cu_q=cu)
+    attention_ref.assert_close(bd.attn4_prefill(q, cache, cu, lens, ws, 208, slots=slots), want, bound)
+    k, v = ref.held(cache)
+    a, b = bd.cache4_read(*torch.zeros(2, 10, hk, d, dtype=torch.bfloat16, device=DEV), cache, lens, ws, slots=slots, cu_q=cu)
+    for i in range(5):
+        r, n, s = slice(int(cu[i]), int(cu[i + 1])), int(lens[i]), int(slots[i])
+        assert torch.equal(a[r].double(), k[s, n - (r.stop - r.start):n]) and torch.equal(b[r].double(), v[s, n - (r.stop - r.start):n])
+    assert bd.device_status(ws) == 0
+
+
+def test_two_streams_at_once(bd):
+    """Calls on two streams with a workspace and a cache each, many of them under way together."""
+    g, hq, hk, d, sides = gen(28), 32, 4, 128, []
+    for n in (3, 5):
+        cache, lens = make_cache(n, 2048, hk, d, g), torch.randint(1, 2049, (n,), generator=g, device=DEV, dtype=torch.int32)
+        lens[0] = 2048
+        news = [30 + 7 * i for i in range(n)]
+        lens = torch.maximum(lens, i32(news))
+        cu = i32([sum(news[:i]) for i in range(n + 1)])
+        q, q2 = queries(n, hq, d, g), queries(sum(news), hq, d, g)
+        ws = bd.attn4_workspace(sum(news), n, hq, hk, d, longest=2048, device=DEV)
+        want = ref.attention(q, cache, lens), ref.attention(q2, cache, lens, cu_q=cu)
+        sides.append((torch.cuda.Stream(), cache, lens, cu, q, q2, ws, want, torch.empty_like(q), torch.empty_like(q2)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, cache, lens, cu, q, q2, ws, _, out, out2 in sides:
+            with torch.cuda.stream(stream):
+                bd.attn4_decode(q, cache, lens, ws, out=out)
+                bd.attn4_prefill(q2, cache, cu, lens, ws, 2048, out=out2)
+    torch.cuda.synchronize()
+    for _, _, _, _, _, _, ws, want, out, out2 in sides:
+        for got, (x, bound) in zip((out, out2), want):
+            attention_ref.assert_close(got, x, bound)
+        assert bd.device_status(ws) == 0
+
+
+def test_prompts_longer_than_the_plan_keeps(bd):
+    """More requests than the reading back and the plan keep on chip, most of one token."""
+    g, hq, hk, d, n = gen(29), 8, 2, 64, 600
+    cache = make_cache(n, 64, hk, d, g)
+    news = [1 + (i % 37 == 5) * 9 for i in range(n)]
+    lens = torch.randint(10, 65, (n,), generator=g, device=DEV, dtype=torch.int32)
+    cu = torch.tensor([0] + news, device=DEV).cumsum(0).to(torch.int32)
+    slots = torch.randperm(n, generator=g, device=DEV).to(torch.int32)
+    q = queries(sum(news), hq, d, g)
+    ref.hide_unseen(cache, lens, rows=news, slots=slots, window=17, sinks=2)
+    ws = bd.attn4_workspace(sum(news), n, hq, hk, d, longest=64, device=DEV)
+    out = bd.attn4_prefill(q, cache, cu, lens, ws, 64, slots=slots, window=17, sinks=2)
+    want, bound = ref.attention(q, cache, lens, cu_q=cu, slots=slots, window=17, sinks=2)
+    attention_ref.assert_close(out, want, bound)
+    assert bd.device_status(ws) == 0
+
+
+def test_flat_scores_over_long_requests(bd):
+    """Every key weighs the same, and the result is a small mean of many values."""
+    g, hq, hk, d, n = gen(30), 8, 1, 128, 40000
+    cache = make_cache(2, n, hk, d, g)
+    q = torch.zeros(2, hq, d, dtype=torch.bfloat16, device=DEV)
+    lens = i32([n, n - 7])
+    ws = bd.attn4_workspace(2, 2, hq, hk, d, device=DEV)
+    out = bd.attn4_decode(q, cache, lens, ws).double()
+    v = ref.held(cache)[1]
+    want = torch.stack([v[i, :m].mean(0) for i, m in enumerate(lens.tolist())]).expand(2, hq, d)
+    # all probabilities are the same power of two: f32 sums of them times exact values, the terms' sizes
+    # added up times 2^-23 for each of at most n / 16 steps and joins, and one rounding of the result
+    size = torch.stack([v[i, :m].abs().mean(0) for i, m in enumerate(lens.tolist())]).expand(2, hq, d)
+    assert ((out - want).abs() <= want.abs() * 2.0 ** -8 + size * (n / 16 + 64) * 2.0 ** -23).all()
