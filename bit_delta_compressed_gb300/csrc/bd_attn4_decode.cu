@@ -39,10 +39,14 @@ constexpr float kLift = 6.f;
 
 // Where the visible keys of a request lie: tiles from the first key on (`head` of them)
 // and, behind a gap, those from tile `from` on.
+// Measured on both sides: kUnitCost 1 / 2 / 4 on 128 windowed requests 96.8 / 94.1 / 96.3 us; kLeast 8 / 16 / 32 on one
+// request of 4000 keys 12.7 / 15.5 / 16.8; kShort 12 / 30 / 64 on 4 requests of 600 to 1200 keys 13.7 / 11.4 / 11.4, on 8
+// of 500 to 3000 15.3 / 15.2 / 17.9; kJoin 2 / 4 / 8 on 2 requests of 4000 to 8000 keys with 32
+// query heads on 2 17.3 / 22.3 / 23.1 (more instructions, fetched for this alone), 1 and 2 alike.
 template <int BLOCKS>
 struct Keys4 {
     static constexpr int kTile = BLOCKS * kBlock;                           // keys of a tile
-    static constexpr int kUnitCost = 2, kLeast = 8, kShort = 30;
+    static constexpr int kUnitCost = 2, kLeast = 8, kShort = 30, kJoin = 2;
     int len, lo, sinks, head, from, n;
     static __device__ __forceinline__ Keys4 of(const Args& a, const Request& r) {
         Keys4 k;
@@ -65,7 +69,7 @@ struct Keys4 {
 template <int D, int R>
 struct Shape4 {
     static constexpr int kWarps = R == 8 ? 12 : 8;
-    static constexpr int kBlocks = R == 8 ? 3 : 2;                          // cache blocks of a tile
+    static constexpr int kBlocks = 3;                          // cache blocks of a tile
     static constexpr int kStage = kBlocks * Layout<D>::kBytes;
     static constexpr int kStages = 2 * (128 / D);
     static constexpr int kRing = kStage * kStages;                          // of one warp

@@ -62,7 +62,7 @@ struct Shape {
 // 16.8; kLeast 16 / 64 on the latter 17.4 / 18.3; a block for each short unit, with /
 // without, one request of 300 keys 7.8 / 10.3 us, 16 of 200 to 900 12.5 / 15.6.
 struct Keys {
-    static constexpr int kUnitCost = 3, kLeast = 16, kShort = 64;
+    static constexpr int kUnitCost = 3, kLeast = 16, kShort = 64, kJoin = 4;
     int n, head, gap;
     static __device__ __forceinline__ Keys of(const Args& a, const Request& r) {
         Keys k;

@@ -9,6 +9,7 @@
 //   kUnitCost   places of a unit besides its tiles
 //   kLeast      places of a block
 //   kShort      tiles up to which a unit may have a block of its own
+//   kJoin       parts of a unit whose loads are under way together when they are joined
 #pragma once
 
 #include "bd_attn_math.cuh"
@@ -199,22 +200,22 @@ __device__ __forceinline__ void note_open(LineBlock<W>& sh, const Line<Keys>& li
 }
 
 // Joins parts 0 .. count - 1 of one unit for one (row, four values): part(s)
-// gives a part's base, O [R][D] then (m, l) [R].  Four at a time, so that their
+// gives a part's base, O [R][D] then (m, l) [R].  N at a time, so that their
 // loads are under way together.
-template <int D, int R, typename F>
+template <int D, int R, int N, typename F>
 __device__ __forceinline__ void join(int row, int col, int count, F part, float& m, float& l, float4& o) {
-    for (int s0 = 0; s0 < count; s0 += 4) {
-        float2 ml[4];
-        float4 v[4];
+    for (int s0 = 0; s0 < count; s0 += N) {
+        float2 ml[N];
+        float4 v[N];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < N; ++s) {
             const float* p = part(min(s0 + s, count - 1));
             ml[s] = *reinterpret_cast<const float2*>(p + R * D + 2 * row);
             v[s] = *reinterpret_cast<const float4*>(p + row * D + col);
         }
         float top = m;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < N; ++s) {
             if (s0 + s >= count) ml[s] = make_float2(-INFINITY, 0.f);
             top = fmaxf(top, ml[s].x);
         }
@@ -223,7 +224,7 @@ __device__ __forceinline__ void join(int row, int col, int count, F part, float&
         l *= f;
         o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < N; ++s) {
             if (s0 + s >= count) break;
             f = exp2_approx(ml[s].x - use);
             l += f * ml[s].y;
@@ -275,7 +276,7 @@ __device__ __forceinline__ void join_open(const Args& a, const DecodeBuffers& bu
             const int r = i / (D / 4), col = (i % (D / 4)) * 4;
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            join<D, R>(r, col, next - first, [&](int j) { return local(sh.chain[first + j]); }, m, l, o);
+            join<D, R, Keys::kJoin>(r, col, next - first, [&](int j) { return local(sh.chain[first + j]); }, m, l, o);
             if (before || after) {
                 float* part = buf.parts + (int64_t)(2 * blockIdx.x + (before ? 0 : 1)) * (R * D + 2 * R);
                 *reinterpret_cast<float4*>(part + r * D + col) = o;
@@ -302,7 +303,7 @@ __device__ __forceinline__ void join_open(const Args& a, const DecodeBuffers& bu
                     const int r = i / (D / 4), col = (i % (D / 4)) * 4;
                     float m = -INFINITY, l = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    join<D, R>(r, col, c1 - c0 + 1,
+                    join<D, R, Keys::kJoin>(r, col, c1 - c0 + 1,
                                [&](int s) { return buf.parts + (int64_t)(2 * (c0 + s) + (s ? 0 : 1)) * (R * D + 2 * R); }, m, l, o);
                     if (g0 + r < a.G) finish<D>(a, buf, rec.b, hk, g0 + r, col, m, l, o);
                 }
