@@ -21,6 +21,7 @@ struct Args {
     int64_t ss, st, sh;                 // cache strides: slot, token, head
     int32_t n_slots, capacity;
     int32_t T, B, Hq, Hk, G;            // query rows, requests, heads, heads of a group
+    int32_t R;                          // where each row stands as a request of its own (B = T): the requests
     const int32_t *slots, *lens, *cu_q; // cu_q NULL: one row a request
     const int32_t *prefix_ids, *prefix_slots, *prefix_lens;
     int32_t P;

@@ -11,10 +11,19 @@
 // keys and dims are the 16 rows and a group's heads the 8 columns, so a group of 8 wastes nothing.  Which
 // dims meet in a product's step is free, so the cache's words are laid out for the
 // lanes: 16 bytes a lane are its part of a key, and a word is two steps' operand after
-// nine operations (bd_cache4.cuh).  Numbers times scales are exact in f16; only the
-// query (16-bit already, brought to f16's range by a power of two of its own) and the
-// probabilities (11 significant bits) are rounded, both below the result's bf16.
+// nine operations (bd_cache4.cuh).  Numbers times scales are exact in f16, and so is a
+// query, which a power of two of its own brings to f16's range (but values below 2^-27 of
+// its largest one); the probabilities are rounded to 11 significant bits, less than the result to bf16.
 // P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
+// What bounds it: those nine operations a word, logical ones and f16 fmas, each issued in two
+// cycles and hardly beside one another.  4 requests of 90,001 to 131,072 keys (481 MB) 87 us = 5.5 TB/s, 82% of a copy's rate
+// (the bf16 cache's kernel 270 us); the same loads without the arithmetic take 77 us, the arithmetic without the loads
+// 82.  128 requests of 1 to 16,384 keys seeing 4 + 4096 of them 95 us; one of 300 keys 7 us.
+// Twelve warps with tiles of 48 keys: 8 with 64 take 89 us, 16 with 32 (no more fit) 89.  A tile whose keys are
+// all seen has a path of its own: one path with masks 91.  Bulk copies with barriers in place of cp.async: 93 (one path for both: 98).
+// Taking 8 s p and 8 s q off sums of q s, so that the fma reads two registers in place of three: 86 with what makes the sums exact
+// again, for a bound on the error that grows with q's 15 in place of n's 7: not taken.
+// Prompts of few rows come here too, each row with the keys up to its own (bd_attn4.cu).
 #include <math.h>
 
 #include <type_traits>
@@ -43,11 +52,36 @@ constexpr float kLift = 6.f;
 // request of 4000 keys 12.7 / 15.5 / 16.8; kShort 12 / 30 / 64 on 4 requests of 600 to 1200 keys 13.7 / 11.4 / 11.4, on 8
 // of 500 to 3000 15.3 / 15.2 / 17.9; kJoin 2 / 4 / 8 on 2 requests of 4000 to 8000 keys with 32
 // query heads on 2 17.3 / 22.3 / 23.1 (more instructions, fetched for this alone), 1 and 2 alike.
-template <int BLOCKS>
+// ROWS: the rows of a prompt call, each as a request of its own, with the keys up to its own; a row of no
+// request has length -1.
+template <int BLOCKS, bool ROWS>
 struct Keys4 {
     static constexpr int kTile = BLOCKS * kBlock;                           // keys of a tile
     static constexpr int kUnitCost = 2, kLeast = 8, kShort = 30, kJoin = 2;
     int len, lo, sinks, head, from, n;
+    static __device__ __forceinline__ Request read(const Args& a, int b) {
+        if constexpr (!ROWS) return read_request(a, b);
+        int mine = -1, broken = -1;                     // requests from the first whose offsets do not ascend on are not served
+#pragma unroll 4
+        for (int i = a.R - 1; i >= 0; --i) {
+            const int lo = a.cu_q[i], hi = a.cu_q[i + 1];
+            mine = b >= lo && b < hi ? i : mine;
+            broken = lo < 0 || hi < lo || hi > a.T ? i : broken;
+        }
+        Request r{};
+        r.len = -1;
+        if (mine >= 0 && (broken < 0 || mine < broken)) {
+            const int hi = a.cu_q[mine + 1], slot = a.slots ? a.slots[mine] : mine, len = a.lens[mine];
+            const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[mine] && len <= a.capacity;
+            if (!ok) report(a.status, BD_ERR_SLOT);
+            r.slot = ok ? slot : 0;
+            r.len = ok ? len - (hi - 1 - b) : 0;
+        } else if (broken >= 0) {
+            report(a.status, BD_ERR_SLOT);
+            if (b >= a.cu_q[broken]) r.len = 0;         // zeros
+        }
+        return r;
+    }
     static __device__ __forceinline__ Keys4 of(const Args& a, const Request& r) {
         Keys4 k;
         k.len = r.len;
@@ -142,14 +176,14 @@ __device__ __forceinline__ void load_tile4(const uint8_t* unit, const Keys& k, i
     }
 }
 
-template <int D, int R>
+template <int D, int R, bool ROWS>
 __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     decode4_kernel(const Args a, const Cache cache, const DecodeBuffers buf) {
     using S = Shape4<D, R>;
     using Lay = Layout<D>;
     constexpr int NT = R / 8;              // columns of eight heads
     constexpr int kBlocks = S::kBlocks;
-    using Keys = Keys4<kBlocks>;
+    using Keys = Keys4<kBlocks, ROWS>;
     constexpr int W = D / 32;              // words of a lane's part of a key, or of two values
     constexpr int MT = D / 16;             // sixteens of dims
     extern __shared__ __align__(128) uint8_t smem[];
@@ -367,7 +401,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
                         if (g == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(m[n][i], l[n][i]);
                     }
                 if (lane == 0) note_open(sh, line, c, open_start, open_end);
-            } else {
+            } else if (!ROWS || c.k.len >= 0) {            // (a row of no request is one tile, whole: it ends here)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -390,20 +424,27 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     });
 }
 
-template <int D, int R>
+template <int D, int R, bool ROWS>
 bd_status launch_shape4(const Args& a, const Cache& cache, const DecodeBuffers& buf, cudaStream_t stream) {
     using S = Shape4<D, R>;
-    const void* kernel = reinterpret_cast<const void*>(decode4_kernel<D, R>);
-    if (!set_smem_attr(kernel, S::kSmem, D == 128 ? (R == 8 ? 11 : 12) : (R == 8 ? 13 : 14))) return BD_ERR_CUDA;
-    decode4_kernel<D, R><<<decode_blocks(), S::kWarps * 32, S::kSmem, stream>>>(a, cache, buf);
+    const void* kernel = reinterpret_cast<const void*>(decode4_kernel<D, R, ROWS>);
+    if (!set_smem_attr(kernel, S::kSmem, 11 + (D == 64) * 2 + (R == 16) + ROWS * 4)) return BD_ERR_CUDA;
+    decode4_kernel<D, R, ROWS><<<decode_blocks(), S::kWarps * 32, S::kSmem, stream>>>(a, cache, buf);
     return launch_status();
 }
 
 }  // namespace
 
+namespace {
+template <bool ROWS>
+bd_status launch_rows(const Args& a, const cache4::Cache& cache, int head_dim, const DecodeBuffers& buf, cudaStream_t stream) {
+    if (a.G <= 8) return head_dim == 128 ? launch_shape4<128, 8, ROWS>(a, cache, buf, stream) : launch_shape4<64, 8, ROWS>(a, cache, buf, stream);
+    return head_dim == 128 ? launch_shape4<128, 16, ROWS>(a, cache, buf, stream) : launch_shape4<64, 16, ROWS>(a, cache, buf, stream);
+}
+}  // namespace
+
 bd_status launch_decode4(const Args& a, const cache4::Cache& cache, int head_dim, const DecodeBuffers& buf, cudaStream_t stream) {
-    if (a.G <= 8) return head_dim == 128 ? launch_shape4<128, 8>(a, cache, buf, stream) : launch_shape4<64, 8>(a, cache, buf, stream);
-    return head_dim == 128 ? launch_shape4<128, 16>(a, cache, buf, stream) : launch_shape4<64, 16>(a, cache, buf, stream);
+    return a.cu_q ? launch_rows<true>(a, cache, head_dim, buf, stream) : launch_rows<false>(a, cache, head_dim, buf, stream);
 }
 
 }  // namespace attn

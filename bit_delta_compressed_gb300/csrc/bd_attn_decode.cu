@@ -64,6 +64,7 @@ struct Shape {
 struct Keys {
     static constexpr int kUnitCost = 3, kLeast = 16, kShort = 64, kJoin = 4;
     int n, head, gap;
+    static __device__ __forceinline__ Request read(const Args& a, int b) { return read_request(a, b); }
     static __device__ __forceinline__ Keys of(const Args& a, const Request& r) {
         Keys k;
         const int lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);

@@ -5,7 +5,8 @@
 // timing.
 //
 // `Keys` says which keys of a request a tile holds, and what a unit costs:
-//   static Keys of(const Args&, const Request&), int tiles() >= 1,
+//   static Request read(const Args&, int b), static Keys of(const Args&, const Request&),
+//   int tiles() >= 1,
 //   kUnitCost   places of a unit besides its tiles
 //   kLeast      places of a block
 //   kShort      tiles up to which a unit may have a block of its own
@@ -70,7 +71,7 @@ __device__ __forceinline__ void load_request(const Args& a, const Kept* kept, Cu
         c.r.len = kept[c.b].len;
         c.r.plen = kept[c.b].plen;
     } else {
-        c.r = read_request(a, c.b);
+        c.r = Keys::read(a, c.b);
     }
     c.k = Keys::of(a, c.r);
     c.tiles = c.k.tiles();
@@ -115,7 +116,7 @@ __device__ __forceinline__ Line<Keys> lay_line(const Args& a, LineBlock<W>& s, i
         int64_t mine = 0;
         int most = 0;
         for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) {
-            const Request r = read_request(a, b);
+            const Request r = Keys::read(a, b);
             if (b < kKept) s.kept[b] = Kept{r.slot, r.len, r.plen};
             const int n = Keys::of(a, r).tiles();
             mine += Keys::kUnitCost + n;

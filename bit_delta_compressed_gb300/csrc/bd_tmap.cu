@@ -9,7 +9,7 @@ namespace bd {
 namespace {
 std::mutex g_tc_mutex;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-int g_smem_set[64][16] = {};
+int g_smem_set[64][20] = {};
 
 bool encoder() {
     std::lock_guard<std::mutex> lock(g_tc_mutex);

@@ -118,11 +118,16 @@ def attention(q, cache, lens, **how):
     Decode multiplies probabilities rounded to f16, in the sum that divides as in the product, so the
     result is off by 2 x 2^-11 of the sum of |p v| for them; that sum is at most `bound` / 2^-8 of the bf16 cache's
     bound, which counts one bf16 rounding of it.  Probabilities below 2^-14 lose bits, 2^-25 each at most
-    where the largest one is 2^6 or more: 2^-31 of it, and so of the sum, for each key."""
+    where the largest one is 2^6 or more: 2^-31 of it, and so of the sum, for each key.
+
+    A prompt call of few rows is served by the same arithmetic, row by row: 2 x 2^-11 is less than the bf16 rounding of
+    the probabilities that its bound counts, and the last term is added."""
     k, v = held(cache)
     out, bound, _ = attention_ref.attention(q, k, v, lens, **how)
+    keys = lens.double()[:, None, None]
     if how.get("cu_q") is None:
-        largest = torch.nan_to_num(v.abs(), nan=0.0).amax() if v.numel() else 0.0
         bound = bound * (1 + 2 * 2.0 ** -11 * (1 + 2.0 ** -11) / attention_ref.BF16)
-        bound = bound + lens.double()[:, None, None] * 2.0 ** -31 * largest
-    return out, bound
+    else:
+        keys = lens.max() if lens.numel() else 0
+    largest = torch.nan_to_num(v.abs(), nan=0.0).amax() if v.numel() else 0.0
+    return out, bound + keys * 2.0 ** -31 * largest

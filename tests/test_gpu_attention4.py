@@ -394,3 +394,114 @@ def test_flat_scores_over_long_requests(bd):
     # added up times 2^-23 for each of at most n / 16 steps and joins, and one rounding of the result
     size = torch.stack([v[i, :m].abs().mean(0) for i, m in enumerate(lens.tolist())]).expand(2, hq, d)
     assert ((out - want).abs() <= want.abs() * 2.0 ** -8 + size * (n / 16 + 64) * 2.0 ** -23).all()
+
+
+FEW = [  # (tokens before, new tokens) of each request: few enough to be served row by row
+    [(0, 1)], [(300, 8)], [(0, 0), (5, 1), (100, 3), (0, 4), (300, 2)], [(47, 2), (15, 1), (500, 7), (0, 2)], [(31, 1)] * 64, [(95, 4)] * 20,
+]
+
+
+@pytest.mark.parametrize("heads", HEADS, ids=str)
+@pytest.mark.parametrize("mask", MASKS, ids=str)
+def test_few_rows(bd, heads, mask):
+    (hq, hk, d), (window, sinks) = heads, mask
+    for case, requests in enumerate(FEW):
+        before, counts = zip(*requests)
+        g, n, T = gen(hq + window + case), len(counts), sum(counts)
+        cache = make_cache(n + 1, 512, hk, d, g)
+        slots = torch.randperm(n + 1, generator=g, device=DEV)[:n].to(torch.int32)
+        lens, cu = i32([a + b for a, b in zip(before, counts)]), i32([sum(counts[:i]) for i in range(n + 1)])
+        ref.hide_unseen(cache, lens, rows=counts, slots=slots, window=window, sinks=sinks)
+        q, longest = queries(T, hq, d, g), int(lens.max())
+        ws = bd.attn4_workspace(T, n, hq, hk, d, longest=longest, device=DEV)
+        out = torch.full_like(q, math.nan)
+        bd.attn4_prefill(q, cache, cu, lens, ws, longest, slots=slots, window=window, sinks=sinks, out=out)
+        assert bd.device_status(ws) == 0
+        # row by row it is decode: its bound, on the keys up to the row
+        rows = [(b, i) for b, c in enumerate(counts) for i in range(c)]
+        at = i32([before[b] + i + 1 for b, i in rows])
+        want, bound = ref.attention(q, cache, at, slots=slots[[b for b, _ in rows]], window=window, sinks=sinks)
+        attention_ref.assert_close(out, want, bound, str(case))
+        again = bd.attn4_prefill(q, cache, cu, lens, ws, longest, slots=slots, window=window, sinks=sinks)
+        assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("rows", [2, 40], ids=["row by row", "tiles"])
+@pytest.mark.parametrize("lens,slots,served", [([50, 97, 49], [0, 1, 2], [1, 0, 1]), ([60, -1, 49], [0, 1, 2], [1, 0, 1]), ([60, 1, 49], [0, 1, 2], [1, 0, 1]),
+                                               ([60, 45, 49], [0, -1, 2], [1, 0, 1]), ([60, 45, 49], [0, 3, 2], [1, 0, 1]),
+                                               ([60, 45, 2 ** 31 - 1], [0, 1, -2 ** 31], [1, 1, 0])], ids=str)
+def test_prompts_out_of_range(bd, rows, lens, slots, served):
+    g, hq, hk, d = gen(31), 8, 2, 128
+    cache = make_cache(3, 96, hk, d, g)
+    ws = bd.attn4_workspace(3 * rows, 3, hq, hk, d, longest=96, device=DEV)
+    q = queries(3 * rows + 2, hq, d, g)[1:-1]
+    whole = torch.full((3 * rows + 2, hq, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = bd.attn4_prefill(q, cache, i32([0, rows, 2 * rows, 3 * rows]), i32(lens), ws, 96, slots=i32(slots), out=whole[1:-1])
+    assert bd.device_status(ws) == bd.BD_ERR_SLOT and (whole[0] == 7).all() and (whole[-1] == 7).all()
+    for b in range(3):
+        mine = slice(rows * b, rows * b + rows)
+        if served[b]:
+            how = dict(slots=[slots[b]] * rows) if rows == 2 else dict(slots=[slots[b]], cu_q=[0, rows])
+            at = i32([lens[b] - rows + 1 + i for i in range(rows)] if rows == 2 else [lens[b]])
+            want, bound = ref.attention(q[mine], cache, at, **how)
+            attention_ref.assert_close(out[mine], want, bound)
+        else:
+            assert (out[mine] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [2, 40], ids=["row by row", "tiles"])
+@pytest.mark.parametrize("cu,served,zeros", [([0, 2, 1, 3], [1, 0, 0], 2), ([0, 1, 2, 4], [1, 1, 0], 2), ([-1, 1, 2, 3], [0, 0, 0], 0), ([0, 0, -1, 3], [1, 0, 0], 0),
+                                             ([1, 1, 2, 3], [1, 1, 1], 3), ([0, 1, 1, 2], [1, 1, 1], 3), ([0, 2 ** 30, 2, 3], [0, 0, 0], 0)], ids=str)
+def test_offsets_of_prompts(bd, rows, cu, served, zeros):
+    """Offsets (in `rows`): rows behind ones that do not ascend become zeros, rows of no request stay."""
+    g, hq, hk, d = gen(32), 8, 2, 64
+    cache, lens = make_cache(3, 128, hk, d, g), [100, 120, 90]
+    cu = [x * rows if x != 2 ** 30 else x for x in cu]
+    T = 3 * rows
+    ws = bd.attn4_workspace(T, 3, hq, hk, d, longest=128, device=DEV)
+    q = queries(T, hq, d, g)
+    out = torch.full_like(q, 7.0)
+    bd.attn4_prefill(q, cache, i32(cu), i32(lens), ws, 128, out=out)
+    assert bd.device_status(ws) == (0 if all(served) else bd.BD_ERR_SLOT)
+    put = torch.zeros(T, dtype=torch.bool, device=DEV)
+    for b in range(3):
+        n = cu[b + 1] - cu[b]
+        if not served[b] or n == 0:
+            continue
+        mine = slice(cu[b], cu[b + 1])
+        put[mine] = True
+        want, bound = ref.attention(q[mine], cache, i32([lens[b]]), slots=[b], cu_q=[0, n])
+        if rows == 2:
+            want, bound = ref.attention(q[mine], cache, i32([lens[b] - n + 1 + i for i in range(n)]), slots=[b] * n)
+        attention_ref.assert_close(out[mine], want, bound)
+    behind = torch.arange(T, device=DEV) >= zeros * rows
+    if not all(served):
+        assert (out[behind] == 0).all()
+        put |= behind
+    assert (out[~put] == 7).all()
+
+
+def test_few_rows_in_a_graph(bd):
+    """A captured call of few rows whose offsets, lengths and slots change between replays."""
+    g, hq, hk, d, n = gen(33), 16, 2, 128, 4
+    cache = make_cache(6, 208, hk, d, g)
+    q = queries(12, hq, d, g)
+    cu, lens, slots = i32([0, 3, 6, 9, 12]), i32([50, 60, 70, 80]), i32([0, 1, 2, 3])
+    ws = bd.attn4_workspace(12, n, hq, hk, d, longest=208, device=DEV)
+    out = torch.empty_like(q)
+    bd.attn4_prefill(q, cache, cu, lens, ws, 208, slots=slots, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bd.attn4_prefill(q, cache, cu, lens, ws, 208, slots=slots, out=out)
+    for ends, sizes, places in (([0, 1, 1, 8, 12], [208, 3, 7, 130], [5, 4, 3, 2]), ([0, 12, 12, 12, 12], [100, 1, 1, 1], [1, 0, 0, 0]), ([1, 2, 3, 4, 5], [1, 1, 16, 17], [2, 2, 2, 2])):
+        for t, x in ((cu, ends), (lens, sizes), (slots, places)):
+            t.copy_(i32(x))
+        out.fill_(7)
+        graph.replay()
+        rows = [(b, t) for b in range(n) for t in range(ends[b], ends[b + 1])]
+        which = [t for _, t in rows]
+        want, bound = ref.attention(q[which], cache, i32([sizes[b] - (ends[b + 1] - 1 - t) for b, t in rows]), slots=[places[b] for b, _ in rows])
+        attention_ref.assert_close(out[which], want, bound)
+        assert (out[[t for t in range(12) if t not in which]] == 7).all()
+    assert bd.device_status(ws) == 0
