@@ -12,7 +12,7 @@
 // dims meet in a product's step is free, so the cache's words are laid out for the
 // lanes: 16 bytes a lane are its part of a key, and a word is two steps' operand after
 // nine operations (bd_cache4.cuh).  Numbers times scales are exact in f16, and so is a
-// query, which a power of two of its own brings to f16's range (but values below 2^-27 of
+// query, which a power of two of its own brings to f16's range (but values below 2^-30 of
 // its largest one); the probabilities are rounded to 11 significant bits, less than the result to bf16.
 // P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
 // What bounds it: those nine operations a word, logical ones and f16 fmas, each issued in two
