@@ -291,12 +291,13 @@ __device__ __forceinline__ void join_open(const Args& a, const DecodeBuffers& bu
             const int c0 = (int)(rec.start / line.per), c1 = (int)((rec.start + rec.tiles - 1) / line.per);
             __syncthreads();
             if (tid == 0) {
-                __threadfence();
+                // the ticket releases this block's part (written before the barrier) and acquires the others'
                 unsigned* ticket = buf.tickets + c0 / 4;
-                const int at = 8 * (c0 % 4), n = atomicAdd(ticket, 1u << at) >> at & 255u;
-                sh.last_block = n == c1 - c0;
+                const int at = 8 * (c0 % 4);
+                unsigned before_it;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before_it) : "l"(ticket), "r"(1u << at) : "memory");
+                sh.last_block = (int)(before_it >> at & 255u) == c1 - c0;
                 if (sh.last_block) atomicAnd(ticket, ~(255u << at));
-                __threadfence();
             }
             __syncthreads();
             if (sh.last_block) {
