@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     const int chunks = (a.G + R - 1) / R;  // a group of more than 16 heads is read once a 16
     const int units = a.Hk * chunks;
 
+    grid_wait();
     const Line<Keys> line = lay_line<Keys>(a, sh, units);
     uint8_t* const ring = smem + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(ring);
@@ -429,8 +430,8 @@ bd_status launch_shape4(const Args& a, const Cache& cache, const DecodeBuffers& 
     using S = Shape4<D, R>;
     const void* kernel = reinterpret_cast<const void*>(decode4_kernel<D, R, ROWS>);
     if (!set_smem_attr(kernel, S::kSmem, 11 + (D == 64) * 2 + (R == 16) + ROWS * 4)) return BD_ERR_CUDA;
-    decode4_kernel<D, R, ROWS><<<decode_blocks(), S::kWarps * 32, S::kSmem, stream>>>(a, cache, buf);
-    return launch_status();
+    // (a launch that is set up while the kernel before it ends: 3 us less of calls that follow one another)
+    return launch_close(decode4_kernel<D, R, ROWS>, decode_blocks(), S::kWarps * 32, S::kSmem, stream, a, cache, buf);
 }
 
 }  // namespace

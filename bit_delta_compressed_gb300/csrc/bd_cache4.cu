@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(const Args a, const 
     __shared__ Items items;
     __shared__ __align__(4) uint8_t codes[kWarps][D];
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
+    attn::grid_wait();
     const int64_t total = lay_items<false>(a, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
         int64_t i = at / a.Hk;
@@ -346,6 +347,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
     if (SCRATCH) attn::grid_go_on();
     const Ones ones;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
+    if (!SCRATCH) attn::grid_wait();
     const int64_t total = lay_items<SCRATCH>(a, items) * a.Hk;
     for (int64_t at = (int64_t)blockIdx.x * kWarps + tid / 32; at < total; at += (int64_t)gridDim.x * kWarps) {
         int64_t i = at / a.Hk;
@@ -424,14 +426,11 @@ bd_status rows_call(bool write, void* k, int64_t k_stride, void* v, int64_t v_st
     const Rows rows{static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v), k_stride, v_stride};
     const unsigned grid = grid_for(T < T / kBlock + 2 * B ? T : T / kBlock + 2 * B, cache->kv_heads, write ? 4 : 8);
     const Scratch none{};
-    if (write) {
-        if (cache->head_dim == 128) write_kernel<128><<<grid, kThreads, 0, stream>>>(a, c, rows);
-        else write_kernel<64><<<grid, kThreads, 0, stream>>>(a, c, rows);
-    } else {
-        if (cache->head_dim == 128) read_kernel<128, false><<<grid, kThreads, 0, stream>>>(a, c, rows, none);
-        else read_kernel<64, false><<<grid, kThreads, 0, stream>>>(a, c, rows, none);
-    }
-    return launch_status();
+    if (write)
+        return cache->head_dim == 128 ? attn::launch_close(write_kernel<128>, grid, kThreads, 0, stream, a, c, rows)
+                                      : attn::launch_close(write_kernel<64>, grid, kThreads, 0, stream, a, c, rows);
+    return cache->head_dim == 128 ? attn::launch_close(read_kernel<128, false>, grid, kThreads, 0, stream, a, c, rows, none)
+                                  : attn::launch_close(read_kernel<64, false>, grid, kThreads, 0, stream, a, c, rows, none);
 }
 
 }  // namespace
