@@ -16,13 +16,15 @@
 // its largest one); the probabilities are rounded to 11 significant bits, less than the result to bf16.
 // P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
 // What bounds it: those nine operations a word, logical ones and f16 fmas, each issued in two
-// cycles and hardly beside one another.  4 requests of 90,001 to 131,072 keys (481 MB) 87 us = 5.5 TB/s, 82% of a copy's rate
-// (the bf16 cache's kernel 270 us); the same loads without the arithmetic take 77 us, the arithmetic without the loads
-// 82.  128 requests of 1 to 16,384 keys seeing 4 + 4096 of them 95 us; one of 300 keys 7 us.
-// Twelve warps with tiles of 48 keys: 8 with 64 take 89 us, 16 with 32 (no more fit) 89.  A tile whose keys are
-// all seen has a path of its own: one path with masks 91.  Bulk copies with barriers in place of cp.async: 93 (one path for both: 98).
-// Taking 8 s p and 8 s q off sums of q s, so that the fma reads two registers in place of three: 86 with what makes the sums exact
-// again, for a bound on the error that grows with q's 15 in place of n's 7: not taken.
+// cycles and hardly beside one another.  4 requests of 90,001 to 131,072 keys (481 MB) 85 us
+// = 5.7 TB/s, 84% of a copy's rate (the bf16 cache's kernel 265 us); 128 requests of 1 to
+// 16,384 keys seeing 4 + 4096 of them 93 us; one of 300 keys 6.8 us.
+// When the first of these took 87 us, the same loads without the arithmetic took 77 us and
+// the arithmetic without the loads 82.  Other forms of it, on the same case: 8 warps with tiles of 64 keys 89,
+// 16 with 32 (more do not fit) 89; one path with masks for all tiles, where those whose keys
+// are all seen have their own, 91; bulk copies with barriers in place of cp.async 93; sums of
+// q s, q = n + 8, that lose 8 s p and 8 s q at their end, so that the fma reads two registers and not three,
+// 86, for a bound on the error that grows with q's 15 in place of n's 7: not taken.
 // Prompts of few rows come here too, each row with the keys up to its own (bd_attn4.cu).
 #include <math.h>
 

@@ -7,8 +7,8 @@
 // word of V holds four dims of two tokens; the lanes of the two swap halves, so that
 // whole words are written wherever both tokens are.
 // Measured (8 heads of 128): 131,080 tokens of 16 requests written in 125 us and read in 116, 680 MB
-// each way = 5.4 and 5.9 TB/s, 81% and 87% of a copy's rate; prompts of 9,525 tokens 14 and 11.4 us (7.3 for the bytes),
-// one token 3.7 and 3.2, most of it lengths and slots, then rows, that wait for one another.  Writing is bound by its
+// each way = 5.4 and 5.9 TB/s, 81% and 87% of a copy's rate; prompts of 9,525 tokens 13.5 and 10.8 us (7.3 for the bytes),
+// one token 3.5 and 3.1, most of it lengths and slots, then rows, that wait for one another.  Writing is bound by its
 // instructions: without a path for whole halves of a block, which needs no predicates, it took 159.
 #include <math.h>
 
