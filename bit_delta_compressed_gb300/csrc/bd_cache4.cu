@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
     using Lay = Layout<D>;
     constexpr int L = D / 8, R = 32 / L, kSteps = kBlock / R;
     __shared__ Items items;
-    if (SCRATCH) attn::grid_go_on();
     const Ones ones;
     const int tid = threadIdx.x, lane = tid % 32, col = lane % L;
     if (!SCRATCH) attn::grid_wait();
@@ -397,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
                 make_uint4(__byte_perm(f0, f1, 0x5410), __byte_perm(f2, f3, 0x5410), __byte_perm(f0, f1, 0x7632), __byte_perm(f2, f3, 0x7632));
         }
     }
-    if (SCRATCH) attn::grid_wait();                // the plan, for those that wait for this
+    // the plan, for those that wait for this (they begin at its end: letting them in earlier took 4 us more of windowed prompts)
+    if (SCRATCH) attn::grid_wait();
 }
 
 // Thread blocks for at most `blocks` cache blocks, up to `each` a SM.
