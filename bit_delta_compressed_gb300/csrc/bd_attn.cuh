@@ -22,6 +22,7 @@ struct Args {
     int32_t n_slots, capacity;
     int32_t T, B, Hq, Hk, G;            // query rows, requests, heads, heads of a group
     int32_t R;                          // where each row stands as a request of its own (B = T): the requests
+    int32_t longest;                    // keys that a request with rows may have (0: as many as a slot holds)
     const int32_t *slots, *lens, *cu_q; // cu_q NULL: one row a request
     const int32_t *prefix_ids, *prefix_slots, *prefix_lens;
     int32_t P;
@@ -63,6 +64,8 @@ __device__ __forceinline__ Request read_request(const Args& a, int b) {
         r.row0 = min(max(lo, 0), a.T);
         r.rows = min(max(hi, r.row0), a.T) - r.row0;
         ok = ok && lo == r.row0 && hi == r.row0 + r.rows && r.len >= r.rows;
+        // (one without rows asks for nothing that could be too long)
+        ok = ok && (r.rows == 0 || a.longest == 0 || r.len <= a.longest);
     }
     if (!ok) {
         report(a.status, BD_ERR_SLOT);

@@ -79,16 +79,15 @@ bd_status attention4(const void* q, int64_t q_stride, int64_t T, int64_t B, int3
     const cache4::Cache cache = cache4::kernel_cache(c);
     const Workspace4 w = layout4(workspace, T, B, q_heads, c->kv_heads, c->head_dim, longest);
     if (!cu_q) return launch_decode4(a, cache, c->head_dim, w.w.decode, stream);
+    a.longest = longest < a.capacity ? (int32_t)longest : a.capacity;
     if (B <= kFewRequests && (T <= kFewRows || T <= 4 * B)) {
         a.R = a.B;
         a.B = a.T;
-        if (longest < a.capacity) a.capacity = (int32_t)longest;
         return launch_decode4(a, cache, c->head_dim, w.w.decode, stream);
     }
     // the plan (one block) and the reading beside it go by the cache's slots and lengths, the
     // tiles by the plan: request b's keys lie in slot b of what was read back
     a.stands_in = 1;
-    if (longest < a.capacity) a.capacity = (int32_t)longest;
     st = launch_plan(a, w.w.plan, stream);
     if (st != BD_OK) return st;
     st = cache4::launch_seen(a, cache, c->head_dim, w.k, w.v, w.length, stream);

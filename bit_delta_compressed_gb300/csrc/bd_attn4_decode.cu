@@ -74,7 +74,7 @@ struct Keys4 {
         r.len = -1;
         if (mine >= 0 && (broken < 0 || mine < broken)) {
             const int hi = a.cu_q[mine + 1], slot = a.slots ? a.slots[mine] : mine, len = a.lens[mine];
-            const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[mine] && len <= a.capacity;
+            const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[mine] && len <= a.longest;
             if (!ok) report(a.status, BD_ERR_SLOT);
             r.slot = ok ? slot : 0;
             r.len = ok ? len - (hi - 1 - b) : 0;

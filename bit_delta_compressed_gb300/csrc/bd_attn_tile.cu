@@ -1095,7 +1095,7 @@ int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
 // prefill of few units, if a unit can be longer than the parts' price at all.
 bool may_split(const Args& a) {
     if (!a.cu_q) return true;
-    const int source = (a.capacity + kKeys - 1) / kKeys + 1;
+    const int source = ((a.longest ? a.longest : a.capacity) + kKeys - 1) / kKeys + 1;
     return most_tiles(a.T, a.B, a.G) * a.Hk < split_below() && source * (a.prefix_ids ? 2 : 1) > kSplitPrice + 1;
 }
 

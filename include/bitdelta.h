@@ -449,8 +449,8 @@ size_t bitdelta_attn4_workspace(int64_t tokens, int64_t batch, int32_t q_heads, 
 
 /* bitdelta_attn_decode and bitdelta_attn_prefill (without prefixes and weights) on a 4-bit
  * cache: attention on the values that the cache stands for, with the same heads, mask,
- * requests, results, errors and workspace rules.  `longest` bounds the keys of every request: one
- * with more gets zero rows and sets BD_ERR_SLOT.
+ * requests, results, errors and workspace rules.  `longest` bounds the keys of every request that has
+ * rows: one with more gets zero rows and sets BD_ERR_SLOT.
  * Precision: f32 statistics and sums, the result rounded once to bf16; decode, and
  * prompts of few rows, multiply probabilities of 11 significant bits, other prompts ones
  * rounded to bf16.  Which of the two a prompt call takes follows from T and B alone.
