@@ -9,6 +9,7 @@
 #include <math.h>
 
 #include "bd_attn4.cuh"
+#include "bd_attn_line.cuh"
 #include "bd_cache4_host.cuh"
 
 namespace bd {
@@ -23,6 +24,7 @@ namespace {
 // of 64 in one request of 16,000 keys, the others on 300, take 147 us,
 // read back 89 (of 100,000 819 and 296).
 constexpr int kFewRows = 8, kFewRequests = 64;
+static_assert(kFewRows <= kKept && 4 * kFewRequests <= kKept, "a block keeps every row on chip");
 
 // The attention's workspace, and behind it the keys and values that prompts read back.
 struct Workspace4 {

@@ -48,42 +48,55 @@ using cache4::Scales;
 // least, and others keep f16's bits down to 2^-20 of it), and moves only once a probability exceeds 2^14.
 constexpr float kLift = 6.f;
 
+// Looks at every request of a prompt call, those without rows too, and reports what is wrong with them; the number of
+// requests before the first whose offsets do not ascend.  All threads of a block.
+__device__ __forceinline__ int served_requests(const Args& a, int& served) {
+    if (threadIdx.x == 0) served = a.R;
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.R; b += blockDim.x) {
+        const int lo = a.cu_q[b], hi = a.cu_q[b + 1];
+        if (lo < 0 || hi < lo || hi > a.T) atomicMin(&served, b);
+        read_request(a, b);
+    }
+    __syncthreads();
+    return served;
+}
+
+// A row of a prompt call as a request of its own, with the keys up to its own; a row of no request has length -1.  The
+// requests from `served` on are not served: rows from there on have no keys.
+__device__ __forceinline__ Request row_request(const Args& a, int served, int row) {
+    Request r{};
+    r.len = -1;
+    int n = 0;                                          // requests that begin at the row or before it
+    for (int end = served; n < end;) {
+        const int mid = (n + end) / 2;
+        if (a.cu_q[mid] <= row) n = mid + 1;
+        else end = mid;
+    }
+    if (n > 0 && row < a.cu_q[n]) {
+        const int b = n - 1, hi = a.cu_q[n], slot = a.slots ? a.slots[b] : b, len = a.lens[b];
+        const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[b] && len <= a.longest;
+        r.slot = ok ? slot : 0;
+        r.len = ok ? len - (hi - 1 - row) : 0;
+    } else if (served < a.R && row >= a.cu_q[served]) {
+        r.len = 0;                                      // zeros
+    }
+    return r;
+}
+
 // Where the visible keys of a request lie: tiles from the first key on (`head` of them)
 // and, behind a gap, those from tile `from` on.
 // Measured on both sides: kUnitCost 1 / 2 / 4 on 128 windowed requests 96.8 / 94.1 / 96.3 us; kLeast 8 / 16 / 32 on one
 // request of 4000 keys 12.7 / 15.5 / 16.8; kShort 12 / 30 / 64 on 4 requests of 600 to 1200 keys 13.7 / 11.4 / 11.4, on 8
 // of 500 to 3000 15.3 / 15.2 / 17.9; kJoin 2 / 4 / 8 on 2 requests of 4000 to 8000 keys with 32
 // query heads on 2 17.3 / 22.3 / 23.1 (more instructions, fetched for this alone), 1 and 2 alike.
-// ROWS: the rows of a prompt call, each as a request of its own, with the keys up to its own; a row of no
-// request has length -1.
+// ROWS: the requests are the rows of a prompt call.
 template <int BLOCKS, bool ROWS>
 struct Keys4 {
     static constexpr int kTile = BLOCKS * kBlock;                           // keys of a tile
     static constexpr int kUnitCost = 2, kLeast = 8, kShort = 30, kJoin = 2;
     int len, lo, sinks, head, from, n;
-    static __device__ __forceinline__ Request read(const Args& a, int b) {
-        if constexpr (!ROWS) return read_request(a, b);
-        int mine = -1, broken = -1;                     // requests from the first whose offsets do not ascend on are not served
-#pragma unroll 4
-        for (int i = a.R - 1; i >= 0; --i) {
-            const int lo = a.cu_q[i], hi = a.cu_q[i + 1];
-            mine = b >= lo && b < hi ? i : mine;
-            broken = lo < 0 || hi < lo || hi > a.T ? i : broken;
-        }
-        Request r{};
-        r.len = -1;
-        if (mine >= 0 && (broken < 0 || mine < broken)) {
-            const int hi = a.cu_q[mine + 1], slot = a.slots ? a.slots[mine] : mine, len = a.lens[mine];
-            const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[mine] && len <= a.longest;
-            if (!ok) report(a.status, BD_ERR_SLOT);
-            r.slot = ok ? slot : 0;
-            r.len = ok ? len - (hi - 1 - b) : 0;
-        } else if (broken >= 0) {
-            report(a.status, BD_ERR_SLOT);
-            if (b >= a.cu_q[broken]) r.len = 0;         // zeros
-        }
-        return r;
-    }
+    static constexpr bool kAllKept = ROWS;
     static __device__ __forceinline__ Keys4 of(const Args& a, const Request& r) {
         Keys4 k;
         k.len = r.len;
@@ -195,7 +208,15 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     const int units = a.Hk * chunks;
 
     grid_wait();
-    const Line<Keys> line = lay_line<Keys>(a, sh, units);
+    int served = a.B;
+    if constexpr (ROWS) {
+        __shared__ int least;
+        served = served_requests(a, least);
+    }
+    const Line<Keys> line = lay_line<Keys>(a, sh, units, [&](int b) {
+        if constexpr (ROWS) return row_request(a, served, b);
+        else return read_request(a, b);
+    });
     uint8_t* const ring = smem + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(ring);
     float* const head_part = reinterpret_cast<float*>(smem + S::kWarps * S::kRing + warp * S::kPart);

@@ -64,7 +64,7 @@ struct Shape {
 struct Keys {
     static constexpr int kUnitCost = 3, kLeast = 16, kShort = 64, kJoin = 4;
     int n, head, gap;
-    static __device__ __forceinline__ Request read(const Args& a, int b) { return read_request(a, b); }
+    static constexpr bool kAllKept = false;
     static __device__ __forceinline__ Keys of(const Args& a, const Request& r) {
         Keys k;
         const int lo = min(max(window_lo(a, r.plen + r.len - 1) - r.plen, 0), r.len);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     const int units = a.Hk * chunks;
 
     grid_go_on();
-    const Line<Keys> line = lay_line<Keys>(a, sh, units);
+    const Line<Keys> line = lay_line<Keys>(a, sh, units, [&](int b) { return read_request(a, b); });
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
     float* const head_part = reinterpret_cast<float*>(smem + kWarps * S::kRing + warp * S::kPart);

@@ -5,8 +5,9 @@
 // timing.
 //
 // `Keys` says which keys of a request a tile holds, and what a unit costs:
-//   static Request read(const Args&, int b), static Keys of(const Args&, const Request&),
+//   static Keys of(const Args&, const Request&),
 //   int tiles() >= 1,
+//   kAllKept    whether its calls have no more than kKept requests
 //   kUnitCost   places of a unit besides its tiles
 //   kLeast      places of a block
 //   kShort      tiles up to which a unit may have a block of its own
@@ -66,12 +67,12 @@ struct LineBlock {
 
 template <typename Keys>
 __device__ __forceinline__ void load_request(const Args& a, const Kept* kept, Cursor<Keys>& c) {
-    if (c.b < kKept) {
+    if (Keys::kAllKept || c.b < kKept) {
         c.r.slot = kept[c.b].slot;
         c.r.len = kept[c.b].len;
         c.r.plen = kept[c.b].plen;
-    } else {
-        c.r = Keys::read(a, c.b);
+    } else if constexpr (!Keys::kAllKept) {
+        c.r = read_request(a, c.b);
     }
     c.k = Keys::of(a, c.r);
     c.tiles = c.k.tiles();
@@ -105,9 +106,9 @@ __device__ __forceinline__ bool next_unit(const Args& a, const Kept* kept, const
     return seek(a, kept, line, c, units);
 }
 
-// Lays out the line and gives this warp its part of it; all threads of a block of W warps.
-template <typename Keys, int W>
-__device__ __forceinline__ Line<Keys> lay_line(const Args& a, LineBlock<W>& s, int units) {
+// Lays out the line of the requests that read(b) gives and hands this warp its part of it; all threads of a block of W warps.
+template <typename Keys, int W, typename F>
+__device__ __forceinline__ Line<Keys> lay_line(const Args& a, LineBlock<W>& s, int units, F read) {
     static_assert(W * 32 >= kRuns && 2 * W <= 32, "a thread for each run, a lane for each record");
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     // places of the requests before each of kRuns runs of requests
@@ -116,7 +117,7 @@ __device__ __forceinline__ Line<Keys> lay_line(const Args& a, LineBlock<W>& s, i
         int64_t mine = 0;
         int most = 0;
         for (int b = tid * run; tid < kRuns && b < min(a.B, (tid + 1) * run); ++b) {
-            const Request r = Keys::read(a, b);
+            const Request r = read(b);
             if (b < kKept) s.kept[b] = Kept{r.slot, r.len, r.plen};
             const int n = Keys::of(a, r).tiles();
             mine += Keys::kUnitCost + n;

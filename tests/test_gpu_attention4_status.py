@@ -1,5 +1,5 @@
 """GPU: what a prompt call on a 4-bit cache reports goes by its arguments, not by the kernels that
-serve it."""
+serve it: of requests without rows too, and of offsets behind the last row."""
 import pytest
 import torch
 
@@ -46,6 +46,34 @@ def test_a_long_request_without_rows(bd, rows):
     check(out, q, cache, slice(0, rows), 48, 0)
     check(out, q, cache, slice(rows, 2 * rows), 41, 2)
     assert bd.device_status(ws) == 0
+
+
+@ROWS
+@pytest.mark.parametrize("length,slot", [(CAP + 1, 1), (-1, 1), (2 ** 31 - 1, 1), (9, -1), (9, 3), (0, 2 ** 31 - 1)])
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_a_request_without_rows_that_is_out_of_range(bd, rows, length, slot, at):
+    cache, q, ws = make(bd, 61, rows)
+    cu, lens, slots = [0, rows, 2 * rows], [90, 77], [2, 0]
+    cu.insert(at, cu[at])
+    lens.insert(at, length)
+    slots.insert(at, slot)
+    out = torch.full_like(q, 7.0)
+    bd.attn4_prefill(q, cache, i32(cu), i32(lens), ws, CAP, slots=i32(slots), out=out)
+    check(out, q, cache, slice(0, rows), 90, 2)
+    check(out, q, cache, slice(rows, 2 * rows), 77, 0)
+    assert bd.device_status(ws) == bd.BD_ERR_SLOT
+
+
+@ROWS
+@pytest.mark.parametrize("behind", [(-1, 0), (0, -1), (1, 0), (0, 1), (-2 ** 31, 2 ** 31 - 1)], ids=str)
+def test_offsets_that_do_not_ascend_behind_the_last_row(bd, rows, behind):
+    """All rows are the first request's; the offsets behind it are no offsets."""
+    cache, q, ws = make(bd, 62, rows)
+    T = 2 * rows
+    cu = [0, T] + [T + x if abs(x) < 2 else x for x in behind]
+    out = bd.attn4_prefill(q, cache, i32(cu), i32([85, 20, 30]), ws, CAP)
+    check(out, q, cache, slice(0, T), 85, 0)
+    assert bd.device_status(ws) == bd.BD_ERR_SLOT
 
 
 @ROWS
