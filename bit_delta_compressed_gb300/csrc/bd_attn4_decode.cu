@@ -47,6 +47,9 @@ using cache4::Scales;
 // The running maximum is kept this many powers of two below the scores' (so the largest probability is 2^6 at
 // least, and others keep f16's bits down to 2^-20 of it), and moves only once a probability exceeds 2^14.
 constexpr float kLift = 6.f;
+// What it begins with: below any score's but -inf, so that one that is -inf weighs nothing even where no other has been
+// seen (with -inf in this place it would be a NaN).
+constexpr float kLowest = -3.402823466e38f;
 
 // Looks at every request of a prompt call, those without rows too, and reports what is wrong with them; the number of
 // requests before the first whose offsets do not ascend.  All threads of a block.
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
                 return __any_sync(0xffffffffu, over(top));
             };
             if (weigh()) {
-                // the maximum moves (from -inf, at first)
+                // the maximum moves (from the lowest, at first)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float f[2];
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
 #pragma unroll
                     for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
                     l[n][0] = l[n][1] = l[n][2] = l[n][3] = 0.f;
-                    m[n][0] = m[n][1] = -INFINITY;
+                    m[n][0] = m[n][1] = kLowest;
                 }
             }
 #pragma unroll 1
