@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(kThreads, 4) write_kernel(const Args a, const 
         const int lo = max(s.first - t0, 0), hi = min(s.len - t0, kBlock);      // tokens of the block
         const int64_t row0 = (int64_t)s.row0 - s.first + t0;
         const int row = lane / L;
-        const __nv_bfloat16 *k_from = rows.k + (row0 + row) * rows.k_stride + h * D + col * 8, *v_from = rows.v + (row0 + row) * rows.v_stride + h * D + col * 8;
+        // a row may hold 2^31 values and more (2^32 times eight of them, and a block of each of its heads, no GPU)
+        const unsigned eights = (unsigned)h * L + col;
+        const __nv_bfloat16* k_from = rows.k + (row0 + row) * rows.k_stride + (uint64_t)eights * 8;
+        const __nv_bfloat16* v_from = rows.v + (row0 + row) * rows.v_stride + (uint64_t)eights * 8;
         uint8_t* const k_to = to + row * (D / 2) + col * 4;
         uint8_t* const v_to = to + Lay::kV + row / 2 * D + col * 8;
         uint8_t* const code_to = codes[tid / 32] + (col % 4 ? 0 : row * (D / 32) + col / 4);
@@ -366,8 +369,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const Args a, const Cach
             k_next = v_next = D;
         } else {
             const int64_t row0 = (int64_t)s.row0 - s.first + t0;
-            k_to = rows.k + row0 * rows.k_stride + h * D;
-            v_to = rows.v + row0 * rows.v_stride + h * D;
+            k_to = rows.k + row0 * rows.k_stride + (uint64_t)(uint32_t)h * D;
+            v_to = rows.v + row0 * rows.v_stride + (uint64_t)(uint32_t)h * D;
             k_next = rows.k_stride;
             v_next = rows.v_stride;
         }
