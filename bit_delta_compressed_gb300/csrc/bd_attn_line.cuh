@@ -296,7 +296,7 @@ __device__ __forceinline__ void join_open(const Args& a, const DecodeBuffers& bu
                 unsigned* ticket = buf.tickets + c0 / 4;
                 const int at = 8 * (c0 % 4);
                 unsigned before_it;
-                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before_it) : "l"(ticket), "r"(1u << at) : "memory");
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before_it) : "l"(__cvta_generic_to_global(ticket)), "r"(1u << at) : "memory");
                 sh.last_block = (int)(before_it >> at & 255u) == c1 - c0;
                 if (sh.last_block) atomicAnd(ticket, ~(255u << at));
             }

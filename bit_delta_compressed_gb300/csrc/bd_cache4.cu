@@ -46,7 +46,7 @@ struct Span {
     int first, len, row0, head, from, n;
 };
 
-__device__ __forceinline__ Span rows_span(const Args& a, const Request& r) {
+__device__ __forceinline__ Span rows_span(const Request& r) {
     Span s;
     s.first = r.len - r.rows;
     s.len = r.len;
@@ -92,7 +92,7 @@ __device__ __forceinline__ bool span_of(const Args& a, int b, int served, Span& 
         report(a.status, BD_ERR_SLOT);
         return false;
     }
-    s = SCRATCH ? seen_span(a, r) : rows_span(a, r);
+    s = SCRATCH ? seen_span(a, r) : rows_span(r);
     return true;
 }
 
