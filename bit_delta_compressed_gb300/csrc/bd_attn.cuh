@@ -23,6 +23,7 @@ struct Args {
     int32_t T, B, Hq, Hk, G;            // query rows, requests, heads, heads of a group
     int32_t R;                          // where each row stands as a request of its own (B = T): the requests
     int32_t longest;                    // keys that a request with rows may have (0: as many as a slot holds)
+    int32_t few;                        // where two kernels share a prompt call: rows of a request up to which the one takes it
     const int32_t *slots, *lens, *cu_q; // cu_q NULL: one row a request
     const int32_t *prefix_ids, *prefix_slots, *prefix_lens;
     int32_t P;
@@ -72,6 +73,7 @@ __device__ __forceinline__ Request read_request(const Args& a, int b) {
         r.slot = r.pslot = 0;
         r.len = r.plen = 0;
     }
+    if (a.few && r.rows <= a.few) r.rows = 0;
     if (a.stands_in) r.slot = b;
     return r;
 }

@@ -16,15 +16,21 @@ namespace bd {
 namespace attn {
 namespace {
 
-// A prompt call of up to kFewRows rows, or four for each of up to kFewRequests requests, goes through the
-// decode kernel, each row as a request of its own: its keys are then read, as they lie, once for every row, and not read back.
-// Measured, row by row / read back (64 query heads on 8 of 128): one request's 8 rows on 300 keys 8.2 / 17.3 us, on 16,000
-// 34 / 49, on 100,000 148 / 186; 16 rows 8.5 / 17.4, 56 / 51, 278 / 187.  Four rows of each of 16 requests of 300, 4000 and
-// 16,000 keys 18 / 21, 60 / 120, 186 / 400; of 64 of 4000 keys 195 / 422.  The host does not see how the rows lie: 49
-// of 64 in one request of 16,000 keys, the others on 300, take 147 us,
-// read back 89 (of 100,000 819 and 296).
-constexpr int kFewRows = 8, kFewRequests = 64;
-static_assert(kFewRows <= kKept && 4 * kFewRequests <= kKept, "a block keeps every row on chip");
+// A prompt call of up to kFewRows rows, or four for each request, goes through the decode kernel, each row as a request of its
+// own: its keys are then read, as they lie, once for every row, and not read back.  The host does not see how the rows lie, so
+// of a call of more than kFewInAll rows this is so for the requests that have up to kFewEach; the others' keys are read back for the
+// tiles, in launches of their own that find nothing where there are none.
+// Measured (64 query heads on 8 of 128), row by row / read back: one request's 8 rows on 300 keys 7.7 / 17.2 us, on 16,000 32 / 49, on
+// 100,000 142 / 186; 16 rows 8.5 / 17.4, 56 / 51, 270 / 187.  In a call that both kinds share, with 3 rows of each of 19
+// other requests of 500 keys, one request's 16 rows on 4000, 16,000 and 100,000 keys: by rows 38 / 67 / 284 us, by tiles 44 / 66 / 199; 10 rows 33 / 52 /
+// 188, 43 / 65 / 198; 20 rows by tiles 45 / 68 / 199, all by rows 32 / 72 / 348, all read back 52 / 78 / 220.
+// All by rows / shared / all read back: 4 rows of each of 16 requests of 300, 4000 and 16,000 keys 16 / 22 / 21 us, 57 / 64 / 118, 180 / 188 /
+// 401; one row of each of 64 of 300 keys 16 / 25 / 61, four of 4000 186 / 195 / 420; of 128 of 4000 keys one row - / 108 / 776,
+// four - / 370 / 778.  49 of 64 rows in one request of 16,000 keys, the others on 300, 143 / 76 / 83; 193 of 256 528 / 136 / 227, of
+// 100,000 keys 3163 / 555 / 1170.  Calls of up to kFewInAll: 4 rows of each of 8 requests of 300 and 4000 keys 13 / 20 / 19 and
+// 34 / 41 / 70; 25 of 32 in one request of 4000, 16,000 and 100,000 keys 28 / 37 / 37, 77 / 61 / 61, 415 / 190 / 203.
+constexpr int kFewRows = 8, kFewInAll = 32, kFewEach = 16;
+// (Of calls of more than kKept rows or requests, which a block of the decode kernel does not keep on chip, all are read back.)
 
 // The attention's workspace, and behind it the keys and values that prompts read back.
 struct Workspace4 {
@@ -82,10 +88,13 @@ bd_status attention4(const void* q, int64_t q_stride, int64_t T, int64_t B, int3
     const Workspace4 w = layout4(workspace, T, B, q_heads, c->kv_heads, c->head_dim, longest);
     if (!cu_q) return launch_decode4(a, cache, c->head_dim, w.w.decode, stream);
     a.longest = longest < a.capacity ? (int32_t)longest : a.capacity;
-    if (B <= kFewRequests && (T <= kFewRows || T <= 4 * B)) {
-        a.R = a.B;
-        a.B = a.T;
-        return launch_decode4(a, cache, c->head_dim, w.w.decode, stream);
+    if (T <= kKept && B <= kKept && (T <= kFewRows || T <= 4 * B)) {
+        if (T > kFewInAll) a.few = kFewEach;
+        Args rows = a;
+        rows.R = a.B;
+        rows.B = a.T;
+        st = launch_decode4(rows, cache, c->head_dim, w.w.decode, stream);
+        if (st != BD_OK || !a.few) return st;
     }
     // the plan (one block) and the reading beside it go by the cache's slots and lengths, the
     // tiles by the plan: request b's keys lie in slot b of what was read back

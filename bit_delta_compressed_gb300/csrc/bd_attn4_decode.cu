@@ -65,8 +65,8 @@ __device__ __forceinline__ int served_requests(const Args& a, int& served) {
     return served;
 }
 
-// A row of a prompt call as a request of its own, with the keys up to its own; a row of no request has length -1.  The
-// requests from `served` on are not served: rows from there on have no keys.
+// A row of a prompt call as a request of its own, with the keys up to its own; a row of no request, or of one that the
+// tiles take, has length -1.  The requests from `served` on are not served: rows from there on have no keys.
 __device__ __forceinline__ Request row_request(const Args& a, int served, int row) {
     Request r{};
     r.len = -1;
@@ -78,7 +78,9 @@ __device__ __forceinline__ Request row_request(const Args& a, int served, int ro
     }
     if (n > 0 && row < a.cu_q[n]) {
         const int b = n - 1, hi = a.cu_q[n], slot = a.slots ? a.slots[b] : b, len = a.lens[b];
-        const bool ok = slot >= 0 && slot < a.n_slots && len >= hi - a.cu_q[b] && len <= a.longest;
+        const int rows = hi - a.cu_q[b];
+        if (a.few && rows > a.few) return r;            // the tiles'
+        const bool ok = slot >= 0 && slot < a.n_slots && len >= rows && len <= a.longest;
         r.slot = ok ? slot : 0;
         r.len = ok ? len - (hi - 1 - row) : 0;
     } else if (served < a.R && row >= a.cu_q[served]) {
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     const int units = a.Hk * chunks;
 
     grid_wait();
+    if (ROWS && a.few) grid_go_on();       // the tiles' plan is laid out and their keys are read beside this
     int served = a.B;
     if constexpr (ROWS) {
         __shared__ int least;

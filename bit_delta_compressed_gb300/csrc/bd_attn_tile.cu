@@ -345,6 +345,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Args a, const 
         }
     }
     if (tid == 0) *plan.head = PlanHead{tiles, line * a.Hk, per, split, sorted};
+    // (the kernel before it has waited for all that this reads, and lets it begin beside itself)
+    if (a.few) grid_wait();
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
@@ -1091,17 +1093,25 @@ int64_t most_tiles(int64_t tokens, int64_t batch, int G) { return tokens / (kPar
 int tile_blocks() { return decode_blocks(); }
 int64_t split_below() { return 2 * (int64_t)tile_blocks(); }
 
+// Row tiles that this call can have at most.  (Of requests that have more than `few` rows there are fewer; one more may
+// end the rows that are served.)
+int64_t most_tiles(const Args& a) {
+    const int64_t most = a.few ? a.T / (a.few + 1) + 1 : a.B;
+    return most_tiles(a.T, most < a.B ? most : a.B, a.G);
+}
+
 // Whether a call's parts may be left in the workspace, which holds those of few rows: a
 // prefill of few units, if a unit can be longer than the parts' price at all.
 bool may_split(const Args& a) {
     if (!a.cu_q) return true;
     const int source = ((a.longest ? a.longest : a.capacity) + kKeys - 1) / kKeys + 1;
-    return most_tiles(a.T, a.B, a.G) * a.Hk < split_below() && source * (a.prefix_ids ? 2 : 1) > kSplitPrice + 1;
+    return most_tiles(a) * a.Hk < split_below() && source * (a.prefix_ids ? 2 : 1) > kSplitPrice + 1;
 }
 
 bd_status launch_plan(const Args& a, const TilePlan& plan, cudaStream_t stream) {
     const int counts = a.cu_q ? 0 : (a.P + 1) * (int)sizeof(int);
     if (!set_smem_attr(reinterpret_cast<const void*>(plan_kernel), (kMaxPrefixes + 1) * (int)sizeof(int), 10)) return BD_ERR_CUDA;
+    if (a.few) return launch_close(plan_kernel, 1, kPlanThreads, counts, stream, a, plan, tile_blocks(), (int)may_split(a));
     plan_kernel<<<1, kPlanThreads, counts, stream>>>(a, plan, tile_blocks(), may_split(a));
     return launch_status();
 }
@@ -1115,7 +1125,7 @@ bd_status launch_tiles(const Args& a, int head_dim, const TilePlan& plan, cudaSt
     const bd_status st = head_dim == 128 ? launch_kernel<128>(a, plan, stream) : launch_kernel<64>(a, plan, stream);
     if (st != BD_OK || !may_split(a)) return st;
     // (few units are joined by many blocks each)
-    const int64_t units = most_tiles(a.T, a.B, a.G) * a.Hk, each = 8 * (int64_t)tile_blocks() / units;
+    const int64_t units = most_tiles(a) * a.Hk, each = 8 * (int64_t)tile_blocks() / units;
     const dim3 grid((unsigned)units, (unsigned)(each < 4 ? 4 : each > 32 ? 32 : each));
     return head_dim == 128 ? launch_close(join_kernel<128>, grid, 256, 0, stream, a, plan)
                            : launch_close(join_kernel<64>, grid, 256, 0, stream, a, plan);

@@ -453,7 +453,7 @@ size_t bitdelta_attn4_workspace(int64_t tokens, int64_t batch, int32_t q_heads, 
  * rows: one with more gets zero rows and sets BD_ERR_SLOT.
  * Precision: f32 statistics and sums, the result rounded once to bf16; decode, and
  * prompts of few rows, multiply probabilities of 11 significant bits, other prompts ones
- * rounded to bf16.  Which of the two a prompt call takes follows from T and B alone.
+ * rounded to bf16.  Which of the two a request's rows take follows from T, B and their number alone.
  * A query that is not finite gives results that are not finite, but zeros where every visible
  * score is -inf. */
 bd_status bitdelta_attn4_decode(const void *q, int64_t q_stride, int64_t B, int32_t q_heads,
