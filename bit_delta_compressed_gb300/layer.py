@@ -83,9 +83,14 @@ class CachedAttention:
 
     With ``bits=4`` the keys and values are ``cache``, a 4-bit cache (see ``bd.cache4``; k and v are
     None), in 17/64 of the bytes; ``capacity`` is then a multiple of 16.  ``longest``: the most keys, new ones
-    included, of a request whose prompt is served (the capacity, unless given: prompts read
-    the keys they see back to bf16, and the workspace has room for `batch` requests of that many).  Shared
-    prefixes, weights and eviction are the bf16 cache's.
+    included, of a request whose prompt is served (the capacity, unless given).  Prompts read
+    the keys they see back to bf16, so the workspace has room for `batch` requests of that many, 4 * batch * kv_heads *
+    longest * head_dim bytes: for as many requests as slots, and the whole capacity, as much as a bf16 cache
+    takes.  Layers that run one after another need it once (``ws``).  Shared prefixes, weights and
+    eviction are the bf16 cache's.
+
+    ``ws``: the workspace of another layer's cache, to be shared with it (made for at least these sizes;
+    layers that share one run one after another, on one stream, and have one status word).
 
     A request whose slot is not there, or has no room for all its new tokens, is
     left as it is: nothing is appended, its rows come out as zeros, and the status
@@ -95,7 +100,7 @@ class CachedAttention:
 
     def __init__(self, bd, slots: int, capacity: int, q_heads: int, kv_heads: int, head_dim: int, tokens: int,
                  batch: int, window: int = 0, sinks: int = 0, weigh: bool = False, device="cuda", bits: int = 16,
-                 longest: int | None = None):
+                 longest: int | None = None, ws=None):
         import torch
         if bits not in (4, 16):
             raise ValueError("a cache holds 4 or 16 bits a value")
@@ -115,7 +120,7 @@ class CachedAttention:
             self._k = self._v = None
             self.longest = capacity if longest is None else min(longest, capacity)
             self.cache = bd.cache4(slots, capacity, kv_heads, head_dim, device)
-            self.ws = bd.attn4_workspace(tokens, batch, q_heads, kv_heads, head_dim, self.longest, device)
+            self.ws = self._workspace(ws, bd.attn4_workspace, tokens, batch, self.longest, device)
             return
         self.longest = capacity
         # Behind the cache's places lies one more key: what has no place of its own goes
@@ -129,8 +134,17 @@ class CachedAttention:
             self.slot_weights = torch.zeros(slots + 1, kv_heads, capacity, device=device)
             self._weights = self.slot_weights[:-1]
             self.zero = torch.zeros((), device=device)
-        self.ws = bd.attn_workspace(tokens, batch, q_heads, kv_heads, head_dim, capacity if weigh else 0, device)
+        self.ws = self._workspace(ws, bd.attn_workspace, tokens, batch, capacity if weigh else 0, device)
         self.evict_ws = bd.evict_workspace(batch, kv_heads, capacity, device)
+
+    def _workspace(self, given, make, tokens, batch, length, device):
+        """A workspace for these sizes: the one that was given, if it is large enough, or a new one."""
+        if given is None:
+            return make(tokens, batch, *self.heads, length, device)
+        need = make(tokens, batch, *self.heads, length, "meta").numel()
+        if given.numel() < need:
+            raise ValueError("the workspace must have at least %d bytes" % need)
+        return given
 
     def _slots(self, slots):
         """Places in ``slot_lens``: those of no slot (-1 and ``slots``) are the one behind."""
