@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(Shape4<D, R>::kWarps * 32, 1)
     }
     const Line<Keys> line = lay_line<Keys>(a, sh, units, [&](int b) {
         if constexpr (ROWS) return row_request(a, served, b);
-        else return read_request(a, b);
+        else return read_request<true>(a, b);
     });
     uint8_t* const ring = smem + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(ring);

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
     const int units = a.Hk * chunks;
 
     grid_go_on();
-    const Line<Keys> line = lay_line<Keys>(a, sh, units, [&](int b) { return read_request(a, b); });
+    const Line<Keys> line = lay_line<Keys>(a, sh, units, [&](int b) { return read_request<true>(a, b); });
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     float* const tail_part = reinterpret_cast<float*>(smem + warp * S::kRing);
     float* const head_part = reinterpret_cast<float*>(smem + kWarps * S::kRing + warp * S::kPart);
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a, const
 __global__ void __launch_bounds__(256) weigh_kernel(const Args a, const DecodeBuffers buf) {
     const int b = blockIdx.z, hk = blockIdx.y;
     grid_wait();
-    const Request r = read_request(a, b);
+    const Request r = read_request<true>(a, b);
     const Keys k = Keys::of(a, r);
     const int64_t row = (int64_t)b * a.Hq + (int64_t)hk * a.G;
     float* w = a.weights + ((int64_t)r.slot * a.Hk + hk) * a.capacity;

@@ -72,7 +72,7 @@ __device__ __forceinline__ void load_request(const Args& a, const Kept* kept, Cu
         c.r.len = kept[c.b].len;
         c.r.plen = kept[c.b].plen;
     } else if constexpr (!Keys::kAllKept) {
-        c.r = read_request(a, c.b);
+        c.r = read_request<true>(a, c.b);
     }
     c.k = Keys::of(a, c.r);
     c.tiles = c.k.tiles();
