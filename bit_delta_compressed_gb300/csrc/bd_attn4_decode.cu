@@ -17,7 +17,7 @@
 // P^T comes out of S^T's layout by one 8 x 8 transposition in registers.
 // What bounds it: those nine operations a word, logical ones and f16 fmas, each issued in two
 // cycles and hardly beside one another.  4 requests of 90,001 to 131,072 keys (481 MB) 85 us
-// = 5.7 TB/s, 84% of a copy's rate (the bf16 cache's kernel 265 us); 128 requests of 1 to
+// = 5.7 TB/s, 84% of a copy's rate (the bf16 cache's kernel 266 us); 128 requests of 1 to
 // 16,384 keys seeing 4 + 4096 of them 93 us; one of 300 keys 6.8 us.
 // When the first of these took 87 us, the same loads without the arithmetic took 77 us and
 // the arithmetic without the loads 82.  Other forms of it, on the same case: 8 warps with tiles of 64 keys 89,
@@ -25,7 +25,7 @@
 // are all seen have their own, 91; bulk copies with barriers in place of cp.async 93; sums of
 // q s, q = n + 8, that lose 8 s p and 8 s q at their end, so that the fma reads two registers and not three,
 // 86, for a bound on the error that grows with q's 15 in place of n's 7: not taken.
-// Prompts of few rows come here too, each row with the keys up to its own (bd_attn4.cu).
+// Requests of few rows of a prompt call come here too, each row with the keys up to its own (bd_attn4.cu).
 #include <math.h>
 
 #include <type_traits>

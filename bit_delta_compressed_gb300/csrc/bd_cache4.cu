@@ -6,9 +6,9 @@
 // group's largest value is two shuffles away and a lane's eight numbers are one word of K.  A
 // word of V holds four dims of two tokens; the lanes of the two swap halves, so that
 // whole words are written wherever both tokens are.
-// Measured (8 heads of 128): 131,080 tokens of 16 requests written in 125 us and read in 116, 680 MB
-// each way = 5.4 and 5.9 TB/s, 81% and 87% of a copy's rate; prompts of 9,525 tokens 13.5 and 10.8 us (7.3 for the bytes),
-// one token 3.5 and 3.1, most of it lengths and slots, then rows, that wait for one another.  Writing is bound by its
+// Measured (8 heads of 128): 131,080 tokens of 16 requests written in 125 us and read in 117, 680 MB
+// each way = 5.4 and 5.8 TB/s, 81% and 86% of a copy's rate; prompts of 9,525 tokens 13.6 and 10.9 us (7.3 for the bytes),
+// one token 3.6 and 3.2, most of it lengths and slots, then rows, that wait for one another.  Writing is bound by its
 // instructions: without a path for whole halves of a block, which needs no predicates, it took 159.
 #include <math.h>
 
@@ -143,7 +143,9 @@ __device__ __forceinline__ int64_t lay_items(const Args& a, Items& items) {
     return items.before[kThreads];
 }
 
-// The request that holds block i of all, which becomes the block's number within it, and its slot.
+// The request that holds block i of all, which becomes the block's number within it, and its slot.  (Of more requests than
+// threads a thread's run is walked again for every block: one token of each of 256, 512, 1024, 2048 and 8192 requests is
+// written in 4.3, 6.6, 11.5, 22 and 149 us.)
 template <bool SCRATCH>
 __device__ __forceinline__ int find(const Args& a, const Items& items, int64_t& i, Span& s, int& slot) {
     int t = 0;
